@@ -294,6 +294,119 @@ hyb_status_t hyb_linear_attn_chunked_prefill(void* out, const void* q, const voi
 size_t hyb_linear_attn_chunked_prefill_workspace_size(void);
 
 /* -------------------------------------------------------------------------
+ * Gated delta rule: the Linear layer of hybrid models whose state forgets and corrects
+ * itself. Per value head, with S the fp32 D x D state (rows: key dim, columns: value dim),
+ * q and k of query/key head h / (num_v_heads / num_qk_heads), g the log of the decay
+ * and beta the strength of the correction of this token and head:
+ *     S <- exp(g) S
+ *     S <- S + k (outer) beta (v - S^T k)
+ *     out = scale * S^T q
+ * With qk_norm_eps > 0, q and k are first divided by sqrt(sum of squares + qk_norm_eps);
+ * 0 takes them as they are (the rule is then stable only for beta |k|^2 < 2).
+ *
+ *   q, k        [T][num_qk_heads][D], v and out [T][num_v_heads][D], of d->dtype. Rows of q, k
+ *               and v may be parts of wider rows (a fused projection's): q_stride, k_stride and
+ *               v_stride are the elements from one token to the next, 0 for packed rows; a stride
+ *               covers at least the row and is a multiple of 16 bytes. out is packed.
+ *   g, beta     fp32 [T][num_v_heads] (4-byte aligned); g <= 0, -infinity clears the state. Below
+ *               -10 000 it counts as that (exp of either is 0 in fp32). g > 0 lets the state grow.
+ *   state pool  fp32 [num_slots][num_v_heads][D][D], as for hyb_linear_attn_step
+ * out must overlap none of the inputs. A NaN or infinity in one request's rows or state stays
+ * within that request; in the chunked call it also reaches the other rows of its chunk.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t num_qk_heads;        /* heads of q and k                                      */
+  int32_t num_v_heads;         /* heads of v, out, g, beta and the state; a multiple    */
+  int32_t head_dim;            /* D: 16, 32, 64, 128 or 256                             */
+  int32_t dtype;               /* HYB_BF16 or HYB_F32: q, k, v and out                  */
+  float scale;                 /* of the output (1/sqrt(D) usual)                       */
+  float qk_norm_eps;           /* > 0: q and k are brought to unit length; 0: not       */
+  int64_t q_stride;            /* elements between tokens; 0: packed                    */
+  int64_t k_stride;
+  int64_t v_stride;
+} hyb_delta_dims_t;
+
+/* One token per request: row b of q, k, v, g, beta and out is request b's, its state
+ * state_pool[state_slots[b]] is updated in place. A slot outside [0, num_state_slots) sets
+ * HYB_DEVERR_BAD_STATE and that request is skipped (its out row is left as it was). Two
+ * requests of one call must not share a slot. B = 0 is a no-op; B, num_v_heads <= 65535. */
+hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const void* v,
+                                  const float* g, const float* beta, float* state_pool,
+                                  int32_t num_state_slots, const int32_t* state_slots, int32_t B,
+                                  const hyb_delta_dims_t* d, void* stream);
+
+/* Whole prompts, or their next parts: request b owns rows [cu_seqlens[b], cu_seqlens[b+1]) and
+ * starts from zero when reset[b] != 0 (reset may be NULL: no reset), else from
+ * state_pool[state_slots[b]]; its last state goes back there. Equals hyb_gated_delta_step
+ * applied token by token. A call may start and end at any row: where a prompt is cut
+ * between calls changes only the rounding. A request without rows keeps its state (zero with
+ * reset). T (host) is the number of rows of q, k, v, g, beta and out, max_len (host) a bound on
+ * every request's rows. A request whose rows are not within [0, T), or more than max_len, sets
+ * HYB_DEVERR_BAD_LENGTH, one with a bad slot HYB_DEVERR_BAD_STATE; it is skipped. Rows that
+ * belong to no request are left as they were.
+ * bf16 with D = 128 runs the tensor-core kernel (chunks of 64 rows), other shapes the token
+ * recurrence on the CUDA cores. `workspace`: device memory, 8-byte aligned, of
+ * hyb_gated_delta_chunked_prefill_workspace_size() bytes (a short, misaligned or missing one is
+ * HYB_ERR_INVALID_ARG when B > 0); no initialisation, left alone between calls. Calls that may
+ * run at the same time need workspaces of their own: see hyb_linear_attn_chunked_prefill, whose
+ * rules on it hold here too. */
+size_t hyb_gated_delta_chunked_prefill_workspace_size(int32_t B, int32_t T,
+                                                      const hyb_delta_dims_t* d);
+hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const void* k,
+                                             const void* v, const float* g, const float* beta,
+                                             const int32_t* cu_seqlens, float* state_pool,
+                                             int32_t num_state_slots, const int32_t* state_slots,
+                                             const uint8_t* reset, int32_t B, int32_t T,
+                                             int32_t max_len, const hyb_delta_dims_t* d,
+                                             void* workspace, size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------------------------
+ * A Full layer's rows on their way from the projection to attention, in one pass: each
+ * head of q and k is normed and turned to its position, q goes to q_out, k and v into the paged
+ * cache. Per row x of q (weight w = q_weight) or k (k_weight), with p = positions[t]:
+ *     y = (w + weight_offset) * x / sqrt(mean(x^2) + eps)         (without norm when w is NULL)
+ *     the first rot_dim elements turn in pairs (a, b) = (y[i], y[i + rot_dim/2]), or
+ *     (y[2i], y[2i+1]) when interleaved, i < rot_dim/2:
+ *         a' = m (a cos(p f_i) - b sin(p f_i)),   b' = m (b cos(p f_i) + a sin(p f_i))
+ *     with f = inv_freq and m = attn_factor; the elements behind them stay y.
+ * Everything is computed in fp32 (the angle p f_i without loss at any position) and
+ * rounded once. Scaling for long contexts is a choice of inv_freq and attn_factor.
+ *   q [T][num_q_heads][D], k and v [T][d->num_heads][D] of d->dtype; strides as in
+ *               hyb_delta_dims_t (0: packed)
+ *   positions   int32 [T]. Negative: the row is skipped and nothing of it written (a padded
+ *               batch). Above 2^24: HYB_DEVERR_BAD_LENGTH, skipped
+ *   slot_mapping int64 [T], as for hyb_paged_kv_append: -1 writes k and v nowhere, a slot beyond
+ *               the pool sets HYB_DEVERR_BAD_SLOT and writes none. No two rows may share a slot
+ *   inv_freq    fp32 [rot_dim / 2]; NULL when rot_dim is 0 (norm and append only)
+ *   q_weight, k_weight  fp32 [D], or NULL
+ *   q_out       packed [T][num_q_heads][D]; NULL with num_q_heads = 0. May be q when q is packed
+ *   k_out       packed [T][d->num_heads][D]: k's rows, for use without a cache; may be NULL, or k
+ *               when k is packed
+ *   k_cache, v_cache, slot_mapping: all three, or all three NULL (no append; v may then be NULL)
+ * Apart from those, outputs overlap neither inputs nor one another. d gives the cache's shape
+ * (num_heads, head_dim: 16, 32, 64, 128 or 256, block_size, num_blocks) and the type;
+ * scale, window and max_blocks_per_seq are not used. T = 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t num_q_heads;         /* heads of q; 0: no queries                             */
+  int32_t rot_dim;             /* elements of a head that turn: a multiple of 8, <= D   */
+  int32_t interleaved;         /* pairs (2i, 2i+1) instead of (i, i + rot_dim/2)        */
+  float eps;                   /* of the norm, > 0                                      */
+  float weight_offset;         /* added to the weights (0, or 1 for weights around 0)   */
+  float attn_factor;           /* m: 1 without long-context scaling                     */
+  int64_t q_stride;            /* elements between tokens; 0: packed                    */
+  int64_t k_stride;
+  int64_t v_stride;
+} hyb_rope_dims_t;
+
+hyb_status_t hyb_qk_norm_rope_append(void* q_out, void* k_out, const void* q, const void* k,
+                                     const void* v, const int32_t* positions,
+                                     const int64_t* slot_mapping, const float* inv_freq,
+                                     const float* q_weight, const float* k_weight, int32_t T,
+                                     void* k_cache, void* v_cache, const hyb_rope_dims_t* r,
+                                     const hyb_attn_dims_t* d, void* stream);
+
+/* -------------------------------------------------------------------------
  * A7. Layer dispatch [KV §2.2: layer types registered from the model config,
  * split memory pools, per-forward metadata of seq lens, block tables and state
  * buffers handed to each op together with the layer type; VL §3.2: an execution

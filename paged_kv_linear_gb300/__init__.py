@@ -45,6 +45,18 @@ class hyb_batch_meta_t(C.Structure):
                 ("max_q_len", C.c_int32)]
 
 
+class hyb_delta_dims_t(C.Structure):
+    _fields_ = [("num_qk_heads", C.c_int32), ("num_v_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("dtype", C.c_int32), ("scale", C.c_float), ("qk_norm_eps", C.c_float),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64)]
+
+
+class hyb_rope_dims_t(C.Structure):
+    _fields_ = [("num_q_heads", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("eps", C.c_float), ("weight_offset", C.c_float), ("attn_factor", C.c_float),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64)]
+
+
 class HybError(RuntimeError):
     pass
 
@@ -71,6 +83,11 @@ def _load():
         "hyb_linear_attn_chunked_prefill": [p, p, p, p, p, p, p, i32, p, p, i32, i32, i32, i32,
                                             i32, i32, i32, p, sz, p],
         "hyb_linear_attn_chunked_prefill_workspace_size": ([], sz),
+        "hyb_gated_delta_step": [p, p, p, p, p, p, p, i32, p, i32, p, p],
+        "hyb_gated_delta_chunked_prefill": [p, p, p, p, p, p, p, p, i32, p, p, i32, i32, i32, p, p,
+                                            sz, p],
+        "hyb_gated_delta_chunked_prefill_workspace_size": ([i32, i32, p], sz),
+        "hyb_qk_norm_rope_append": [p, p, p, p, p, p, p, p, p, p, i32, p, p, p, p, p],
         "hyb_layer_dispatch": [p, i32, i32, p, p, p, i32, p, sz, p],
         "hyb_cache_bytes": ([i32, i32, i32, i32, i64, i32, i32, i32, p, p], u64),
         "hyb_device_status": [p, i32],
@@ -110,8 +127,21 @@ def _p(x):
     return x.data_ptr()
 
 
+def _rows(x, stride):
+    """Device pointer of rows [T][H][D] whose tokens lie `stride` elements apart (0: packed)."""
+    if x is None or isinstance(x, int) or stride == 0:
+        return _p(x)
+    if not x.is_cuda:
+        raise HybError("device argument is not a CUDA tensor")
+    T, H, D = x.shape
+    sT, sH, sD = x.stride()
+    if (D > 1 and sD != 1) or (H > 1 and sH != D) or (T > 1 and sT != stride):
+        raise HybError(f"rows must have strides ({stride}, {D}, 1), not {(sT, sH, sD)}")
+    return x.data_ptr()
+
+
 def _d(d):
-    """Pointer to a hyb_attn_dims_t (None passes NULL)."""
+    """Pointer to a dims structure (None passes NULL)."""
     return None if d is None else C.byref(d)
 
 
@@ -141,6 +171,22 @@ def dims(num_heads, head_dim, num_blocks, max_blocks_per_seq, dtype=HYB_BF16, sc
         scale = head_dim ** -0.5
     return hyb_attn_dims_t(num_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
                            dtype, scale, window)
+
+
+def delta_dims(num_qk_heads, num_v_heads, head_dim, dtype=HYB_BF16, scale=None, qk_norm_eps=0.0,
+               q_stride=0, k_stride=0, v_stride=0) -> hyb_delta_dims_t:
+    if not isinstance(dtype, int):
+        dtype = dtype_code(dtype)
+    if scale is None:
+        scale = head_dim ** -0.5
+    return hyb_delta_dims_t(num_qk_heads, num_v_heads, head_dim, dtype, scale, qk_norm_eps,
+                            q_stride, k_stride, v_stride)
+
+
+def rope_dims(num_q_heads, rot_dim, eps=1e-6, interleaved=False, weight_offset=0.0,
+              attn_factor=1.0, q_stride=0, k_stride=0, v_stride=0) -> hyb_rope_dims_t:
+    return hyb_rope_dims_t(num_q_heads, rot_dim, 1 if interleaved else 0, eps, weight_offset,
+                           attn_factor, q_stride, k_stride, v_stride)
 
 
 def check(status: int, what: str = "hyb call") -> None:
@@ -229,6 +275,38 @@ def hyb_linear_attn_chunked_prefill(out, q, k, v, cu_seqlens, ctx_lens, state_po
 
 def hyb_linear_attn_chunked_prefill_workspace_size() -> int:
     return int(_lib.hyb_linear_attn_chunked_prefill_workspace_size())
+
+
+def hyb_gated_delta_step(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, d,
+                         stream=None):
+    """One token per request of the gated delta rule; d: delta_dims(...). q, k and v may be
+    views of wider rows whose token stride d gives."""
+    return _lib.hyb_gated_delta_step(_p(out), _rows(q, d.q_stride), _rows(k, d.k_stride),
+                                     _rows(v, d.v_stride), _p(g), _p(beta), _p(state_pool),
+                                     num_state_slots, _p(state_slots), B, _d(d), _s(stream))
+
+
+def hyb_gated_delta_chunked_prefill_workspace_size(B, T, d) -> int:
+    return int(_lib.hyb_gated_delta_chunked_prefill_workspace_size(B, T, _d(d)))
+
+
+def hyb_gated_delta_chunked_prefill(out, q, k, v, g, beta, cu_seqlens, state_pool, num_state_slots,
+                                    state_slots, reset, B, T, max_len, d, workspace, ws_bytes,
+                                    stream=None):
+    return _lib.hyb_gated_delta_chunked_prefill(
+        _p(out), _rows(q, d.q_stride), _rows(k, d.k_stride), _rows(v, d.v_stride), _p(g), _p(beta),
+        _p(cu_seqlens), _p(state_pool), num_state_slots, _p(state_slots), _p(reset), B, T, max_len,
+        _d(d), _p(workspace), ws_bytes, _s(stream))
+
+
+def hyb_qk_norm_rope_append(q_out, k_out, q, k, v, positions, slot_mapping, inv_freq, q_weight,
+                            k_weight, T, k_cache, v_cache, r, d, stream=None):
+    """Norm of each q and k head, rotary position and KV append in one pass; r: rope_dims(...),
+    d: dims(...) of the cache. q, k and v may be views of wider rows whose token stride r gives."""
+    return _lib.hyb_qk_norm_rope_append(
+        _p(q_out), _p(k_out), _rows(q, r.q_stride), _rows(k, r.k_stride), _rows(v, r.v_stride),
+        _p(positions), _p(slot_mapping), _p(inv_freq), _p(q_weight), _p(k_weight), T, _p(k_cache),
+        _p(v_cache), _d(r), _d(d), _s(stream))
 
 
 def layer_io(out=None, q=None, k=None, v=None, k_cache=None, v_cache=None, state_pool=None,

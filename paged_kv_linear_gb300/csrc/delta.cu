@@ -1,0 +1,424 @@
+// The gated delta rule: its one-token step, its prefill on the CUDA cores, and the entry points
+// of both calls (the tensor-core prefill is in delta_tc.cu).
+//
+// Per token and value head, with S the fp32 state (row i: key dim, column j: value dim):
+//     S <- e^g S,   u = beta (v - S^T k),   S <- S + k u^T,   out = scale S^T q.
+// Both kernels read the state once for k and q together: with S the state before the token,
+//     u = beta (v - e^g S^T k),   out = scale (e^g S^T q + (q.k) u),
+// so the two sums over i share their pass and their reduction, and the new state needs no second
+// one. q and k brought to unit length are q / |q| and k / |k|: factors of the sums, never
+// rounded rows.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "hyb_internal.cuh"
+
+namespace hyb {
+namespace {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+// 1 / |x| from the sum of squares; 1 where the rows are taken as they are
+__device__ __forceinline__ float inv_len(float ss, float eps) {
+  return eps > 0.f ? 1.f / sqrtf(ss + eps) : 1.f;
+}
+
+// ------------------------------------------------------------------ one token
+// Bound by HBM: each state is read and written once (2 x 64 KiB at D = 128), against 7 flops an
+// element. A CTA owns 32 columns of one state, 8 threads x float4 to a row and 32 rows a pass; all
+// loads of a thread (PASSES x 16 bytes) are in flight before the first use, and columns do not
+// depend on one another, so no CTA waits for another. The sums over the 128 rows go through
+// shuffles (4 rows of a warp) and shared memory (8 warps), one barrier in all.
+template <int D>
+struct DeltaStep {
+  static constexpr int COLS = D < 32 ? D : 32;
+  static constexpr int TPR = COLS / 4;                      // threads per row (float4 each)
+  static constexpr int THREADS = D * TPR < 256 ? D * TPR : 256;
+  static constexpr int RPP = THREADS / TPR;                 // rows per pass
+  static constexpr int PASSES = D / RPP;
+  static constexpr int NW = THREADS / 32;
+  static_assert(PASSES * RPP == D && NW * 32 == THREADS, "shape");
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(DeltaStep<D>::THREADS)
+delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restrict__ k,
+                  const T* __restrict__ v, const float* __restrict__ g,
+                  const float* __restrict__ beta, float* __restrict__ pool, int NS,
+                  const int32_t* __restrict__ slots, int Hv, int rep, int64_t qs, int64_t ks,
+                  int64_t vs, float scale, float eps, unsigned* status) {
+  using Sh = DeltaStep<D>;
+  constexpr int COLS = Sh::COLS, TPR = Sh::TPR, RPP = Sh::RPP, PASSES = Sh::PASSES, NW = Sh::NW;
+  __shared__ __align__(16) float red_k[NW][COLS], red_q[NW][COLS], red_s[NW][4];
+
+  pdl_wait();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int slot = slots[b];
+  if (slot < 0 || slot >= NS) {
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) flag(status, HYB_DEVERR_BAD_STATE);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tc = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  const int col = blockIdx.x * COLS + tc * 4;
+  float* S = pool + ((int64_t)slot * Hv + h) * D * D;
+
+  float4 st[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p)
+    st[p] = __ldcs(reinterpret_cast<const float4*>(S + (int64_t)(rg + p * RPP) * D + col));
+  pdl_trigger();                           // the next kernel may launch (it waits for this one)
+  const T* kr = k + b * ks + (int64_t)(h / rep) * D;
+  const T* qr = q + b * qs + (int64_t)(h / rep) * D;
+  const T* vr = v + b * vs + (int64_t)h * D + col;
+  float ki[PASSES], qi[PASSES], vv[4];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    ki[p] = to_f(kr[rg + p * RPP]);
+    qi[p] = to_f(qr[rg + p * RPP]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) vv[e] = to_f(vr[e]);
+  const float eg = expf(g[(int64_t)b * Hv + h]), be = beta[(int64_t)b * Hv + h];
+
+  float a[11] = {};                        // S^T k (4 columns), S^T q (4), k.k, q.q, q.k
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const float s[4] = {st[p].x, st[p].y, st[p].z, st[p].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = fmaf(ki[p], s[e], a[e]);
+      a[4 + e] = fmaf(qi[p], s[e], a[4 + e]);
+    }
+    a[8] = fmaf(ki[p], ki[p], a[8]);
+    a[9] = fmaf(qi[p], qi[p], a[9]);
+    a[10] = fmaf(qi[p], ki[p], a[10]);
+  }
+#pragma unroll
+  for (int o = TPR; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < 11; ++e) a[e] += __shfl_xor_sync(0xffffffffu, a[e], o);
+  if (lane < TPR) {
+    *reinterpret_cast<float4*>(&red_k[warp][lane * 4]) = make_float4(a[0], a[1], a[2], a[3]);
+    *reinterpret_cast<float4*>(&red_q[warp][lane * 4]) = make_float4(a[4], a[5], a[6], a[7]);
+    if (lane == 0) *reinterpret_cast<float4*>(red_s[warp]) = make_float4(a[8], a[9], a[10], 0.f);
+  }
+  __syncthreads();
+  float sk[4] = {}, sq[4] = {}, kk = 0.f, qq = 0.f, qk = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const float4 x = *reinterpret_cast<const float4*>(&red_k[w][tc * 4]);
+    const float4 y = *reinterpret_cast<const float4*>(&red_q[w][tc * 4]);
+    const float4 z = *reinterpret_cast<const float4*>(red_s[w]);
+    sk[0] += x.x; sk[1] += x.y; sk[2] += x.z; sk[3] += x.w;
+    sq[0] += y.x; sq[1] += y.y; sq[2] += y.z; sq[3] += y.w;
+    kk += z.x; qq += z.y; qk += z.z;
+  }
+  const float rk = inv_len(kk, eps), rq = inv_len(qq, eps);
+  float u[4];                              // the correction, times rk for the state's k
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = be * (vv[e] - eg * (rk * sk[e]));
+    if (rg == 0)
+      put(out + ((int64_t)b * Hv + h) * D + col + e, scale * rq * fmaf(rk * qk, x, eg * sq[e]));
+    u[e] = rk * x;
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p)
+    __stcs(reinterpret_cast<float4*>(S + (int64_t)(rg + p * RPP) * D + col),
+           make_float4(fmaf(ki[p], u[0], eg * st[p].x), fmaf(ki[p], u[1], eg * st[p].y),
+                       fmaf(ki[p], u[2], eg * st[p].z), fmaf(ki[p], u[3], eg * st[p].w)));
+}
+
+// ------------------------------------------------------------------ prefill on the CUDA cores
+// The recurrence itself, for the shapes without a tensor-core kernel (fp32 rows, other head
+// sizes): fp32 throughout. Columns of a state do not depend on one another, so a CTA carries 32
+// columns of one (request, head) in registers for the whole prompt, and D / 32 CTAs share a
+// state. A column's D rows lie with RG lanes of one warp, so a token takes two sums over registers
+// and one round of shuffles, and no barrier; barriers come with each batch of kTB tokens, whose
+// rows and scalars are staged in shared memory. Bound by the latency of that chain when there are
+// few chains, by fp32 arithmetic (4 D^2 fma per token and head) when there are many.
+template <int D>
+struct DeltaScan {
+  static constexpr int COLS = D < 32 ? D : 32;              // columns per CTA
+  static constexpr int RG = D < 32 ? 2 : D / 32;            // lanes per column
+  static constexpr int R = D / RG;                          // rows per lane
+  static constexpr int THREADS = COLS * RG;
+  static constexpr int CW = 32 / RG;                        // columns per warp
+  static_assert(R % 4 == 0 && THREADS % 32 == 0, "shape");
+};
+constexpr int kTB = 16;                                     // tokens per batch
+
+template <typename T, int D>
+__global__ void __launch_bounds__(DeltaScan<D>::THREADS)
+delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restrict__ k,
+                  const T* __restrict__ v, const float* __restrict__ g,
+                  const float* __restrict__ beta, const int32_t* __restrict__ cu,
+                  float* __restrict__ pool, int NS, const int32_t* __restrict__ slots,
+                  const uint8_t* __restrict__ reset, int rows_total, int max_len, int Hv, int rep,
+                  int64_t qs, int64_t ks, int64_t vs, float scale, float eps, unsigned* status) {
+  using Sh = DeltaScan<D>;
+  constexpr int COLS = Sh::COLS, RG = Sh::RG, R = Sh::R, CW = Sh::CW, NT = Sh::THREADS;
+  __shared__ __align__(16) float sq[kTB][D], sk[kTB][D];    // unit (or given) rows; q times scale
+  __shared__ float sv[kTB][COLS];
+  __shared__ float s_eg[kTB], s_be[kTB], s_qk[kTB];
+
+  const int c0 = blockIdx.x * COLS, h = blockIdx.y, b = blockIdx.z;
+  const bool first = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
+  const int slot = slots[b], t0 = cu[b], t1 = cu[b + 1];
+  if (slot < 0 || slot >= NS) {
+    if (first) flag(status, HYB_DEVERR_BAD_STATE);
+    return;
+  }
+  if (!delta_rows_ok(t0, t1, rows_total, max_len)) {
+    if (first) flag(status, HYB_DEVERR_BAD_LENGTH);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rg = lane / CW, c = warp * CW + lane % CW;      // row group, column of this CTA
+  float* S = pool + ((int64_t)slot * Hv + h) * D * D + c0 + c;
+  const bool zero = reset && reset[b];
+  if (t0 == t1 && !zero) return;
+  // rows 4 (m RG + rg) + e: the RG lanes' 16-byte reads of a staged row lie side by side
+  float s[R];
+#pragma unroll
+  for (int m = 0; m < R; ++m) {
+    const int i = 4 * ((m / 4) * RG + rg) + m % 4;
+    s[m] = zero ? 0.f : S[(int64_t)i * D];
+  }
+  for (int tb = t0; tb < t1; tb += kTB) {
+    const int nt = min(kTB, t1 - tb);
+    __syncthreads();                       // the last batch is used up
+    for (int e = threadIdx.x; e < nt * D; e += NT) {
+      const int t = e / D, i = e - t * D;
+      sq[t][i] = to_f(q[(tb + t) * qs + (int64_t)(h / rep) * D + i]);
+      sk[t][i] = to_f(k[(tb + t) * ks + (int64_t)(h / rep) * D + i]);
+    }
+    for (int e = threadIdx.x; e < nt * COLS; e += NT) {
+      const int t = e / COLS, j = e - t * COLS;
+      sv[t][j] = to_f(v[(tb + t) * vs + (int64_t)h * D + c0 + j]);
+    }
+    __syncthreads();
+    for (int t = warp; t < nt; t += NT / 32) {              // a warp per token: lengths, q.k
+      float kk = 0.f, qq = 0.f, qk = 0.f;
+      for (int i = lane; i < D; i += 32) {
+        const float x = sk[t][i], y = sq[t][i];
+        kk = fmaf(x, x, kk);
+        qq = fmaf(y, y, qq);
+        qk = fmaf(x, y, qk);
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        kk += __shfl_xor_sync(0xffffffffu, kk, o);
+        qq += __shfl_xor_sync(0xffffffffu, qq, o);
+        qk += __shfl_xor_sync(0xffffffffu, qk, o);
+      }
+      const float rk = inv_len(kk, eps), rq = scale * inv_len(qq, eps);
+      for (int i = lane; i < D; i += 32) {
+        sk[t][i] *= rk;
+        sq[t][i] *= rq;
+      }
+      if (lane == 0) {
+        const int64_t at = (int64_t)(tb + t) * Hv + h;
+        s_eg[t] = expf(g[at]);
+        s_be[t] = beta[at];
+        s_qk[t] = qk * rk * rq;
+      }
+    }
+    __syncthreads();
+    for (int t = 0; t < nt; ++t) {
+      float pk[4] = {}, pq[4] = {};        // four partial sums each: a shorter chain
+#pragma unroll
+      for (int m = 0; m < R; m += 4) {
+        const int i = 4 * ((m / 4) * RG + rg);
+        const float4 x = *reinterpret_cast<const float4*>(&sk[t][i]);
+        const float4 y = *reinterpret_cast<const float4*>(&sq[t][i]);
+        pk[0] = fmaf(x.x, s[m], pk[0]); pq[0] = fmaf(y.x, s[m], pq[0]);
+        pk[1] = fmaf(x.y, s[m + 1], pk[1]); pq[1] = fmaf(y.y, s[m + 1], pq[1]);
+        pk[2] = fmaf(x.z, s[m + 2], pk[2]); pq[2] = fmaf(y.z, s[m + 2], pq[2]);
+        pk[3] = fmaf(x.w, s[m + 3], pk[3]); pq[3] = fmaf(y.w, s[m + 3], pq[3]);
+      }
+      float dk = (pk[0] + pk[1]) + (pk[2] + pk[3]), dq = (pq[0] + pq[1]) + (pq[2] + pq[3]);
+#pragma unroll
+      for (int o = CW; o < 32; o <<= 1) {
+        dk += __shfl_xor_sync(0xffffffffu, dk, o);
+        dq += __shfl_xor_sync(0xffffffffu, dq, o);
+      }
+      const float eg = s_eg[t], u = s_be[t] * (sv[t][c] - eg * dk);
+      if (rg == 0)
+        put(out + ((int64_t)(tb + t) * Hv + h) * D + c0 + c, fmaf(s_qk[t], u, eg * dq));
+#pragma unroll
+      for (int m = 0; m < R; m += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&sk[t][4 * ((m / 4) * RG + rg)]);
+        s[m] = fmaf(x.x, u, eg * s[m]);
+        s[m + 1] = fmaf(x.y, u, eg * s[m + 1]);
+        s[m + 2] = fmaf(x.z, u, eg * s[m + 2]);
+        s[m + 3] = fmaf(x.w, u, eg * s[m + 3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < R; ++m) {
+    const int i = 4 * ((m / 4) * RG + rg) + m % 4;
+    S[(int64_t)i * D] = s[m];
+  }
+}
+
+// ------------------------------------------------------------------ launches
+struct Strides {
+  int64_t q, k, v;
+};
+Strides strides_of(const hyb_delta_dims_t* d) {
+  const int64_t qk = (int64_t)d->num_qk_heads * d->head_dim, vv = (int64_t)d->num_v_heads * d->head_dim;
+  return {d->q_stride ? d->q_stride : qk, d->k_stride ? d->k_stride : qk,
+          d->v_stride ? d->v_stride : vv};
+}
+
+template <typename T, int D>
+cudaError_t step_typed(void* out, const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, float* pool, int NS, const int32_t* slots, int B,
+                       const hyb_delta_dims_t* d, unsigned* status, cudaStream_t s) {
+  using Sh = DeltaStep<D>;
+  const Strides st = strides_of(d);
+  const dim3 grid(D / Sh::COLS, d->num_v_heads, B);
+  const cudaError_t e = launch_pdl(
+      delta_step_kernel<T, D>, grid, dim3(Sh::THREADS), 0, s, (T*)out, (const T*)q, (const T*)k,
+      (const T*)v, g, beta, pool, NS, slots, d->num_v_heads, d->num_v_heads / d->num_qk_heads, st.q,
+      st.k, st.v, d->scale, d->qk_norm_eps, status);
+  count_launch();
+  return e;
+}
+
+template <typename T, int D>
+cudaError_t scan_typed(void* out, const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, const int32_t* cu, float* pool, int NS,
+                       const int32_t* slots, const uint8_t* reset, int B, int rows, int max_len,
+                       const hyb_delta_dims_t* d, unsigned* status, cudaStream_t s) {
+  using Sh = DeltaScan<D>;
+  const Strides st = strides_of(d);
+  const dim3 grid(D / Sh::COLS, d->num_v_heads, B);
+  delta_scan_kernel<T, D><<<grid, Sh::THREADS, 0, s>>>(
+      (T*)out, (const T*)q, (const T*)k, (const T*)v, g, beta, cu, pool, NS, slots, reset, rows,
+      max_len, d->num_v_heads, d->num_v_heads / d->num_qk_heads, st.q, st.k, st.v, d->scale,
+      d->qk_norm_eps, status);
+  count_launch();
+  return cudaGetLastError();
+}
+
+#define HYB_DELTA_EACH(CALL)                                                            \
+  switch (d->head_dim) {                                                                \
+    case 16: return d->dtype == HYB_BF16 ? CALL(__nv_bfloat16, 16) : CALL(float, 16);    \
+    case 32: return d->dtype == HYB_BF16 ? CALL(__nv_bfloat16, 32) : CALL(float, 32);    \
+    case 64: return d->dtype == HYB_BF16 ? CALL(__nv_bfloat16, 64) : CALL(float, 64);    \
+    case 128: return d->dtype == HYB_BF16 ? CALL(__nv_bfloat16, 128) : CALL(float, 128); \
+    case 256: return d->dtype == HYB_BF16 ? CALL(__nv_bfloat16, 256) : CALL(float, 256); \
+  }                                                                                     \
+  return cudaErrorInvalidValue;
+
+cudaError_t launch_step(void* out, const void* q, const void* k, const void* v, const float* g,
+                        const float* beta, float* pool, int NS, const int32_t* slots, int B,
+                        const hyb_delta_dims_t* d, unsigned* status, cudaStream_t s) {
+#define HYB_CALL(T, DD) step_typed<T, DD>(out, q, k, v, g, beta, pool, NS, slots, B, d, status, s)
+  HYB_DELTA_EACH(HYB_CALL)
+#undef HYB_CALL
+}
+
+cudaError_t launch_scan(void* out, const void* q, const void* k, const void* v, const float* g,
+                        const float* beta, const int32_t* cu, float* pool, int NS,
+                        const int32_t* slots, const uint8_t* reset, int B, int rows, int max_len,
+                        const hyb_delta_dims_t* d, unsigned* status, cudaStream_t s) {
+#define HYB_CALL(T, DD) \
+  scan_typed<T, DD>(out, q, k, v, g, beta, cu, pool, NS, slots, reset, B, rows, max_len, d, status, s)
+  HYB_DELTA_EACH(HYB_CALL)
+#undef HYB_CALL
+}
+#undef HYB_DELTA_EACH
+
+// ------------------------------------------------------------------ argument checks
+bool al(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+hyb_status_t check_delta_dims(const hyb_delta_dims_t* d) {
+  if (!d || d->num_qk_heads <= 0 || d->num_v_heads <= 0 || d->head_dim <= 0) return HYB_ERR_INVALID_ARG;
+  if (d->num_v_heads % d->num_qk_heads != 0) return HYB_ERR_INVALID_ARG;
+  if (d->dtype != HYB_BF16 && d->dtype != HYB_F32) return HYB_ERR_INVALID_ARG;
+  if (!std::isfinite(d->scale) || !(d->qk_norm_eps >= 0.f) || !std::isfinite(d->qk_norm_eps))
+    return HYB_ERR_INVALID_ARG;
+  const int D = d->head_dim;
+  if (d->num_v_heads > 65535 || (D != 16 && D != 32 && D != 64 && D != 128 && D != 256))
+    return HYB_ERR_UNSUPPORTED;
+  const int64_t qk = (int64_t)d->num_qk_heads * D, vv = (int64_t)d->num_v_heads * D;
+  const int64_t unit = d->dtype == HYB_BF16 ? 8 : 4;       // 16 bytes
+  const int64_t given[3] = {d->q_stride, d->k_stride, d->v_stride}, least[3] = {qk, qk, vv};
+  for (int i = 0; i < 3; ++i)
+    if (given[i] != 0 && (given[i] < least[i] || given[i] % unit != 0 || given[i] > ((int64_t)1 << 32)))
+      return HYB_ERR_INVALID_ARG;
+  return HYB_OK;
+}
+
+hyb_status_t check_delta(const void* out, const void* q, const void* k, const void* v,
+                         const float* g, const float* beta, const float* pool, int NS,
+                         const int32_t* slots, int B, const hyb_delta_dims_t* d) {
+  const hyb_status_t st = check_delta_dims(d);
+  if (st != HYB_OK) return st;
+  if (B < 0 || NS <= 0) return HYB_ERR_INVALID_ARG;
+  if (B > 65535) return HYB_ERR_UNSUPPORTED;               // grid.z
+  if ((int64_t)NS * d->num_v_heads * d->head_dim * d->head_dim > ((int64_t)1 << 40))
+    return HYB_ERR_UNSUPPORTED;
+  if (B == 0) return HYB_OK;
+  if (!out || !q || !k || !v || !g || !beta || !pool || !slots) return HYB_ERR_INVALID_ARG;
+  if (!al(out, 16) || !al(q, 16) || !al(k, 16) || !al(v, 16) || !al(pool, 16) || !al(g, 4) ||
+      !al(beta, 4) || !al(slots, 4))
+    return HYB_ERR_INVALID_ARG;
+  return HYB_OK;
+}
+
+}  // namespace
+}  // namespace hyb
+
+using namespace hyb;
+
+extern "C" {
+
+hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const void* v,
+                                  const float* g, const float* beta, float* state_pool,
+                                  int32_t num_state_slots, const int32_t* state_slots, int32_t B,
+                                  const hyb_delta_dims_t* d, void* stream) {
+  const hyb_status_t st =
+      check_delta(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, d);
+  if (st != HYB_OK || B == 0) return st;
+  unsigned* sw = status_word();
+  if (!sw) return HYB_ERR_CUDA;
+  return cuda_status(launch_step(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B,
+                                 d, sw, (cudaStream_t)stream));
+}
+
+size_t hyb_gated_delta_chunked_prefill_workspace_size(int32_t B, int32_t T,
+                                                      const hyb_delta_dims_t* d) {
+  if (B <= 0 || T < 0 || check_delta_dims(d) != HYB_OK) return 0;
+  return kLinPrefillWsBytes;
+}
+
+hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const void* k,
+                                             const void* v, const float* g, const float* beta,
+                                             const int32_t* cu_seqlens, float* state_pool,
+                                             int32_t num_state_slots, const int32_t* state_slots,
+                                             const uint8_t* reset, int32_t B, int32_t T,
+                                             int32_t max_len, const hyb_delta_dims_t* d,
+                                             void* workspace, size_t ws_bytes, void* stream) {
+  const hyb_status_t st =
+      check_delta(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, d);
+  if (st != HYB_OK) return st;
+  if (T < 0 || max_len < 0 || max_len > T) return HYB_ERR_INVALID_ARG;
+  if (B == 0) return HYB_OK;
+  if (!cu_seqlens || !al(cu_seqlens, 4)) return HYB_ERR_INVALID_ARG;
+  if (!workspace || !al(workspace, 8) || ws_bytes < kLinPrefillWsBytes) return HYB_ERR_INVALID_ARG;
+  unsigned* sw = status_word();
+  if (!sw) return HYB_ERR_CUDA;
+  return cuda_status(launch_scan(out, q, k, v, g, beta, cu_seqlens, state_pool, num_state_slots,
+                                 state_slots, reset, B, T, max_len, d, sw, (cudaStream_t)stream));
+}
+
+}  // extern "C"

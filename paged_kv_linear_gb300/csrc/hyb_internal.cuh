@@ -142,6 +142,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// A gated delta request's rows [t0, t1): within the call's T rows and its bound on a request's.
+__device__ __forceinline__ bool delta_rows_ok(int t0, int t1, int T, int max_len) {
+  return t0 >= 0 && t1 >= t0 && t1 <= T && t1 - t0 <= max_len;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
