@@ -417,6 +417,13 @@ hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const voi
   if (!workspace || !al(workspace, 8) || ws_bytes < kLinPrefillWsBytes) return HYB_ERR_INVALID_ARG;
   unsigned* sw = status_word();
   if (!sw) return HYB_ERR_CUDA;
+  if (delta_prefill_tc_supported(d)) {
+    const Strides x = strides_of(d);
+    return cuda_status(launch_delta_prefill_tc(out, q, k, v, g, beta, cu_seqlens, state_pool,
+                                               num_state_slots, state_slots, reset, B, T, max_len,
+                                               d, x.q, x.k, x.v, workspace, sw,
+                                               (cudaStream_t)stream));
+  }
   return cuda_status(launch_scan(out, q, k, v, g, beta, cu_seqlens, state_pool, num_state_slots,
                                  state_slots, reset, B, T, max_len, d, sw, (cudaStream_t)stream));
 }

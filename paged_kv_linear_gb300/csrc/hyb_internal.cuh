@@ -112,11 +112,20 @@ bool linear_prefill_tc_supported(int dtype, int D, int C);
 // (at most kLinMaxCtas CTAs), 64-bit words.
 constexpr int kLinMaxCtas = 256;
 constexpr size_t kLinPrefillWsBytes = 8 * (1 + kLinMaxCtas);
+cudaError_t launch_handoff_epoch(void* ws, cudaStream_t s);   // a new epoch in such a workspace
 cudaError_t launch_linear_prefill_tc(void* out, const void* q, const void* k, const void* v,
                                      const int32_t* cu, const int32_t* ctx, float* pool, int NS,
                                      const int32_t* slots, const uint8_t* reset, int B, int T,
                                      int max_len, int H, int C, void* ws, unsigned* status,
                                      cudaStream_t s);
+bool delta_prefill_tc_supported(const hyb_delta_dims_t* d);
+// qs, ks, vs: elements between tokens
+cudaError_t launch_delta_prefill_tc(void* out, const void* q, const void* k, const void* v,
+                                    const float* g, const float* beta, const int32_t* cu,
+                                    float* pool, int NS, const int32_t* slots,
+                                    const uint8_t* reset, int B, int T, int max_len,
+                                    const hyb_delta_dims_t* d, int64_t qs, int64_t ks, int64_t vs,
+                                    void* ws, unsigned* status, cudaStream_t s);
 bool prefill_tc_supported(int dtype, int D);
 cudaError_t launch_prefill_tc(void* out, const void* q, const void* kc, const void* vc,
                               const int32_t* bt, const int32_t* cu, const int32_t* ctx, int B,

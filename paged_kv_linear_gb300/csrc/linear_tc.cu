@@ -39,6 +39,7 @@
 // token row of 256 bytes).
 #include <cuda_bf16.h>
 
+#include "chain_split.cuh"
 #include "tc.cuh"
 
 namespace hyb {
@@ -77,21 +78,7 @@ struct Bars {
 static_assert(sizeof(Bars) <= 256, "barriers overflow their shared-memory slot");
 
 // ------------------------------------------------------------------ work split
-// Units are the (request, head) chains, in order u = b * H + h; unit u has nch(b) chunks.
-// Laid end to end they occupy G chunk positions. CTA p takes positions [p*L, (p+1)*L) with
-// L = max(longest chain, ceil(G / P)) (McNaughton's wrap-around rule for preemptive
-// scheduling on P machines), so no chain crosses more than one CTA boundary. A chain cut
-// at the boundary (p+1)*L is run in two parts, its first chunks by CTA p+1 FIRST and the
-// rest by CTA p LAST: the first part is no longer than the work CTA p does before its last
-// part, so the state it hands over (through the state pool) is ready when it is needed.
-// A handoff is announced by a flag that names the call: the call's epoch (a counter that a
-// one-thread kernel bumps right before every launch, in stream order, so graph replays get
-// fresh epochs too) and the launch's grid id (distinct for launches that run at the same
-// time). A waiting CTA accepts only its own call's value, never one left by an earlier call.
-// Epoch and flags live in the caller's workspace: hs[0] is the epoch, hs[1 + p] holds the tag
-// of the call whose CTA p has written the state of the chain it cut (at its first boundary)
-// to the pool. The library itself holds no handoff state, so calls with distinct workspaces
-// never see each other's flags.
+// (see chain_split.cuh)
 constexpr int kMaxCtas = kLinMaxCtas;        // grid limit (one CTA per SM)
 
 __global__ void linear_handoff_epoch_kernel(unsigned long long* hs) {
@@ -99,81 +86,9 @@ __global__ void linear_handoff_epoch_kernel(unsigned long long* hs) {
   hs[0] += 1;
 }
 
-struct Plan {
-  int head_u, head_end;      // chain run first, chunks [0, head_end); -1: none
-  int full_u0, full_u1;      // chains run whole, in order
-  int tail_u, tail_begin;    // chain run last, chunks [tail_begin, nch); -1: none
-};
-
 __device__ __forceinline__ int chunks_of(const int32_t* cu, int b) {
   const int n = cu[b + 1] - cu[b];
   return n > 0 ? (n + kC - 1) / kC : 0;
-}
-
-__device__ __forceinline__ int warp_incl_scan(int x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-
-// Run by one whole warp; every lane returns the same plan for CTA p of P.
-__device__ Plan make_plan(const int32_t* cu, int B, int H, int P, int p, int lane) {
-  long long total = 0;
-  int longest = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int nc = b0 + lane < B ? chunks_of(cu, b0 + lane) : 0;
-    total += __reduce_add_sync(0xffffffffu, (unsigned)nc);
-    longest = max(longest, (int)__reduce_max_sync(0xffffffffu, (unsigned)nc));
-  }
-  const long long G = total * H;
-  const long long L = max((long long)longest, (G + P - 1) / P);
-  const long long s = (long long)p * L, e = min(s + L, G);
-  Plan pl{-1, 0, 0, 0, -1, 0};
-  if (s >= G) return pl;
-  // locate positions s and e: request b holds [base + H*excl, base + H*incl)
-  int us = -1, offs = 0, ue = -1, offe = 0;
-  long long base = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane;
-    const int nc = b < B ? chunks_of(cu, b) : 0;
-    const int incl = warp_incl_scan(nc, lane);
-    const long long lo = base + (long long)H * (incl - nc), hi = base + (long long)H * incl;
-    const bool in_s = nc > 0 && s >= lo && s < hi, in_e = nc > 0 && e >= lo && e < hi;
-    const unsigned ms = __ballot_sync(0xffffffffu, in_s), me = __ballot_sync(0xffffffffu, in_e);
-    const int u_s = in_s ? b * H + (int)((s - lo) / nc) : 0, o_s = in_s ? (int)((s - lo) % nc) : 0;
-    const int u_e = in_e ? b * H + (int)((e - lo) / nc) : 0, o_e = in_e ? (int)((e - lo) % nc) : 0;
-    if (ms) {
-      const int l = __ffs(ms) - 1;
-      us = __shfl_sync(0xffffffffu, u_s, l);
-      offs = __shfl_sync(0xffffffffu, o_s, l);
-    }
-    if (me) {
-      const int l = __ffs(me) - 1;
-      ue = __shfl_sync(0xffffffffu, u_e, l);
-      offe = __shfl_sync(0xffffffffu, o_e, l);
-    }
-    base += (long long)H * __shfl_sync(0xffffffffu, incl, 31);
-  }
-  if (offs > 0) {
-    pl.head_u = us;
-    pl.head_end = chunks_of(cu, us / H) - offs;
-    pl.full_u0 = us + 1;
-  } else {
-    pl.full_u0 = us;
-  }
-  if (e >= G) {
-    pl.full_u1 = B * H;
-  } else if (offe > 0) {
-    pl.tail_u = ue;
-    pl.tail_begin = chunks_of(cu, ue / H) - offe;
-    pl.full_u1 = ue;
-  } else {
-    pl.full_u1 = ue;
-  }
-  return pl;
 }
 
 // A contiguous run of one chain's chunks, [c0, c1).
@@ -236,20 +151,6 @@ __device__ __forceinline__ bool next_run(Walk& w, const Plan& pl, const int32_t*
       return false;
     }
   }
-}
-
-__device__ __forceinline__ unsigned long long grid_id() {
-  unsigned long long g;
-  asm volatile("mov.u64 %0, %%gridid;" : "=l"(g));
-  return g;
-}
-__device__ __forceinline__ void st_release_u64(unsigned long long* p, unsigned long long v) {
-  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
-__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long* p) {
-  unsigned long long v;
-  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-  return v;
 }
 
 __device__ __forceinline__ uint4 pack8(const float* v) {     // bf16 copy of 8 values
@@ -328,7 +229,7 @@ linear_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     }
   }
   if (warp == 0) {
-    const Plan pl = make_plan(cu, B, H, P, p, lane);
+    const Plan pl = make_plan([&](int b) { return chunks_of(cu, b); }, B, H, P, p, lane);
     if (lane == 0) plan_sh = pl;
   }
   __syncthreads();
@@ -648,6 +549,13 @@ linear_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 
 }  // namespace
 
+cudaError_t launch_handoff_epoch(void* ws, cudaStream_t s) {
+  const cudaError_t e = launch_pdl(linear_handoff_epoch_kernel, dim3(1), dim3(1), 0, s,
+                                   static_cast<unsigned long long*>(ws));
+  count_launch();
+  return e;
+}
+
 bool linear_prefill_tc_supported(int dtype, int D, int C) {
   return dtype == HYB_BF16 && D == kD && C == kAlign;
 }
@@ -671,8 +579,7 @@ cudaError_t launch_linear_prefill_tc(void* out, const void* q, const void* k, co
   cudaError_t e = set_smem((const void*)linear_prefill_tc_kernel, kSmem);
   if (e != cudaSuccess) return e;
   unsigned long long* hs = static_cast<unsigned long long*>(ws);
-  e = launch_pdl(linear_handoff_epoch_kernel, dim3(1), dim3(1), 0, s, hs);
-  count_launch();
+  e = launch_handoff_epoch(ws, s);
   if (e != cudaSuccess) return e;
   // One CTA per SM at most (the shared memory allows no more), all resident at once: a CTA
   // may wait for the state another CTA hands over, so the launch is cooperative.
