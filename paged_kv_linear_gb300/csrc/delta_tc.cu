@@ -65,18 +65,28 @@ struct Gates {                                 // factors of a chunk's rows
   float cA[kC], rk[kC], pq[kC];                // beta / |k|, 1 / |k|, scale / |q|
   float dec, pad[3];                           // e^(G_C)
 };
-constexpr int kOffBar = kOffG + 2 * (int)sizeof(Gates);
+// What the warps need to know of a chunk. Warp 16 walks the CTA's runs and writes these, four
+// chunks deep; n = 0 ends them.
+struct Chunk {
+  float* S;                                    // the chain's state in the pool
+  int row, n, h, flags;                        // first row, rows, value head
+  int pad[2];
+};
+constexpr int kFirst = 1, kLast = 2, kZero = 4, kTake = 8, kHand = 16;   // of a run; its state: zero
+                                               // at first, taken over first, handed over at last
+constexpr int kOffChunk = kOffG + 2 * (int)sizeof(Gates);
+constexpr int kOffBar = kOffChunk + 4 * (int)sizeof(Chunk);
 
 struct Bars {
   uint64_t full_kq[2], full_v[2], free_kq[2], free_v[2];
-  uint64_t gates[2], w_ready[2], o_free[2];    // two: their readers may lag a chunk
+  uint64_t info[2], gates[2], w_ready[2], o_free[2];   // two: their readers may lag a chunk
   uint64_t d0_ready, d0_free, sa_ready, d1k_ready, d1q_ready, ra_ready, x_ready, xa_ready, s_ready;
   uint64_t q_read, o_ready, published, drain;
 };
 constexpr int kSmem = kOffBar + 512 + 1024;    // + slack for 1024-byte alignment
 static_assert(sizeof(Bars) <= 512 && kOffG % 16 == 0 && kOffBar % 8 == 0 && kSmem <= 227 * 1024, "smem");
 
-constexpr int kWarpMain = 4, kWarpOut = 12, kWarpTma = 16, kWarpMma = 17;
+constexpr int kWarpMain = 4, kWarpOut = 12, kWarpFeed = 16, kWarpMma = 17;
 constexpr int kThreads = 18 * 32;
 constexpr uint32_t kTmemCols = 512;
 // D0 | D1K | D1Q | S fp32 | operand terms of S. Once (k) and (q) have read the terms, R, X and X'
@@ -91,8 +101,8 @@ constexpr uint32_t kColOh = kCol1K, kColOm = kCol1K + 32;
 constexpr uint32_t kIdesc64 = idesc_bf16(128, 64, 0, 0);
 constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 1);   // B = K rows as K^T: N (key dim) major
 
-constexpr float kGateMin = -1e4f;              // e^g is 0 in fp32 far above
-constexpr double kLog2e = 1.4426950408889634;
+constexpr float kGateMax = 1e4f;               // e^-g is 0 and e^g infinite in fp32 far below
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;   // their sum is 1 / ln 2
 
 // ------------------------------------------------------------------ runs
 struct In {
@@ -132,7 +142,7 @@ __device__ __forceinline__ bool make_run(const In& in, int unit, int c0, int c1,
   return true;
 }
 // This CTA's chunks one after another: the first chain's part, the whole chains, the last
-// chain's part. Every warp walks its own copy.
+// chain's part.
 struct Walk {
   Seg sg;
   int ci;
@@ -174,40 +184,81 @@ __device__ __forceinline__ uint32_t pack_hi(float a, float b) {        // upper 
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+__device__ __forceinline__ void rest(float& a, float& b) {             // x - cut(x) for both
+  unpair(fma2(pair(cut(a), cut(b)), pair(-1.f, -1.f), pair(a, b)), a, b);
+}
 __device__ __forceinline__ void split3(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
   h = pack_hi(a, b);
-  const float a1 = a - cut(a), b1 = b - cut(b);
-  m = pack_hi(a1, b1);
-  l = pack_hi(a1 - cut(a1), b1 - cut(b1));
+  rest(a, b);
+  m = pack_hi(a, b);
+  rest(a, b);
+  l = pack_hi(a, b);
 }
 // two terms, the second rounded: off by at most 2^-16
 __device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m) {
   h = pack_hi(a, b);
-  m = pack_bf16(a - cut(a), b - cut(b));
+  rest(a, b);
+  m = pack_bf16(a, b);
+}
+
+// a gate in units of log 2 and steps of 2^-36 (a NaN is carried beside it)
+__device__ __forceinline__ long long to_fixed(float g) {
+  const float x = fminf(fmaxf(g, -kGateMax), kGateMax);
+  const float h = x * kLog2eHi, l = fmaf(x, kLog2eHi, -h) + x * kLog2eLo;
+  return __float2ll_rn(h * 0x1p36f) + __float2ll_rn(l * 0x1p36f);
+}
+__device__ __forceinline__ void from_fixed(long long x, bool nan, float& hi, float& lo) {
+  const float h = __ll2float_rn(x);
+  hi = nan ? __int_as_float(0x7fffffff) : h * 0x1p-36f;
+  lo = __ll2float_rn(x - __float2ll_rn(h)) * 0x1p-36f;
+}
+// As mbar_wait, timed by the SM's own clock (some 2 s), which is cheaper to read.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > 4000000000ll) return false;
+  return true;
 }
 
 __device__ __forceinline__ void bar_prep() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// the same, and whether ok holds for all of the preparing warps: they stop together
+__device__ __forceinline__ bool bar_prep_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
 
-// 32 values of this lane's state (key dims i0 ..): operand terms, and the accumulator times the
+// 16 values as operand terms: 8 columns at each of h, m and l
+__device__ __forceinline__ void put_terms(uint32_t h_at, uint32_t m_at, uint32_t l_at, const float* v) {
+  uint32_t h[8], m[8], l[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) split3(v[2 * e], v[2 * e + 1], h[e], m[e], l[e]);
+  tmem_st8u(h_at, h);
+  tmem_st8u(m_at, m);
+  tmem_st8u(l_at, l);
+}
+// 16 values of this lane's state (key dims i0 ..): operand terms, and the accumulator times the
 // coming chunk's decay
-__device__ __forceinline__ void put_state(uint32_t tl, int i0, const float* v, float dec) {
-  uint32_t h[16], m[16], l[16];
+__device__ __forceinline__ void put_state(uint32_t tl, int i0, float* v, float dec) {
+  put_terms(tl + kColSA + i0 / 2, tl + kColSA + 64 + i0 / 2, tl + kColSA + 128 + i0 / 2, v);
+  const f32x2 d2 = pair(dec, dec);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) split3(v[2 * e], v[2 * e + 1], h[e], m[e], l[e]);
-  tmem_st16u(tl + kColSA + i0 / 2, h);
-  tmem_st16u(tl + kColSA + 64 + i0 / 2, m);
-  tmem_st16u(tl + kColSA + 128 + i0 / 2, l);
-  float s[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) s[e] = v[e] * dec;
-  tmem_st32(tl + kColS + i0, s);
+  for (int e = 0; e < 16; e += 2) unpair(mul2(pair(v[e], v[e + 1]), d2), v[e], v[e + 1]);
+  tmem_st16(tl + kColS + i0, v);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
 delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
                         const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, __nv_bfloat16* __restrict__ out,
-                        const float* __restrict__ g, const float* __restrict__ beta, const In in,
+                        const float* __restrict__ g, const float* __restrict__ beta, const __grid_constant__ In in,
                         int B, int rep, float scale, float eps,
                         unsigned long long* __restrict__ hs, int cut_chains, unsigned* status) {
   const int p = blockIdx.x, P = gridDim.x;
@@ -234,8 +285,10 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     if (lane == 0) plan_sh = pl;
   }
   __syncthreads();
-  Walk w;
-  if (!first_chunk(in, plan_sh, w)) return;
+  {
+    Walk any;
+    if (!first_chunk(in, plan_sh, any)) return;
+  }
   unsigned long long tag = 0;
   if (cut_chains)
     tag = (*reinterpret_cast<volatile unsigned long long*>(hs) << 32) | (grid_id() & 0xffffffffull);
@@ -245,7 +298,11 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
                                            ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(sm + kOffBar);
   Gates* gates = reinterpret_cast<Gates*>(sm + kOffG);
+  Chunk* chunks = reinterpret_cast<Chunk*>(sm + kOffChunk);
 
+  for (int e = tid; e < (kOffA - kOffW) / 16; e += kThreads)   // W and P: zero above the diagonal
+    reinterpret_cast<uint4*>(sm + kOffW)[e] = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
   if (warp == kWarpMma) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
@@ -253,6 +310,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         mbar_init(&bars->full_v[i], 1);
         mbar_init(&bars->free_kq[i], 1);
         mbar_init(&bars->free_v[i], 256);
+        mbar_init(&bars->info[i], 32);
         mbar_init(&bars->gates[i], 128);
         mbar_init(&bars->w_ready[i], 128);
         mbar_init(&bars->o_free[i], 128);
@@ -281,45 +339,19 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
   const uint32_t tmem = tmem_base;
   const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);   // this warp's TMEM lanes
 
-#define HYB_WAIT(bar, parity) __all_sync(0xffffffffu, mbar_wait(&(bar), (parity)))
+#define HYB_WAIT(bar, parity) __all_sync(0xffffffffu, wait(&(bar), (parity)))
   bool ok = true;
   if (warp < kWarpMain) {
     // ------------------------------------------------------------ preparation
-    // After a wait that ran out these warps go on through the remaining chunks without waiting
-    // (their named barrier needs all four), on data that nobody uses.
     float* A = reinterpret_cast<float*>(sm + kOffA);
-    bool more = true;
-    for (int c = 0; more; ++c) {
-      const int st = c & 1, n = min(kC, w.sg.n - w.ci * kC);
-      const int64_t row0 = (int64_t)(w.sg.t0 + w.ci * kC) * in.H + w.sg.h;
+    for (int c = 0;; ++c) {
+      const int st = c & 1;
       Gates& G = gates[st];
-      float ga = 0.f, gb = 0.f;              // gates (warp 0) or betas (warp 1) of rows lane, lane + 32
-      if (warp < 2) {
-        const float* src = warp == 0 ? g : beta;
-        if (lane < n) ga = src[row0 + (int64_t)lane * in.H];
-        if (lane + 32 < n) gb = src[row0 + (int64_t)(lane + 32) * in.H];
-      }
-      if (ok && c >= 2) ok = HYB_WAIT(bars->o_free[st], ((c - 2) >> 1) & 1);
-      if (warp == 0) {
-        double a = (ga < kGateMin ? kGateMin : ga) * kLog2e, b = (gb < kGateMin ? kGateMin : gb) * kLog2e;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-          if (lane >= o) {
-            a += x;
-            b += y;
-          }
-        }
-        b += __shfl_sync(0xffffffffu, a, 31);
-        G.hi[lane] = (float)a;
-        G.lo[lane] = (float)(a - (double)(float)a);
-        G.hi[lane + 32] = (float)b;
-        G.lo[lane + 32] = (float)(b - (double)(float)b);
-      } else if (warp == 1) {
-        G.bt[lane] = ga;
-        G.bt[lane + 32] = gb;
-      }
-      if (ok) ok = HYB_WAIT(bars->full_kq[st], (c >> 1) & 1);
+      ok = bar_prep_all(HYB_WAIT(bars->info[st], (c >> 1) & 1));
+      if (!ok) break;
+      const int n = chunks[c & 3].n;
+      if (n == 0) break;
+      ok = HYB_WAIT(bars->full_kq[st], (c >> 1) & 1);
       {                                      // lengths: thread r, row r of the stacked [K; Q]
         const uint8_t* kq = sm + kOffKQ + st * kStageKQ + tid * 128;
         float ss = 0.f;
@@ -338,7 +370,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         if (tid < 64) G.rk[t] = t < n ? inv : 0.f;
         else G.pq[t] = t < n ? scale * inv : 0.f;
       }
-      bar_prep();
+      ok = bar_prep_all(ok);
+      if (!ok) break;
       if (tid < 64) {
         const float e = exp2f(G.hi[tid]);    // G.lo is below half an ulp of G.hi
         G.cA[tid] = G.bt[tid] * G.rk[tid];
@@ -349,24 +382,39 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       bar_prep();
       mbar_arrive(&bars->gates[st]);
-      if (ok) ok = HYB_WAIT(bars->d0_ready, c & 1);
+      ok = HYB_WAIT(bars->d0_ready, c & 1);
       tc_fence_after();
       {
-        // warps 0, 1: row t of K K^T -> column t of A^T; warps 2, 3: row t of Q K^T -> row t of P
+        // warps 0, 1: row t of K K^T -> column t of A^T; warps 2, 3: row t of Q K^T -> row t of P.
+        // Rows below 32 have nothing in the columns from 32 on.
         const int t = tid & 63;
-        const float ghi = G.hi[t], glo = G.lo[t], f = tid < 64 ? G.cA[t] : G.pq[t];
+        const bool is_p = tid >= 64;
+        const float ghi = G.hi[t], glo = G.lo[t], f = is_p ? G.pq[t] : G.cA[t];
+        const f32x2 neg = pair(-1.f, -1.f), gh2 = pair(ghi, ghi), gl2 = pair(glo, glo), f2 = pair(f, f);
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
+        for (int part = 0; part <= (t >> 5); ++part) {
           float v[32];
           tmem_ld32(tl + kCol0 + part * 32, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int s = part * 32 + e;
-            const float fade = fast_exp2((ghi - G.hi[s]) + (glo - G.lo[s]));
-            v[e] = s < t || (s == t && tid >= 64) ? (f * G.rk[s]) * fade * v[e] : 0.f;
+          for (int e = 0; e < 32; e += 4) {
+            const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[part * 32 + e]);
+            const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[part * 32 + e]);
+            const float4 r4 = *reinterpret_cast<const float4*>(&G.rk[part * 32 + e]);
+            float d[4];
+            unpair(add2(fma2(pair(h4.x, h4.y), neg, gh2), fma2(pair(l4.x, l4.y), neg, gl2)), d[0], d[1]);
+            unpair(add2(fma2(pair(h4.z, h4.w), neg, gh2), fma2(pair(l4.z, l4.w), neg, gl2)), d[2], d[3]);
+            unpair(mul2(mul2(pair(fast_exp2(d[0]), fast_exp2(d[1])), pair(v[e], v[e + 1])),
+                        mul2(pair(r4.x, r4.y), f2)), v[e], v[e + 1]);
+            unpair(mul2(mul2(pair(fast_exp2(d[2]), fast_exp2(d[3])), pair(v[e + 2], v[e + 3])),
+                        mul2(pair(r4.z, r4.w), f2)), v[e + 2], v[e + 3]);
           }
-          if (tid < 64) {
+          if (part == (t >> 5)) {            // at the diagonal: s < t, or s <= t for P
+            const int most = lane + (is_p ? 1 : 0);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = e < most ? v[e] : 0.f;
+          }
+          if (!is_p) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) A[(part * 32 + e) * kLdA + t] = v[e];
           } else {
@@ -385,20 +433,24 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       tc_fence_before();
       mbar_arrive(&bars->d0_free);
-      bar_prep();
-      // W = (1 + A)^-1 in 32 x 32 blocks. A is held transposed, A^T[s][t] at A[s * kLdA + t]. Warps 0
-      // and 1 invert the diagonal blocks, a lane a column: once w_m is final it is taken
-      // from every later row (independent fma, one 16-byte broadcast read for four). They put
-      // their blocks row-major in place of A's.
-      if (warp < 2) {
-        float* D = A + warp * 32 * (kLdA + 1);
-        float x[32];
+      ok = bar_prep_all(ok);
+      if (!ok) break;
+      // W = (1 + A)^-1 by blocks, 16, 32, 64; A is held transposed, A^T[s][t] at A[s * kLdA + t], W
+      // row-major in its place. Two blocks W00, W11 on the diagonal and A10 below give
+      // W10 = -W11 (A10 W00): the first product goes where W10 will be, A10^T lies in the (zero)
+      // block above it.
+      // 16 x 16, a warp each, a lane a column (lanes 16-31 do the same): once w_m is final it is
+      // taken from every later row (independent fma, one 16-byte broadcast read for four).
+      {
+        float* D = A + warp * 16 * (kLdA + 1);
+        const int col = lane & 15;
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = i == lane ? 1.f : 0.f;
+        for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
 #pragma unroll
-        for (int m = 0; m < 31; ++m) {
+        for (int m = 0; m < 15; ++m) {
 #pragma unroll
-          for (int i4 = (m + 1) / 4; i4 < 8; ++i4) {
+          for (int i4 = (m + 1) / 4; i4 < 4; ++i4) {
             const float4 a = *reinterpret_cast<const float4*>(&D[m * kLdA + i4 * 4]);
             const float y[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -407,57 +459,110 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           }
         }
         __syncwarp();
+        if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) D[i * kLdA + lane] = x[i];
-      }
-      bar_prep();
-      // lower left block: W21 = -W22 (A21 W11). Each warp takes 8 rows, a lane a column. A21^T lies
-      // in rows 0-31, columns 32-63; the product goes to rows 32-63, columns 0-31.
-      float x[8] = {};
-#pragma unroll 8
-      for (int m = 0; m < 32; ++m) {
-        const float b = A[m * kLdA + lane];
-        const float4 a0 = *reinterpret_cast<const float4*>(&A[m * kLdA + 32 + 8 * warp]);
-        const float4 a1 = *reinterpret_cast<const float4*>(&A[m * kLdA + 36 + 8 * warp]);
-        x[0] = fmaf(a0.x, b, x[0]); x[1] = fmaf(a0.y, b, x[1]);
-        x[2] = fmaf(a0.z, b, x[2]); x[3] = fmaf(a0.w, b, x[3]);
-        x[4] = fmaf(a1.x, b, x[4]); x[5] = fmaf(a1.y, b, x[5]);
-        x[6] = fmaf(a1.z, b, x[6]); x[7] = fmaf(a1.w, b, x[7]);
-      }
-#pragma unroll
-      for (int r = 0; r < 8; ++r) A[(32 + 8 * warp + r) * kLdA + lane] = x[r];
-      bar_prep();
-#pragma unroll
-      for (int r = 0; r < 8; ++r) x[r] = 0.f;
-#pragma unroll 4
-      for (int m4 = 0; m4 < 8; ++m4) {
-        float b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = A[(32 + 4 * m4 + e) * kLdA + lane];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float4 a = *reinterpret_cast<const float4*>(&A[(32 + 8 * warp + r) * kLdA + 32 + 4 * m4]);
-          x[r] = fmaf(-a.x, b[0], x[r]);
-          x[r] = fmaf(-a.y, b[1], x[r]);
-          x[r] = fmaf(-a.z, b[2], x[r]);
-          x[r] = fmaf(-a.w, b[3], x[r]);
+          for (int i = 0; i < 16; ++i) D[i * kLdA + col] = x[i];
         }
       }
-      // into the place of A21^T (rows r, columns 32-63), which is used up
-#pragma unroll
-      for (int r = 0; r < 8; ++r) A[(8 * warp + r) * kLdA + 32 + lane] = x[r];
       bar_prep();
-      {                                      // W as three bf16 terms: row t, half of its columns
+      {                                      // 32 x 32: two warps each, a lane 4 rows of a column
+        float* D = A + (warp >> 1) * 32 * (kLdA + 1);
+        const int col = lane & 15, r0 = 8 * (warp & 1) + 4 * (lane >> 4);
+        f32x2 x0 = pair(0.f, 0.f), x1 = x0;
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+          const float b = D[m * kLdA + col];
+          const float4 a = *reinterpret_cast<const float4*>(&D[m * kLdA + 16 + r0]);
+          x0 = fma2(pair(a.x, a.y), pair(b, b), x0);
+          x1 = fma2(pair(a.z, a.w), pair(b, b), x1);
+        }
+        float y[4];
+        unpair(x0, y[0], y[1]);
+        unpair(x1, y[2], y[3]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) D[(16 + r0 + r) * kLdA + col] = y[r];
+        bar_prep();
+        f32x2 z[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[r] = pair(0.f, 0.f);
+#pragma unroll
+        for (int m = 0; m < 16; m += 4) {
+          const f32x2 b0 = pair(D[(16 + m) * kLdA + col], D[(17 + m) * kLdA + col]);
+          const f32x2 b1 = pair(D[(18 + m) * kLdA + col], D[(19 + m) * kLdA + col]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float4 a = *reinterpret_cast<const float4*>(&D[(16 + r0 + r) * kLdA + 16 + m]);
+            z[r] = fma2(pair(a.x, a.y), b0, z[r]);
+            z[r] = fma2(pair(a.z, a.w), b1, z[r]);
+          }
+        }
+        bar_prep();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float a, b;
+          unpair(z[r], a, b);
+          D[(16 + r0 + r) * kLdA + col] = -(a + b);
+          D[(r0 + r) * kLdA + 16 + col] = 0.f;
+        }
+      }
+      bar_prep();
+      {                                      // 64 x 64: each warp 8 rows, a lane a column
+        f32x2 x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = pair(0.f, 0.f);
+#pragma unroll 8
+        for (int m = 0; m < 32; ++m) {
+          const float b = A[m * kLdA + lane];
+          const float4 a0 = *reinterpret_cast<const float4*>(&A[m * kLdA + 32 + 8 * warp]);
+          const float4 a1 = *reinterpret_cast<const float4*>(&A[m * kLdA + 36 + 8 * warp]);
+          const f32x2 b2 = pair(b, b);
+          x[0] = fma2(pair(a0.x, a0.y), b2, x[0]);
+          x[1] = fma2(pair(a0.z, a0.w), b2, x[1]);
+          x[2] = fma2(pair(a1.x, a1.y), b2, x[2]);
+          x[3] = fma2(pair(a1.z, a1.w), b2, x[3]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float a, b;
+          unpair(x[r], a, b);
+          A[(32 + 8 * warp + 2 * r) * kLdA + lane] = a;
+          A[(33 + 8 * warp + 2 * r) * kLdA + lane] = b;
+        }
+        bar_prep();
+        f32x2 z[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) z[r] = pair(0.f, 0.f);
+#pragma unroll 4
+        for (int m = 0; m < 32; m += 4) {
+          const f32x2 b0 = pair(A[(32 + m) * kLdA + lane], A[(33 + m) * kLdA + lane]);
+          const f32x2 b1 = pair(A[(34 + m) * kLdA + lane], A[(35 + m) * kLdA + lane]);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float4 a = *reinterpret_cast<const float4*>(&A[(32 + 8 * warp + r) * kLdA + 32 + m]);
+            z[r] = fma2(pair(a.x, a.y), b0, z[r]);
+            z[r] = fma2(pair(a.z, a.w), b1, z[r]);
+          }
+        }
+        // not back into its place, where others still read: over A10^T (rows r, columns 32-63)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          float a, b;
+          unpair(z[r], a, b);
+          A[(8 * warp + r) * kLdA + 32 + lane] = -(a + b);
+        }
+      }
+      bar_prep();
+      // W as three bf16 terms: row t, half of its columns (the upper right block is zero from the start)
+      if (tid >= 64 || (tid & 1) == 0) {
         const int t = tid >> 1, half = tid & 1;
         const float* src = t < 32 ? A + t * kLdA : A + (half ? t * kLdA + 32 : (t - 32) * kLdA + 32);
-        const bool zero = t < 32 && half;
         uint8_t* dst = sm + kOffW + st * 3 * kTile64 + t * 128;
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; e += 4) {
-            const float4 u = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src + ch * 8 + e);
+            const float4 u = *reinterpret_cast<const float4*>(src + ch * 8 + e);
             v[e] = u.x; v[e + 1] = u.y; v[e + 2] = u.z; v[e + 3] = u.w;
           }
           uint32_t h[4], m[4], l[4];
@@ -471,7 +576,6 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       fence_async_smem();
       mbar_arrive(&bars->w_ready[st]);
-      more = next_chunk(in, plan_sh, w);
     }
     if (!ok && lane == 0) flag(status, HYB_DEVERR_TIMEOUT);
   } else if (warp < kWarpOut) {
@@ -479,13 +583,19 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     const int half = (warp - kWarpMain) >> 2;
     const int j = (warp & 3) * 32 + lane;    // value column: TMEM lane of this thread
     const int x0 = half * 32, i0 = half * 64;
-    bool have = true, start = true;
-    for (int c = 0; have; ++c) {
+    for (int c = 0;; ++c) {
       const int st = c & 1;
       const Gates& G = gates[st];
-      if (start) {                           // the run's first state
-        start = false;
-        if (w.sg.wait_handoff) {
+      ok = HYB_WAIT(bars->info[st], (c >> 1) & 1);
+      if (!ok) break;
+      const Chunk& ch = chunks[c & 3];
+      const int n = ch.n, flags = ch.flags;
+      if (n == 0) break;
+      ok = HYB_WAIT(bars->gates[st], (c >> 1) & 1);
+      if (!ok) break;
+      // this chunk's first state: the run's from the pool, or what the last chunk left in TMEM
+      if (flags & kFirst) {
+        if (flags & kTake) {
           const unsigned long long* fl = hs + 1 + (p + 1);
           const uint64_t t0 = global_ns();
           while (ld_acquire_u64(fl) != tag) {
@@ -496,21 +606,28 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
             __nanosleep(100);
           }
         }
-        ok = HYB_WAIT(bars->gates[st], (c >> 1) & 1);
-        if (!ok) break;
+        const float* S = ch.S;
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          float v[32];
+        for (int i = i0; i < i0 + 64; i += 16) {
+          float v[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            v[e] = w.sg.zero_start ? 0.f : __ldcg(w.sg.S + (int64_t)(i0 + part * 32 + e) * kD + j);
-          put_state(tl, i0 + part * 32, v, G.dec);
+          for (int e = 0; e < 16; ++e)
+            v[e] = flags & kZero ? 0.f : __ldcg(S + (i + e) * kD + j);
+          put_state(tl, i, v, G.dec);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bars->sa_ready);
+      } else {
+        const float dec = G.dec;
+#pragma unroll 2
+        for (int i = i0; i < i0 + 64; i += 16) {
+          float s[16];
+          tmem_ld16(tl + kColS + i, s);
+          tmem_ld_wait();
+          put_state(tl, i, s, dec);
+        }
       }
-      const int n = min(kC, w.sg.n - w.ci * kC);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars->sa_ready);
       // V of this column while (k) runs; rows past the request may hold anything
       ok = HYB_WAIT(bars->full_v[st], (c >> 1) & 1);
       if (!ok) break;
@@ -530,64 +647,70 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       if (!ok) break;
       tc_fence_after();
       {
-        float d[32];
+        float d[32];                         // all read before R's l goes into the same columns
         tmem_ld32(tl + kCol1K + x0, d);
         tmem_ld_wait();
-        uint32_t h[16], m[16], l[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 b = *reinterpret_cast<const float4*>(&G.bt[x0 + e]);
           const float4 a = *reinterpret_cast<const float4*>(&G.aR[x0 + e]);
-          split3(fmaf(-a.x, d[e], b.x * v[e]), fmaf(-a.y, d[e + 1], b.y * v[e + 1]), h[e / 2], m[e / 2], l[e / 2]);
-          split3(fmaf(-a.z, d[e + 2], b.z * v[e + 2]), fmaf(-a.w, d[e + 3], b.w * v[e + 3]), h[e / 2 + 1], m[e / 2 + 1], l[e / 2 + 1]);
+          d[e] = fmaf(-a.x, d[e], b.x * v[e]);
+          d[e + 1] = fmaf(-a.y, d[e + 1], b.y * v[e + 1]);
+          d[e + 2] = fmaf(-a.z, d[e + 2], b.z * v[e + 2]);
+          d[e + 3] = fmaf(-a.w, d[e + 3], b.w * v[e + 3]);
         }
-        tmem_st16u(tl + kColRh + x0 / 2, h);
-        tmem_st16u(tl + kColRm + x0 / 2, m);
-        tmem_st16u(tl + kColRl + x0 / 2, l);
-        tmem_st_wait();
+#pragma unroll
+        for (int x = 0; x < 32; x += 16) {
+          const int at = (x0 + x) / 2;
+          put_terms(tl + kColRh + at, tl + kColRm + at, tl + kColRl + at, d + x);
+        }
       }
+      tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->ra_ready);
       // X: times its way to the chunk's end for the state, and as it is for the outputs
       ok = HYB_WAIT(bars->x_ready, c & 1);
       if (!ok) break;
       tc_fence_after();
-      {
-        float d[32];
-        tmem_ld32(tl + kColX + x0, d);
+#pragma unroll
+      for (int x = 0; x < 32; x += 16) {
+        float d[16];
+        tmem_ld16(tl + kColX + x0 + x, d);
         tmem_ld_wait();
-        uint32_t h[16], m[16], l[16];
+        const int at = (x0 + x) / 2;
+        uint32_t h[8], m[8];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(&G.wX[x0 + e]);
-          split3(a.x * d[e], a.y * d[e + 1], h[e / 2], m[e / 2], l[e / 2]);
-          split3(a.z * d[e + 2], a.w * d[e + 3], h[e / 2 + 1], m[e / 2 + 1], l[e / 2 + 1]);
+        for (int e = 0; e < 8; ++e) split2(d[2 * e], d[2 * e + 1], h[e], m[e]);
+        tmem_st8u(tl + kColOh + at, h);
+        tmem_st8u(tl + kColOm + at, m);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(&G.wX[x0 + x + e]);
+          d[e] *= a.x;
+          d[e + 1] *= a.y;
+          d[e + 2] *= a.z;
+          d[e + 3] *= a.w;
         }
-        tmem_st16u(tl + kColXh + x0 / 2, h);
-        tmem_st16u(tl + kColXm + x0 / 2, m);
-        tmem_st16u(tl + kColXl + x0 / 2, l);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) split2(d[e], d[e + 1], h[e / 2], m[e / 2]);
-        tmem_st16u(tl + kColOh + x0 / 2, h);
-        tmem_st16u(tl + kColOm + x0 / 2, m);
-        tmem_st_wait();
+        put_terms(tl + kColXh + at, tl + kColXm + at, tl + kColXl + at, d);
       }
+      tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->xa_ready);
       // the chunk's last state
       ok = HYB_WAIT(bars->s_ready, c & 1);
       if (!ok) break;
       tc_fence_after();
-      if (w.ci == w.sg.c1 - 1) {             // end of a run: to the pool, and handed over if cut
+      if (flags & kLast) {                   // end of a run: to the pool, and handed over if cut
+        float* S = ch.S;
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          float s[32];
-          tmem_ld32(tl + kColS + i0 + part * 32, s);
+        for (int i = i0; i < i0 + 64; i += 16) {
+          float s[16];
+          tmem_ld16(tl + kColS + i, s);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) w.sg.S[(int64_t)(i0 + part * 32 + e) * kD + j] = s[e];
+          for (int e = 0; e < 16; ++e) S[(i + e) * kD + j] = s[e];
         }
-        if (w.sg.publish) {                  // at most once per CTA (its first run)
+        if (flags & kHand) {                 // at most once per CTA (its first run)
           __threadfence();
           mbar_arrive(&bars->published);
           if (tid == kWarpMain * 32) {
@@ -595,41 +718,28 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
             else flag(status, HYB_DEVERR_TIMEOUT);
           }
         }
-        start = true;
-        have = next_chunk(in, plan_sh, w);
-      } else {
-        next_chunk(in, plan_sh, w);
-        ok = HYB_WAIT(bars->gates[st ^ 1], ((c + 1) >> 1) & 1);
-        if (!ok) break;
-        const float dec = gates[st ^ 1].dec;
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          float s[32];
-          tmem_ld32(tl + kColS + i0 + part * 32, s);
-          tmem_ld_wait();
-          put_state(tl, i0 + part * 32, s, dec);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bars->sa_ready);
       }
     }
     if (!ok && lane == 0) flag(status, HYB_DEVERR_TIMEOUT);
-  } else if (warp < kWarpTma) {
+  } else if (warp < kWarpFeed) {
     // ------------------------------------------------------------ outputs
     const int j = (warp & 3) * 32 + lane;
-    bool more = true;
-    for (int c = 0; more; ++c) {
-      const int st = c & 1, n = min(kC, w.sg.n - w.ci * kC);
+    for (int c = 0;; ++c) {
+      const int st = c & 1;
       const Gates& G = gates[st];
+      ok = HYB_WAIT(bars->info[st], (c >> 1) & 1);
+      if (!ok) break;
+      const int n = chunks[c & 3].n;
+      if (n == 0) break;
+      __nv_bfloat16* dst = out + ((int64_t)chunks[c & 3].row * in.H + chunks[c & 3].h) * kD + j;
       ok = HYB_WAIT(bars->gates[st], (c >> 1) & 1);
       if (!ok) break;
       ok = HYB_WAIT(bars->d1q_ready, c & 1);
       if (!ok) break;
       tc_fence_after();
       float o[64];
-      tmem_ld32(tl + kCol1Q, o);
-      tmem_ld32(tl + kCol1Q + 32, o + 32);
+#pragma unroll
+      for (int x = 0; x < 64; x += 16) tmem_ld16(tl + kCol1Q + x, o + x);
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(&bars->q_read);
@@ -639,53 +749,87 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        float d[32];
-        tmem_ld32(tl + kCol1Q + part * 32, d);
+      for (int x = 0; x < 64; x += 16) {
+        float d[16];
+        tmem_ld16(tl + kCol1Q + x, d);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[part * 32 + e] += d[e];
+        for (int e = 0; e < 16; ++e) o[x + e] += d[e];
       }
       tc_fence_before();
       mbar_arrive(&bars->o_free[st]);
-      __nv_bfloat16* dst = out + ((int64_t)(w.sg.t0 + w.ci * kC) * in.H + w.sg.h) * kD + j;
 #pragma unroll
       for (int t = 0; t < 64; ++t)
         if (t < n) dst[(int64_t)t * in.H * kD] = __float2bfloat16_rn(o[t]);
-      more = next_chunk(in, plan_sh, w);
     }
     if (!ok && lane == 0) flag(status, HYB_DEVERR_TIMEOUT);
-  } else if (warp == kWarpTma) {
-    // ------------------------------------------------------------ loads
+  } else if (warp == kWarpFeed) {
+    // ------------------------------------------------------------ chunks, loads, gates
     if (lane == 0) {
       tma_prefetch_desc(&tq);
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
     }
-    bool more = true;
+    Walk w;
+    bool more = first_chunk(in, plan_sh, w);
     int ckq = 0, cv = 0;                     // chunks requested
-    for (int c = 0; more; ++c) {
-      const int st = c & 1, row = w.sg.t0 + w.ci * kC, hk = w.sg.h / rep;
-      if (c >= 2) ok = HYB_WAIT(bars->free_kq[st], ((c - 2) >> 1) & 1);
-      if (!ok) break;
-      if (lane == 0) {
-        uint8_t* kq = sm + kOffKQ + st * kStageKQ;
-        mbar_expect_tx(&bars->full_kq[st], kStageKQ);
-        for (int sb = 0; sb < 2; ++sb) {
-          tma_load_3d(kq + sb * kSubKQ, &tk, sb * 64, hk, row, &bars->full_kq[st]);
-          tma_load_3d(kq + sb * kSubKQ + 64 * 128, &tq, sb * 64, hk, row, &bars->full_kq[st]);
+    for (int c = 0;; ++c) {
+      const int st = c & 1, row = w.sg.t0 + w.ci * kC;
+      const int n = more ? min(kC, w.sg.n - w.ci * kC) : 0;
+      // gates and betas of rows lane and lane + 32
+      const int64_t at = (int64_t)row * in.H + w.sg.h + (int64_t)lane * in.H, at2 = at + 32ll * in.H;
+      const float ga = lane < n ? g[at] : 0.f, gb = lane + 32 < n ? g[at2] : 0.f;
+      const float ba = lane < n ? beta[at] : 0.f, bb = lane + 32 < n ? beta[at2] : 0.f;
+      if (n > 0) {
+        if (c >= 2) ok = HYB_WAIT(bars->free_kq[st], ((c - 2) >> 1) & 1);
+        if (!ok) break;
+        const int hk = w.sg.h / rep;
+        if (lane == 0) {
+          uint8_t* kq = sm + kOffKQ + st * kStageKQ;
+          mbar_expect_tx(&bars->full_kq[st], kStageKQ);
+          for (int sb = 0; sb < 2; ++sb) {
+            tma_load_3d(kq + sb * kSubKQ, &tk, sb * 64, hk, row, &bars->full_kq[st]);
+            tma_load_3d(kq + sb * kSubKQ + 64 * 128, &tq, sb * 64, hk, row, &bars->full_kq[st]);
+          }
         }
+        ckq = c + 1;
+        if (c >= 2) ok = HYB_WAIT(bars->free_v[st], ((c - 2) >> 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          uint8_t* vs = sm + kOffV + st * kStageV;
+          mbar_expect_tx(&bars->full_v[st], kStageV);
+          for (int sb = 0; sb < 2; ++sb)
+            tma_load_3d(vs + sb * kSubV, &tv, sb * 64, w.sg.h, row, &bars->full_v[st]);
+        }
+        cv = c + 1;
       }
-      ckq = c + 1;
-      if (c >= 2) ok = HYB_WAIT(bars->free_v[st], ((c - 2) >> 1) & 1);
+      // the buffers' last users are done (a slot of `chunks` is used two chunks longer)
+      if (c >= 2) ok = HYB_WAIT(bars->o_free[st], ((c - 2) >> 1) & 1);
       if (!ok) break;
       if (lane == 0) {
-        uint8_t* vs = sm + kOffV + st * kStageV;
-        mbar_expect_tx(&bars->full_v[st], kStageV);
-        for (int sb = 0; sb < 2; ++sb)
-          tma_load_3d(vs + sb * kSubV, &tv, sb * 64, w.sg.h, row, &bars->full_v[st]);
+        const int flags = (w.ci == w.sg.c0 ? kFirst | (w.sg.zero_start ? kZero : 0) | (w.sg.wait_handoff ? kTake : 0) : 0) |
+                          (w.ci == w.sg.c1 - 1 ? kLast | (w.sg.publish ? kHand : 0) : 0);
+        chunks[c & 3] = Chunk{w.sg.S, row, n, w.sg.h, flags, {0, 0}};
       }
-      cv = c + 1;
+      // running sum in units of log 2, exact in integer steps of 2^-36 (fp32 would lose the
+      // small gates behind large ones, and fp64 is slow on this GPU)
+      Gates& G = gates[st];
+      long long a = to_fixed(ga), b = to_fixed(gb);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        a += lane >= o ? x : 0;
+        b += lane >= o ? y : 0;
+      }
+      b += __shfl_sync(0xffffffffu, a, 31);
+      const unsigned na = __ballot_sync(0xffffffffu, ga != ga), nb = __ballot_sync(0xffffffffu, gb != gb);
+      const unsigned upto = 0xffffffffu >> (31 - lane);
+      from_fixed(a, (na & upto) != 0, G.hi[lane], G.lo[lane]);
+      from_fixed(b, na != 0 || (nb & upto) != 0, G.hi[lane + 32], G.lo[lane + 32]);
+      G.bt[lane] = ba;
+      G.bt[lane + 32] = bb;
+      mbar_arrive(&bars->info[st]);
+      if (n == 0) break;
       more = next_chunk(in, plan_sh, w);
     }
     if (!ok && lane == 0) {                  // let the loads in flight land before exiting
@@ -698,10 +842,14 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     const uint32_t sm0 = smem_u32(sm);
     const uint64_t km0 = sw128_desc(sm0, 16, 1024);            // K-major operands
     const uint64_t mn0 = sw128_desc(sm0, kSubKQ, 1024);        // K as [t][i], i-major: two 64-wide blocks
-    Walk ahead = w;                          // the chunk whose (0) comes next
-    // (0) of chunk cn: rows past the request become zero rows of K first
+    bool more = true;
+    // (0) of chunk cn, if there is one: rows past the request become zero rows of K first
     auto issue0 = [&](int cn) {
-      const int st = cn & 1, n = min(kC, ahead.sg.n - ahead.ci * kC);
+      const int st = cn & 1;
+      if (!HYB_WAIT(bars->info[st], (cn >> 1) & 1)) return false;
+      const int n = chunks[cn & 3].n;
+      more = n > 0;
+      if (!more) return true;
       if (!HYB_WAIT(bars->full_kq[st], (cn >> 1) & 1)) return false;
       if (n < kC) {
         uint8_t* ks = sm + kOffKQ + st * kStageKQ;
@@ -712,7 +860,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       if (cn >= 1 && !HYB_WAIT(bars->d0_free, (cn - 1) & 1)) return false;
       __syncwarp();
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after();
         const uint32_t kq = kOffKQ + st * kStageKQ;
 #pragma unroll
@@ -726,13 +874,12 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       return true;
     };
     ok = issue0(0);
-    bool more = true;
     for (int c = 0; ok && more; ++c) {
       const int st = c & 1;
       const uint32_t kq = kOffKQ + st * kStageKQ;
       ok = HYB_WAIT(bars->sa_ready, c & 1);
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < 24; ++x) {       // (k)
@@ -744,7 +891,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       __syncwarp();
       if (c >= 1) ok = HYB_WAIT(bars->o_free[st ^ 1], ((c - 1) >> 1) & 1);
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < 16; ++x) {       // (q)
@@ -754,12 +901,11 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         tc_commit(&bars->d1q_ready);
       }
       __syncwarp();
-      more = next_chunk(in, plan_sh, ahead);
-      if (more) ok = issue0(c + 1);
+      ok = issue0(c + 1);
       if (!ok) break;
       ok = HYB_WAIT(bars->w_ready[st], (c >> 1) & 1) && HYB_WAIT(bars->ra_ready, c & 1);
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after();
         const uint64_t wd = desc_add(km0, kOffW + st * 3 * kTile64);
 #pragma unroll
@@ -775,7 +921,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       __syncwarp();
       ok = HYB_WAIT(bars->xa_ready, c & 1);
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < 3; ++x) {        // (s)
@@ -789,7 +935,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       __syncwarp();
       ok = HYB_WAIT(bars->q_read, c & 1);
       if (!ok) break;
-      if (lane == 0) {
+      if (elect_one()) {
         tc_fence_after();
         const uint64_t pd = desc_add(km0, kOffP + st * 2 * kTile64);
 #pragma unroll
@@ -802,7 +948,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       __syncwarp();
     }
-    if (lane == 0) {
+    if (elect_one()) {
       if (!ok) {                             // let every issued MMA finish before exiting
         flag(status, HYB_DEVERR_TIMEOUT);
         tc_commit(&bars->drain);
