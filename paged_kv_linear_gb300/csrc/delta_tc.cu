@@ -55,18 +55,20 @@ constexpr int kOffKQ = 0;
 constexpr int kOffV = kOffKQ + 2 * kStageKQ;
 constexpr int kOffW = kOffV + 2 * kStageV;     // [buffer][term]
 constexpr int kOffP = kOffW + 2 * 3 * kTile64;
-constexpr int kOffA = kOffP + 2 * 2 * kTile64; // the system, fp32, then its inverse
-constexpr int kLdA = 68;                       // floats per row (16-byte rows, banks spread)
-constexpr int kOffG = kOffA + kC * kLdA * 4;
+constexpr int kOffA = kOffP + 2 * 2 * kTile64; // [group] the system, fp32, then its inverse
+constexpr int kLdA = 72;                       // floats per row: fragments of 4 x 8 hit 32 banks
+constexpr int kOffG = kOffA + 2 * kC * kLdA * 4;
 
 struct Gates {                                 // factors of a chunk's rows
   float hi[kC], lo[kC];                        // G in units of log 2, as a sum of two
-  float aR[kC], bt[kC], wX[kC], oq[kC];        // R = bt V - aR (K S); wX: X to the state; oq: Q S to O
-  float cA[kC], rk[kC], pq[kC];                // beta / |k|, 1 / |k|, scale / |q|
+  float bt[kC];                                // beta
+  float eR[kC], cA[kC], wB[kC];                // e^G / |k|, beta / |k|^2, beta / |k|
+  float wX[kC], pq[kC], oq[kC];                // e^(G_C - G), scale / |q|, scale e^G / |q|
   float dec, pad[3];                           // e^(G_C)
 };
-// What the warps need to know of a chunk. Warp 16 walks the CTA's runs and writes these, four
-// chunks deep; n = 0 ends them.
+// What the warps need to know of a chunk. The feeding warp walks the CTA's runs and writes these,
+// four chunks deep as the gates: chunk c's place is free once (s) of chunk c - 2 is done, which
+// implies that everybody has left chunk c - 4. n = 0 ends them.
 struct Chunk {
   float* S;                                    // the chain's state in the pool
   int row, n, h, flags;                        // first row, rows, value head
@@ -74,20 +76,21 @@ struct Chunk {
 };
 constexpr int kFirst = 1, kLast = 2, kZero = 4, kTake = 8, kHand = 16;   // of a run; its state: zero
                                                // at first, taken over first, handed over at last
-constexpr int kOffChunk = kOffG + 2 * (int)sizeof(Gates);
+constexpr int kOffChunk = kOffG + 4 * (int)sizeof(Gates);
 constexpr int kOffBar = kOffChunk + 4 * (int)sizeof(Chunk);
 
 struct Bars {
   uint64_t full_kq[2], full_v[2], free_kq[2], free_v[2];
-  uint64_t info[2], gates[2], w_ready[2], o_free[2];   // two: their readers may lag a chunk
-  uint64_t d0_ready, d0_free, sa_ready, d1k_ready, d1q_ready, ra_ready, x_ready, xa_ready, s_ready;
-  uint64_t q_read, o_ready, published, drain;
+  uint64_t info[4], gates[4];                  // their readers may lag by more than a chunk
+  uint64_t w_ready[2], o_free[2];
+  uint64_t d0_ready[2], d0_free, sa_ready, d1k_ready, d1q_ready, ra_ready, x_ready, xa_ready, s_ready;
+  uint64_t q_scaled, o_ready, d1q_free, published, drain;
 };
 constexpr int kSmem = kOffBar + 512 + 1024;    // + slack for 1024-byte alignment
 static_assert(sizeof(Bars) <= 512 && kOffG % 16 == 0 && kOffBar % 8 == 0 && kSmem <= 227 * 1024, "smem");
 
-constexpr int kWarpMain = 4, kWarpOut = 12, kWarpFeed = 16, kWarpMma = 17;
-constexpr int kThreads = 18 * 32;
+constexpr int kWarpMain = 8, kWarpOut = 16, kWarpFeed = 20, kWarpMma = 21;
+constexpr int kThreads = 22 * 32;
 constexpr uint32_t kTmemCols = 512;
 // D0 | D1K | D1Q | S fp32 | operand terms of S. Once (k) and (q) have read the terms, R, X and X'
 // take their places: R's h and m over S's l, R's l inside D1K (each thread over columns that only
@@ -222,17 +225,69 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-__device__ __forceinline__ void bar_prep() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// the same, and whether ok holds for all of the preparing warps: they stop together
-__device__ __forceinline__ bool bar_prep_all(bool ok) {
+// Operands of a warp's 16 x 8 x 8 product in two tf32 terms, rounded to nearest: h + l holds 22
+// bits. The low 13 bits of each word are zero.
+__device__ __forceinline__ uint32_t tf32_rn(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
+__device__ __forceinline__ void tf32_terms(float x, uint32_t& h, uint32_t& l) {
+  h = tf32_rn(x);
+  l = tf32_rn(x - __uint_as_float(h));
+}
+struct FragA {                                 // 16 x 8, element (r, k) at p[r * RS + k * KS]
+  uint32_t h[4], l[4];
+  // top, bottom: rows 0-7, 8-15 are read; else they are zero
+  template <int RS, int KS>
+  __device__ __forceinline__ void load(const float* p, int lane, bool top = true, bool bottom = true) {
+    const float* q = p + (lane >> 2) * RS + (lane & 3) * KS;
+    tf32_terms(top ? q[0] : 0.f, h[0], l[0]);
+    tf32_terms(bottom ? q[8 * RS] : 0.f, h[1], l[1]);
+    tf32_terms(top ? q[4 * KS] : 0.f, h[2], l[2]);
+    tf32_terms(bottom ? q[8 * RS + 4 * KS] : 0.f, h[3], l[3]);
+  }
+};
+struct FragB {                                 // 8 x 8, element (k, n) at p[k * kLdA + n]
+  uint32_t h[2], l[2];
+  __device__ __forceinline__ void load(const float* p, int lane) {
+    const float* q = p + (lane & 3) * kLdA + (lane >> 2);
+    tf32_terms(q[0], h[0], l[0]);
+    tf32_terms(q[4 * kLdA], h[1], l[1]);
+  }
+};
+__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void mma_tf32(float* c, const FragA& a, const FragB& b) {
+  mma_tf32(c, a.l, b.h);
+  mma_tf32(c, a.h, b.l);
+  mma_tf32(c, a.h, b.h);
+}
+// a result of such products, times sign, to p[r * kLdA + n]
+__device__ __forceinline__ void store_c(float* p, const float* c, float sign, int lane, bool bottom = true) {
+  float* q = p + (lane >> 2) * kLdA + 2 * (lane & 3);
+  *reinterpret_cast<float2*>(q) = make_float2(sign * c[0], sign * c[1]);
+  if (bottom) *reinterpret_cast<float2*>(q + 8 * kLdA) = make_float2(sign * c[2], sign * c[3]);
+}
+
+// Barrier of a group of four warps.
+__device__ __forceinline__ void bar_group(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+// The same, and whether ok holds for the whole group: where a wait runs out, its warps stop together.
+__device__ __forceinline__ bool bar_group_all(int id, bool ok) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)ok)
+      : "r"(id), "r"((uint32_t)ok)
       : "memory");
   return r != 0;
+}
+// A row of 256 bytes from shared to global memory by the copy engine.
+__device__ __forceinline__ void bulk_row(void* dst, const void* src) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], 256;" ::"l"(dst), "r"(smem_u32(src))
+               : "memory");
 }
 
 // 16 values as operand terms: 8 columns at each of h, m and l
@@ -257,7 +312,8 @@ __device__ __forceinline__ void put_state(uint32_t tl, int i0, float* v, float d
 __global__ void __launch_bounds__(kThreads, 1)
 delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
                         const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, __nv_bfloat16* __restrict__ out,
+                        const __grid_constant__ CUtensorMap tv,
+                        const __grid_constant__ CUtensorMap to, __nv_bfloat16* __restrict__ out,
                         const float* __restrict__ g, const float* __restrict__ beta, const __grid_constant__ In in,
                         int B, int rep, float scale, float eps,
                         unsigned long long* __restrict__ hs, int cut_chains, unsigned* status) {
@@ -300,7 +356,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
   Gates* gates = reinterpret_cast<Gates*>(sm + kOffG);
   Chunk* chunks = reinterpret_cast<Chunk*>(sm + kOffChunk);
 
-  for (int e = tid; e < (kOffA - kOffW) / 16; e += kThreads)   // W and P: zero above the diagonal
+  for (int e = tid; e < (kOffP - kOffW) / 16; e += kThreads)   // W: zero above the diagonal
     reinterpret_cast<uint4*>(sm + kOffW)[e] = make_uint4(0, 0, 0, 0);
   fence_async_smem();
   if (warp == kWarpMma) {
@@ -310,12 +366,14 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         mbar_init(&bars->full_v[i], 1);
         mbar_init(&bars->free_kq[i], 1);
         mbar_init(&bars->free_v[i], 256);
-        mbar_init(&bars->info[i], 32);
-        mbar_init(&bars->gates[i], 128);
         mbar_init(&bars->w_ready[i], 128);
         mbar_init(&bars->o_free[i], 128);
+        mbar_init(&bars->d0_ready[i], 1);
       }
-      mbar_init(&bars->d0_ready, 1);
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&bars->info[i], 32);
+        mbar_init(&bars->gates[i], 128);
+      }
       mbar_init(&bars->d0_free, 128);
       mbar_init(&bars->sa_ready, 256);
       mbar_init(&bars->d1k_ready, 1);
@@ -324,7 +382,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       mbar_init(&bars->x_ready, 1);
       mbar_init(&bars->xa_ready, 256);
       mbar_init(&bars->s_ready, 1);
-      mbar_init(&bars->q_read, 128);
+      mbar_init(&bars->q_scaled, 128);
+      mbar_init(&bars->d1q_free, 128);
       mbar_init(&bars->o_ready, 1);
       mbar_init(&bars->published, 256);
       mbar_init(&bars->drain, 1);
@@ -343,52 +402,67 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
   bool ok = true;
   if (warp < kWarpMain) {
     // ------------------------------------------------------------ preparation
-    float* A = reinterpret_cast<float*>(sm + kOffA);
-    for (int c = 0;; ++c) {
-      const int st = c & 1;
-      Gates& G = gates[st];
-      ok = bar_prep_all(HYB_WAIT(bars->info[st], (c >> 1) & 1));
+    // two groups of four warps, each for every second chunk
+    const int grp = warp >> 2, gw = warp & 3, gt = tid & 127, bar = 1 + grp;
+    const int st = grp;
+    float* A = reinterpret_cast<float*>(sm + kOffA) + grp * kC * kLdA;
+    for (int c = grp;; c += 2) {
+      Gates& G = gates[c & 3];
+      ok = bar_group_all(bar, HYB_WAIT(bars->info[c & 3], (c >> 2) & 1));
       if (!ok) break;
       const int n = chunks[c & 3].n;
       if (n == 0) break;
       ok = HYB_WAIT(bars->full_kq[st], (c >> 1) & 1);
       {                                      // lengths: thread r, row r of the stacked [K; Q]
-        const uint8_t* kq = sm + kOffKQ + st * kStageKQ + tid * 128;
-        float ss = 0.f;
+        const uint8_t* kq = sm + kOffKQ + st * kStageKQ + gt * 128;
+        f32x2 s2 = pair(0.f, 0.f);
 #pragma unroll
         for (int ch = 0; ch < 16; ++ch) {
-          const uint4 u = *reinterpret_cast<const uint4*>(kq + (ch >> 3) * kSubKQ + (((ch & 7) ^ (tid & 7)) << 4));
+          const uint4 u = *reinterpret_cast<const uint4*>(kq + (ch >> 3) * kSubKQ + (((ch & 7) ^ (gt & 7)) << 4));
           const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            ss = fmaf(bf16_lo(x[e]), bf16_lo(x[e]), ss);
-            ss = fmaf(bf16_hi(x[e]), bf16_hi(x[e]), ss);
+            const f32x2 y = pair(bf16_lo(x[e]), bf16_hi(x[e]));
+            s2 = fma2(y, y, s2);
           }
         }
+        float ss, s1;
+        unpair(s2, ss, s1);
+        ss += s1;
         const float inv = eps > 0.f ? 1.f / sqrtf(ss + eps) : 1.f;
-        const int t = tid & 63;
-        if (tid < 64) G.rk[t] = t < n ? inv : 0.f;
-        else G.pq[t] = t < n ? scale * inv : 0.f;
+        const int t = gt & 63;
+        if (gt < 64) {
+          const float rk = t < n ? inv : 0.f;
+          G.wB[t] = G.bt[t] * rk;
+          G.cA[t] = G.bt[t] * rk * rk;
+          G.eR[t] = rk * exp2f(G.hi[t]);     // G.lo is below half an ulp of G.hi
+          G.wX[t] = exp2f((G.hi[63] - G.hi[t]) + (G.lo[63] - G.lo[t]));
+          if (t == 63) G.dec = exp2f(G.hi[63]);
+        } else {
+          const float f = t < n ? scale * inv : 0.f;
+          G.pq[t] = f;
+          G.oq[t] = f * exp2f(G.hi[t]);
+        }
       }
-      ok = bar_prep_all(ok);
+      ok = bar_group_all(bar, ok);
       if (!ok) break;
-      if (tid < 64) {
-        const float e = exp2f(G.hi[tid]);    // G.lo is below half an ulp of G.hi
-        G.cA[tid] = G.bt[tid] * G.rk[tid];
-        G.aR[tid] = G.cA[tid] * e;
-        G.oq[tid] = G.pq[tid] * e;
-        G.wX[tid] = G.rk[tid] * exp2f((G.hi[63] - G.hi[tid]) + (G.lo[63] - G.lo[tid]));
-        if (tid == 63) G.dec = e;
-      }
-      bar_prep();
-      mbar_arrive(&bars->gates[st]);
-      ok = HYB_WAIT(bars->d0_ready, c & 1);
+      mbar_arrive(&bars->gates[c & 3]);
+      ok = HYB_WAIT(bars->d0_ready[st], (c >> 1) & 1);
+      if (c >= 2) ok = HYB_WAIT(bars->o_free[st], ((c - 2) >> 1) & 1) && ok;   // W's and P's buffers
       tc_fence_after();
       {
         // warps 0, 1: row t of K K^T -> column t of A^T; warps 2, 3: row t of Q K^T -> row t of P.
         // Rows below 32 have nothing in the columns from 32 on.
-        const int t = tid & 63;
-        const bool is_p = tid >= 64;
+        const int t = gt & 63;
+        const bool is_p = gt >= 64;
+        if (is_p && t < 32) {
+          uint8_t* dst = sm + kOffP + st * 2 * kTile64 + t * 128;
+#pragma unroll
+          for (int ch = 4; ch < 8; ++ch) {
+            *reinterpret_cast<uint4*>(dst + ((ch ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(dst + kTile64 + ((ch ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+        }
         const float ghi = G.hi[t], glo = G.lo[t], f = is_p ? G.pq[t] : G.cA[t];
         const f32x2 neg = pair(-1.f, -1.f), gh2 = pair(ghi, ghi), gl2 = pair(glo, glo), f2 = pair(f, f);
 #pragma unroll 1
@@ -400,14 +474,11 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           for (int e = 0; e < 32; e += 4) {
             const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[part * 32 + e]);
             const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[part * 32 + e]);
-            const float4 r4 = *reinterpret_cast<const float4*>(&G.rk[part * 32 + e]);
             float d[4];
             unpair(add2(fma2(pair(h4.x, h4.y), neg, gh2), fma2(pair(l4.x, l4.y), neg, gl2)), d[0], d[1]);
             unpair(add2(fma2(pair(h4.z, h4.w), neg, gh2), fma2(pair(l4.z, l4.w), neg, gl2)), d[2], d[3]);
-            unpair(mul2(mul2(pair(fast_exp2(d[0]), fast_exp2(d[1])), pair(v[e], v[e + 1])),
-                        mul2(pair(r4.x, r4.y), f2)), v[e], v[e + 1]);
-            unpair(mul2(mul2(pair(fast_exp2(d[2]), fast_exp2(d[3])), pair(v[e + 2], v[e + 3])),
-                        mul2(pair(r4.z, r4.w), f2)), v[e + 2], v[e + 3]);
+            unpair(mul2(mul2(pair(fast_exp2(d[0]), fast_exp2(d[1])), f2), pair(v[e], v[e + 1])), v[e], v[e + 1]);
+            unpair(mul2(mul2(pair(fast_exp2(d[2]), fast_exp2(d[3])), f2), pair(v[e + 2], v[e + 3])), v[e + 2], v[e + 3]);
           }
           if (part == (t >> 5)) {            // at the diagonal: s < t, or s <= t for P
             const int most = lane + (is_p ? 1 : 0);
@@ -433,25 +504,28 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       tc_fence_before();
       mbar_arrive(&bars->d0_free);
-      ok = bar_prep_all(ok);
+      ok = bar_group_all(bar, ok);
       if (!ok) break;
-      // W = (1 + A)^-1 by blocks, 16, 32, 64; A is held transposed, A^T[s][t] at A[s * kLdA + t], W
+      // W = (1 + A)^-1 by blocks of 8, 16, 32, 64. A is held transposed, A^T[s][t] at A[s * kLdA + t], W
       // row-major in its place. Two blocks W00, W11 on the diagonal and A10 below give
-      // W10 = -W11 (A10 W00): the first product goes where W10 will be, A10^T lies in the (zero)
-      // block above it.
-      // 16 x 16, a warp each, a lane a column (lanes 16-31 do the same): once w_m is final it is
-      // taken from every later row (independent fma, one 16-byte broadcast read for four).
+      // W10 = -W11 (A10 W00); the first product goes where W10 will be. What is left of A^T above the
+      // diagonal blocks is never read as W: those products are skipped. The products are warp
+      // MMAs of 16 x 8 x 8 on two tf32 terms (three products, 2^-22): on the CUDA cores their
+      // operands, broadcast from shared memory, took two thirds of its bandwidth.
       {
-        float* D = A + warp * 16 * (kLdA + 1);
-        const int col = lane & 15;
-        float x[16];
+        // 8 x 8: a warp two blocks, a lane a column (lanes 16-31 do the same). Once w_m is final it is
+        // taken from every later row.
+        float* D = A + gw * 16 * (kLdA + 1);
+        float* E = D + ((lane >> 3) & 1) * 8 * (kLdA + 1);
+        const int col = lane & 7;
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
+        for (int i = 0; i < 8; ++i) x[i] = i == col ? 1.f : 0.f;
 #pragma unroll
-        for (int m = 0; m < 15; ++m) {
+        for (int m = 0; m < 7; ++m) {
 #pragma unroll
-          for (int i4 = (m + 1) / 4; i4 < 4; ++i4) {
-            const float4 a = *reinterpret_cast<const float4*>(&D[m * kLdA + i4 * 4]);
+          for (int i4 = (m + 1) / 4; i4 < 2; ++i4) {
+            const float4 a = *reinterpret_cast<const float4*>(&E[m * kLdA + i4 * 4]);
             const float y[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -461,101 +535,91 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         __syncwarp();
         if (lane < 16) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) D[i * kLdA + col] = x[i];
+          for (int i = 0; i < 8; ++i) E[i * kLdA + col] = x[i];
         }
+        __syncwarp();
+        // 16 x 16, this warp's two blocks (rows 8-15 of the products are idle)
+        FragA fa;
+        FragB fb;
+        float y[4] = {}, z[4] = {};
+        fa.load<1, kLdA>(D + 8, lane, true, false);
+        fb.load(D, lane);
+        mma_tf32(y, fa, fb);
+        store_c(D + 8 * kLdA, y, 1.f, lane, false);
+        __syncwarp();
+        fa.load<kLdA, 1>(D + 8 * (kLdA + 1), lane, true, false);
+        fb.load(D + 8 * kLdA, lane);
+        mma_tf32(z, fa, fb);
+        __syncwarp();
+        store_c(D + 8 * kLdA, z, -1.f, lane, false);
       }
-      bar_prep();
-      {                                      // 32 x 32: two warps each, a lane 4 rows of a column
-        float* D = A + (warp >> 1) * 32 * (kLdA + 1);
-        const int col = lane & 15, r0 = 8 * (warp & 1) + 4 * (lane >> 4);
-        f32x2 x0 = pair(0.f, 0.f), x1 = x0;
-#pragma unroll
-        for (int m = 0; m < 16; ++m) {
-          const float b = D[m * kLdA + col];
-          const float4 a = *reinterpret_cast<const float4*>(&D[m * kLdA + 16 + r0]);
-          x0 = fma2(pair(a.x, a.y), pair(b, b), x0);
-          x1 = fma2(pair(a.z, a.w), pair(b, b), x1);
+      bar_group(bar);
+      {                                      // 32 x 32: two warps each, 8 columns a warp
+        float* D = A + (gw >> 1) * 32 * (kLdA + 1);
+        const int j0 = 8 * (gw & 1);
+        FragA fa;
+        FragB fb;
+        float y[4] = {}, z[4] = {};
+        if (j0 == 0) {
+          fa.load<1, kLdA>(D + 16, lane);
+          fb.load(D, lane);
+          mma_tf32(y, fa, fb);
         }
-        float y[4];
-        unpair(x0, y[0], y[1]);
-        unpair(x1, y[2], y[3]);
+        fa.load<1, kLdA>(D + 8 * kLdA + 16, lane);
+        fb.load(D + 8 * kLdA + j0, lane);
+        mma_tf32(y, fa, fb);
+        store_c(D + 16 * kLdA + j0, y, 1.f, lane);
+        bar_group(bar);
+        fa.load<kLdA, 1>(D + 16 * (kLdA + 1), lane);
+        fb.load(D + 16 * kLdA + j0, lane);
+        mma_tf32(z, fa, fb);
+        fa.load<kLdA, 1>(D + 16 * (kLdA + 1) + 8, lane, false);   // rows 0-7 end before column 8
+        fb.load(D + 24 * kLdA + j0, lane);
+        mma_tf32(z, fa, fb);
+        bar_group(bar);
+        store_c(D + 16 * kLdA + j0, z, -1.f, lane);
+      }
+      bar_group(bar);
+      {                                      // 64 x 64: each warp 16 rows by 16 columns
+        const int r0 = 16 * (gw >> 1), j0 = 16 * (gw & 1);
+        FragA fa;
+        FragB fb;
+        float y[2][4] = {}, z[2][4] = {};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) D[(16 + r0 + r) * kLdA + col] = y[r];
-        bar_prep();
-        f32x2 z[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) z[r] = pair(0.f, 0.f);
-#pragma unroll
-        for (int m = 0; m < 16; m += 4) {
-          const f32x2 b0 = pair(D[(16 + m) * kLdA + col], D[(17 + m) * kLdA + col]);
-          const f32x2 b1 = pair(D[(18 + m) * kLdA + col], D[(19 + m) * kLdA + col]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float4 a = *reinterpret_cast<const float4*>(&D[(16 + r0 + r) * kLdA + 16 + m]);
-            z[r] = fma2(pair(a.x, a.y), b0, z[r]);
-            z[r] = fma2(pair(a.z, a.w), b1, z[r]);
+        for (int m = 0; m < 32; m += 8) {
+          if (m < j0) continue;
+          fa.load<1, kLdA>(A + m * kLdA + 32 + r0, lane);
+          fb.load(A + m * kLdA + j0, lane);
+          mma_tf32(y[0], fa, fb);
+          if (m > j0) {
+            fb.load(A + m * kLdA + j0 + 8, lane);
+            mma_tf32(y[1], fa, fb);
           }
         }
-        bar_prep();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float a, b;
-          unpair(z[r], a, b);
-          D[(16 + r0 + r) * kLdA + col] = -(a + b);
-          D[(r0 + r) * kLdA + 16 + col] = 0.f;
-        }
-      }
-      bar_prep();
-      {                                      // 64 x 64: each warp 8 rows, a lane a column
-        f32x2 x[4];
+        for (int i = 0; i < 2; ++i) store_c(A + (32 + r0) * kLdA + j0 + 8 * i, y[i], 1.f, lane);
+        bar_group(bar);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = pair(0.f, 0.f);
-#pragma unroll 8
-        for (int m = 0; m < 32; ++m) {
-          const float b = A[m * kLdA + lane];
-          const float4 a0 = *reinterpret_cast<const float4*>(&A[m * kLdA + 32 + 8 * warp]);
-          const float4 a1 = *reinterpret_cast<const float4*>(&A[m * kLdA + 36 + 8 * warp]);
-          const f32x2 b2 = pair(b, b);
-          x[0] = fma2(pair(a0.x, a0.y), b2, x[0]);
-          x[1] = fma2(pair(a0.z, a0.w), b2, x[1]);
-          x[2] = fma2(pair(a1.x, a1.y), b2, x[2]);
-          x[3] = fma2(pair(a1.z, a1.w), b2, x[3]);
-        }
+        for (int m = 0; m < 32; m += 8) {
+          if (m > r0 + 8) continue;
+          fa.load<kLdA, 1>(A + (32 + r0) * kLdA + 32 + m, lane, m <= r0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float a, b;
-          unpair(x[r], a, b);
-          A[(32 + 8 * warp + 2 * r) * kLdA + lane] = a;
-          A[(33 + 8 * warp + 2 * r) * kLdA + lane] = b;
-        }
-        bar_prep();
-        f32x2 z[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) z[r] = pair(0.f, 0.f);
-#pragma unroll 4
-        for (int m = 0; m < 32; m += 4) {
-          const f32x2 b0 = pair(A[(32 + m) * kLdA + lane], A[(33 + m) * kLdA + lane]);
-          const f32x2 b1 = pair(A[(34 + m) * kLdA + lane], A[(35 + m) * kLdA + lane]);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const float4 a = *reinterpret_cast<const float4*>(&A[(32 + 8 * warp + r) * kLdA + 32 + m]);
-            z[r] = fma2(pair(a.x, a.y), b0, z[r]);
-            z[r] = fma2(pair(a.z, a.w), b1, z[r]);
+          for (int i = 0; i < 2; ++i) {
+            fb.load(A + (32 + m) * kLdA + j0 + 8 * i, lane);
+            mma_tf32(z[i], fa, fb);
           }
         }
-        // not back into its place, where others still read: over A10^T (rows r, columns 32-63)
+        // not back into its place, where others still read: over A21^T (rows r, columns 32-63)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          float a, b;
-          unpair(z[r], a, b);
-          A[(8 * warp + r) * kLdA + 32 + lane] = -(a + b);
-        }
+        for (int i = 0; i < 2; ++i) store_c(A + r0 * kLdA + 32 + j0 + 8 * i, z[i], -1.f, lane);
       }
-      bar_prep();
-      // W as three bf16 terms: row t, half of its columns (the upper right block is zero from the start)
-      if (tid >= 64 || (tid & 1) == 0) {
-        const int t = tid >> 1, half = tid & 1;
-        const float* src = t < 32 ? A + t * kLdA : A + (half ? t * kLdA + 32 : (t - 32) * kLdA + 32);
+      bar_group(bar);
+      // W's columns times beta / |k|, as three bf16 terms: a warp 32 rows of one half of the columns
+      // (the upper right block is zero from the start)
+      if (gw != 1) {
+        const int half = gw & 1, t = 32 * (gw >> 1) + lane;
+        const float* src = A + (half == (gw >> 1) ? t * kLdA + 32 * half : lane * kLdA + 32);
+        const bool diag = half == (gw >> 1);
         uint8_t* dst = sm + kOffW + st * 3 * kTile64 + t * 128;
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
@@ -563,7 +627,12 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
           for (int e = 0; e < 8; e += 4) {
             const float4 u = *reinterpret_cast<const float4*>(src + ch * 8 + e);
-            v[e] = u.x; v[e + 1] = u.y; v[e + 2] = u.z; v[e + 3] = u.w;
+            const float4 f = *reinterpret_cast<const float4*>(&G.wB[half * 32 + ch * 8 + e]);
+            v[e] = u.x * f.x; v[e + 1] = u.y * f.y; v[e + 2] = u.z * f.z; v[e + 3] = u.w * f.w;
+          }
+          if (diag && ch > (lane >> 3)) {    // above the diagonal blocks
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
           }
           uint32_t h[4], m[4], l[4];
 #pragma unroll
@@ -583,16 +652,42 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     const int half = (warp - kWarpMain) >> 2;
     const int j = (warp & 3) * 32 + lane;    // value column: TMEM lane of this thread
     const int x0 = half * 32, i0 = half * 64;
-    for (int c = 0;; ++c) {
-      const int st = c & 1;
-      const Gates& G = gates[st];
-      ok = HYB_WAIT(bars->info[st], (c >> 1) & 1);
-      if (!ok) break;
-      const Chunk& ch = chunks[c & 3];
-      const int n = ch.n, flags = ch.flags;
-      if (n == 0) break;
-      ok = HYB_WAIT(bars->gates[st], (c >> 1) & 1);
-      if (!ok) break;
+    // Rows in two pieces of 16 (the lower half of the rows starts with its second, see R below).
+    const int xa = x0 + (half ? 0 : 16), xb = x0 + (half ? 16 : 0);
+    int n = 0, flags = 0;
+    uint32_t v[16];                          // pairs of rows of V, this column
+    // Chunk c's description, gates and V: fetched while the chunk before is under way.
+    auto fetch = [&](int c) -> bool {
+      if (!HYB_WAIT(bars->info[c & 3], (c >> 2) & 1)) return false;
+      n = chunks[c & 3].n;
+      flags = chunks[c & 3].flags;
+      if (n == 0) return true;
+      if (!HYB_WAIT(bars->full_v[c & 1], (c >> 1) & 1)) return false;
+      const uint8_t* vs = sm + kOffV + (c & 1) * kStageV + (j >> 6) * kSubV + (j & 7) * 2;
+      const int cj = (j & 63) >> 3;
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const uint8_t* r = vs + ((e < 16 ? xa : xb - 16) + e) * 128;   // pieces start at rows of 8
+        const uint32_t lo = *reinterpret_cast<const uint16_t*>(r + ((cj ^ (e & 7)) << 4));
+        const uint32_t hi = *reinterpret_cast<const uint16_t*>(r + 128 + ((cj ^ ((e + 1) & 7)) << 4));
+        v[e / 2] = __byte_perm(lo, hi, 0x5410);
+      }
+      if (n < kC) {                          // rows past the request may hold anything
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const int t = (e < 16 ? xa : xb - 16) + e;
+          if (t >= n) v[e / 2] = 0;
+          else if (t + 1 >= n) v[e / 2] &= 0xffffu;
+        }
+      }
+      mbar_arrive(&bars->free_v[c & 1]);
+      return HYB_WAIT(bars->gates[c & 3], (c >> 2) & 1);
+    };
+    ok = fetch(0);
+    for (int c = 0; ok && n > 0; ++c) {
+      const Gates& G = gates[c & 3];
+      float* const S = chunks[c & 3].S;
+      const bool last = flags & kLast, hand = flags & kHand;
       // this chunk's first state: the run's from the pool, or what the last chunk left in TMEM
       if (flags & kFirst) {
         if (flags & kTake) {
@@ -606,7 +701,6 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
             __nanosleep(100);
           }
         }
-        const float* S = ch.S;
 #pragma unroll 1
         for (int i = i0; i < i0 + 64; i += 16) {
           float v[16];
@@ -617,7 +711,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         }
       } else {
         const float dec = G.dec;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = i0; i < i0 + 64; i += 16) {
           float s[16];
           tmem_ld16(tl + kColS + i, s);
@@ -628,42 +722,26 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->sa_ready);
-      // V of this column while (k) runs; rows past the request may hold anything
-      ok = HYB_WAIT(bars->full_v[st], (c >> 1) & 1);
-      if (!ok) break;
-      float v[32];
-      {
-        const uint8_t* vs = sm + kOffV + st * kStageV + (j >> 6) * kSubV + (j & 7) * 2;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int t = x0 + e;
-          const uint16_t b = *reinterpret_cast<const uint16_t*>(vs + t * 128 + ((((j & 63) >> 3) ^ (t & 7)) << 4));
-          v[e] = t < n ? __uint_as_float((uint32_t)b << 16) : 0.f;
-        }
-      }
-      mbar_arrive(&bars->free_v[st]);
-      // R = beta (V - e^G K S)
+      // R = V - e^G K S (beta is in W)
       ok = HYB_WAIT(bars->d1k_ready, c & 1);
       if (!ok) break;
       tc_fence_after();
-      {
-        float d[32];                         // all read before R's l goes into the same columns
-        tmem_ld32(tl + kCol1K + x0, d);
+      // R's l goes to columns 16-47 of D1K: the thread's own 16 first rows of d may lie there, so the
+      // piece that lies apart from them is read second
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t0 = x ? xb : xa;
+        float d[16];
+        tmem_ld16(tl + kCol1K + t0, d);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 b = *reinterpret_cast<const float4*>(&G.bt[x0 + e]);
-          const float4 a = *reinterpret_cast<const float4*>(&G.aR[x0 + e]);
-          d[e] = fmaf(-a.x, d[e], b.x * v[e]);
-          d[e + 1] = fmaf(-a.y, d[e + 1], b.y * v[e + 1]);
-          d[e + 2] = fmaf(-a.z, d[e + 2], b.z * v[e + 2]);
-          d[e + 3] = fmaf(-a.w, d[e + 3], b.w * v[e + 3]);
+        for (int e = 0; e < 16; e += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(&G.eR[t0 + e]);
+          const uint32_t v0 = v[x * 8 + e / 2], v1 = v[x * 8 + e / 2 + 1];
+          unpair(fma2(pair(-a.x, -a.y), pair(d[e], d[e + 1]), pair(bf16_lo(v0), bf16_hi(v0))), d[e], d[e + 1]);
+          unpair(fma2(pair(-a.z, -a.w), pair(d[e + 2], d[e + 3]), pair(bf16_lo(v1), bf16_hi(v1))), d[e + 2], d[e + 3]);
         }
-#pragma unroll
-        for (int x = 0; x < 32; x += 16) {
-          const int at = (x0 + x) / 2;
-          put_terms(tl + kColRh + at, tl + kColRm + at, tl + kColRl + at, d + x);
-        }
+        put_terms(tl + kColRh + t0 / 2, tl + kColRm + t0 / 2, tl + kColRl + t0 / 2, d);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -686,22 +764,21 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
           const float4 a = *reinterpret_cast<const float4*>(&G.wX[x0 + x + e]);
-          d[e] *= a.x;
-          d[e + 1] *= a.y;
-          d[e + 2] *= a.z;
-          d[e + 3] *= a.w;
+          unpair(mul2(pair(a.x, a.y), pair(d[e], d[e + 1])), d[e], d[e + 1]);
+          unpair(mul2(pair(a.z, a.w), pair(d[e + 2], d[e + 3])), d[e + 2], d[e + 3]);
         }
         put_terms(tl + kColXh + at, tl + kColXm + at, tl + kColXl + at, d);
       }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->xa_ready);
+      ok = fetch(c + 1);
+      if (!ok) break;
       // the chunk's last state
       ok = HYB_WAIT(bars->s_ready, c & 1);
       if (!ok) break;
       tc_fence_after();
-      if (flags & kLast) {                   // end of a run: to the pool, and handed over if cut
-        float* S = ch.S;
+      if (last) {                            // end of a run: to the pool, and handed over if cut
 #pragma unroll 1
         for (int i = i0; i < i0 + 64; i += 16) {
           float s[16];
@@ -710,7 +787,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
           for (int e = 0; e < 16; ++e) S[(i + e) * kD + j] = s[e];
         }
-        if (flags & kHand) {                 // at most once per CTA (its first run)
+        if (hand) {                          // at most once per CTA (its first run)
           __threadfence();
           mbar_arrive(&bars->published);
           if (tid == kWarpMain * 32) {
@@ -723,45 +800,65 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     if (!ok && lane == 0) flag(status, HYB_DEVERR_TIMEOUT);
   } else if (warp < kWarpFeed) {
     // ------------------------------------------------------------ outputs
-    const int j = (warp & 3) * 32 + lane;
+    const int j = (warp & 3) * 32 + lane, ot = tid - kWarpOut * 32;
     for (int c = 0;; ++c) {
       const int st = c & 1;
-      const Gates& G = gates[st];
-      ok = HYB_WAIT(bars->info[st], (c >> 1) & 1);
+      const Gates& G = gates[c & 3];
+      ok = bar_group_all(3, HYB_WAIT(bars->info[c & 3], (c >> 2) & 1));
       if (!ok) break;
       const int n = chunks[c & 3].n;
       if (n == 0) break;
-      __nv_bfloat16* dst = out + ((int64_t)chunks[c & 3].row * in.H + chunks[c & 3].h) * kD + j;
-      ok = HYB_WAIT(bars->gates[st], (c >> 1) & 1);
-      if (!ok) break;
-      ok = HYB_WAIT(bars->d1q_ready, c & 1);
-      if (!ok) break;
+      const int row = chunks[c & 3].row, h = chunks[c & 3].h;
+      ok = HYB_WAIT(bars->gates[c & 3], (c >> 2) & 1) && HYB_WAIT(bars->d1q_ready, c & 1);
       tc_fence_after();
-      float o[64];
+      // Q S times scale e^G / |q|, in place; (o) adds to it
+#pragma unroll 1
+      for (int x = 0; x < 64; x += 16) {
+        float d[16];
+        tmem_ld16(tl + kCol1Q + x, d);
+        tmem_ld_wait();
 #pragma unroll
-      for (int x = 0; x < 64; x += 16) tmem_ld16(tl + kCol1Q + x, o + x);
-      tmem_ld_wait();
+        for (int e = 0; e < 16; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&G.oq[x + e]);
+          unpair(mul2(pair(f.x, f.y), pair(d[e], d[e + 1])), d[e], d[e + 1]);
+          unpair(mul2(pair(f.z, f.w), pair(d[e + 2], d[e + 3])), d[e + 2], d[e + 3]);
+        }
+        tmem_st16(tl + kCol1Q + x, d);
+      }
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bars->q_read);
-#pragma unroll
-      for (int t = 0; t < 64; ++t) o[t] *= G.oq[t];
-      ok = HYB_WAIT(bars->o_ready, c & 1);
+      mbar_arrive(&bars->q_scaled);
+      ok = bar_group_all(3, ok && HYB_WAIT(bars->o_ready, c & 1));
       if (!ok) break;
       tc_fence_after();
+      // rows of 256 bytes in the place of P, which (o) has used up, and from there to global memory
+      uint8_t* rows = sm + kOffP + st * 2 * kTile64;
 #pragma unroll
       for (int x = 0; x < 64; x += 16) {
         float d[16];
         tmem_ld16(tl + kCol1Q + x, d);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[x + e] += d[e];
+        for (int e = 0; e < 16; e += 2) {
+          const uint32_t y = pack_bf16(d[e], d[e + 1]);
+          *reinterpret_cast<uint16_t*>(rows + (x + e) * 256 + j * 2) = (uint16_t)y;
+          *reinterpret_cast<uint16_t*>(rows + (x + e + 1) * 256 + j * 2) = (uint16_t)(y >> 16);
+        }
       }
       tc_fence_before();
+      mbar_arrive(&bars->d1q_free);
+      fence_async_smem();
+      bar_group(3);
+      // a whole chunk in one store; of the last, partial one only the request's rows, one by one
+      if (n == kC ? ot == 0 : ot < n) {
+        if (n == kC) tma_store_3d(&to, rows, 0, h, row);
+        else bulk_row(out + ((int64_t)(row + ot) * in.H + h) * kD, rows + ot * 256);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      }
       mbar_arrive(&bars->o_free[st]);
-#pragma unroll
-      for (int t = 0; t < 64; ++t)
-        if (t < n) dst[(int64_t)t * in.H * kD] = __float2bfloat16_rn(o[t]);
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) flag(status, HYB_DEVERR_TIMEOUT);
   } else if (warp == kWarpFeed) {
     // ------------------------------------------------------------ chunks, loads, gates
@@ -771,7 +868,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       tma_prefetch_desc(&tv);
     }
     Walk w;
-    bool more = first_chunk(in, plan_sh, w);
+    bool more = first_chunk(in, plan_sh, w), ended = false;
     int ckq = 0, cv = 0;                     // chunks requested
     for (int c = 0;; ++c) {
       const int st = c & 1, row = w.sg.t0 + w.ci * kC;
@@ -780,40 +877,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       const int64_t at = (int64_t)row * in.H + w.sg.h + (int64_t)lane * in.H, at2 = at + 32ll * in.H;
       const float ga = lane < n ? g[at] : 0.f, gb = lane + 32 < n ? g[at2] : 0.f;
       const float ba = lane < n ? beta[at] : 0.f, bb = lane + 32 < n ? beta[at2] : 0.f;
-      if (n > 0) {
-        if (c >= 2) ok = HYB_WAIT(bars->free_kq[st], ((c - 2) >> 1) & 1);
-        if (!ok) break;
-        const int hk = w.sg.h / rep;
-        if (lane == 0) {
-          uint8_t* kq = sm + kOffKQ + st * kStageKQ;
-          mbar_expect_tx(&bars->full_kq[st], kStageKQ);
-          for (int sb = 0; sb < 2; ++sb) {
-            tma_load_3d(kq + sb * kSubKQ, &tk, sb * 64, hk, row, &bars->full_kq[st]);
-            tma_load_3d(kq + sb * kSubKQ + 64 * 128, &tq, sb * 64, hk, row, &bars->full_kq[st]);
-          }
-        }
-        ckq = c + 1;
-        if (c >= 2) ok = HYB_WAIT(bars->free_v[st], ((c - 2) >> 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          uint8_t* vs = sm + kOffV + st * kStageV;
-          mbar_expect_tx(&bars->full_v[st], kStageV);
-          for (int sb = 0; sb < 2; ++sb)
-            tma_load_3d(vs + sb * kSubV, &tv, sb * 64, w.sg.h, row, &bars->full_v[st]);
-        }
-        cv = c + 1;
-      }
-      // the buffers' last users are done (a slot of `chunks` is used two chunks longer)
-      if (c >= 2) ok = HYB_WAIT(bars->o_free[st], ((c - 2) >> 1) & 1);
-      if (!ok) break;
-      if (lane == 0) {
-        const int flags = (w.ci == w.sg.c0 ? kFirst | (w.sg.zero_start ? kZero : 0) | (w.sg.wait_handoff ? kTake : 0) : 0) |
-                          (w.ci == w.sg.c1 - 1 ? kLast | (w.sg.publish ? kHand : 0) : 0);
-        chunks[c & 3] = Chunk{w.sg.S, row, n, w.sg.h, flags, {0, 0}};
-      }
       // running sum in units of log 2, exact in integer steps of 2^-36 (fp32 would lose the
       // small gates behind large ones, and fp64 is slow on this GPU)
-      Gates& G = gates[st];
       long long a = to_fixed(ga), b = to_fixed(gb);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -824,13 +889,50 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       b += __shfl_sync(0xffffffffu, a, 31);
       const unsigned na = __ballot_sync(0xffffffffu, ga != ga), nb = __ballot_sync(0xffffffffu, gb != gb);
       const unsigned upto = 0xffffffffu >> (31 - lane);
-      from_fixed(a, (na & upto) != 0, G.hi[lane], G.lo[lane]);
-      from_fixed(b, na != 0 || (nb & upto) != 0, G.hi[lane + 32], G.lo[lane + 32]);
+      float h0, l0, h1, l1;
+      from_fixed(a, (na & upto) != 0, h0, l0);
+      from_fixed(b, na != 0 || (nb & upto) != 0, h1, l1);
+      if (c >= 2) ok = HYB_WAIT(bars->free_kq[st], ((c - 2) >> 1) & 1);
+      if (!ok) break;
+      Gates& G = gates[c & 3];
+      G.hi[lane] = h0;
+      G.lo[lane] = l0;
+      G.hi[lane + 32] = h1;
+      G.lo[lane + 32] = l1;
       G.bt[lane] = ba;
       G.bt[lane + 32] = bb;
-      mbar_arrive(&bars->info[st]);
-      if (n == 0) break;
-      more = next_chunk(in, plan_sh, w);
+      if (lane == 0) {
+        const int flags = (w.ci == w.sg.c0 ? kFirst | (w.sg.zero_start ? kZero : 0) | (w.sg.wait_handoff ? kTake : 0) : 0) |
+                          (w.ci == w.sg.c1 - 1 ? kLast | (w.sg.publish ? kHand : 0) : 0);
+        chunks[c & 3] = Chunk{w.sg.S, row, n, w.sg.h, flags, {0, 0}};
+      }
+      if (n > 0) {
+        const int hk = w.sg.h / rep;
+        if (lane == 0) {
+          uint8_t* kq = sm + kOffKQ + st * kStageKQ;
+          mbar_expect_tx(&bars->full_kq[st], kStageKQ);
+          for (int sb = 0; sb < 2; ++sb) {
+            tma_load_3d(kq + sb * kSubKQ, &tk, sb * 64, hk, row, &bars->full_kq[st]);
+            tma_load_3d(kq + sb * kSubKQ + 64 * 128, &tq, sb * 64, hk, row, &bars->full_kq[st]);
+          }
+        }
+        ckq = c + 1;
+      }
+      mbar_arrive(&bars->info[c & 3]);
+      if (n > 0) {
+        if (c >= 2) ok = HYB_WAIT(bars->free_v[st], ((c - 2) >> 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          uint8_t* vs = sm + kOffV + st * kStageV;
+          mbar_expect_tx(&bars->full_v[st], kStageV);
+          for (int sb = 0; sb < 2; ++sb)
+            tma_load_3d(vs + sb * kSubV, &tv, sb * 64, w.sg.h, row, &bars->full_v[st]);
+        }
+        cv = c + 1;
+      }
+      if (n > 0) more = next_chunk(in, plan_sh, w);
+      else if (ended) break;               // two end marks: each preparing group gets one
+      else ended = true;
     }
     if (!ok && lane == 0) {                  // let the loads in flight land before exiting
       flag(status, HYB_DEVERR_TIMEOUT);
@@ -844,9 +946,9 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     const uint64_t mn0 = sw128_desc(sm0, kSubKQ, 1024);        // K as [t][i], i-major: two 64-wide blocks
     bool more = true;
     // (0) of chunk cn, if there is one: rows past the request become zero rows of K first
-    auto issue0 = [&](int cn) {
+    auto issue0 = [&](int cn) -> bool {
       const int st = cn & 1;
-      if (!HYB_WAIT(bars->info[st], (cn >> 1) & 1)) return false;
+      if (!HYB_WAIT(bars->info[cn & 3], (cn >> 2) & 1)) return false;
       const int n = chunks[cn & 3].n;
       more = n > 0;
       if (!more) return true;
@@ -868,7 +970,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           const uint64_t d = desc_add(km0, kq + (k >> 2) * kSubKQ + (k & 3) * 32);
           tc_mma(tmem + kCol0, d, d, kIdesc64, k > 0);
         }
-        tc_commit(&bars->d0_ready);
+        tc_commit(&bars->d0_ready[st]);
       }
       __syncwarp();
       return true;
@@ -889,7 +991,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         tc_commit(&bars->d1k_ready);
       }
       __syncwarp();
-      if (c >= 1) ok = HYB_WAIT(bars->o_free[st ^ 1], ((c - 1) >> 1) & 1);
+      if (c >= 1) ok = HYB_WAIT(bars->d1q_free, (c - 1) & 1);
       if (!ok) break;
       if (elect_one()) {
         tc_fence_after();
@@ -933,7 +1035,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         tc_commit(&bars->free_kq[st]);       // the last use of K and Q
       }
       __syncwarp();
-      ok = HYB_WAIT(bars->q_read, c & 1);
+      ok = HYB_WAIT(bars->q_scaled, c & 1);
       if (!ok) break;
       if (elect_one()) {
         tc_fence_after();
@@ -942,7 +1044,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         for (int x = 0; x < 3; ++x) {        // (o): X h P h, h m, m h
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_ta(tmem + kCol1Q, tmem + (x == 2 ? kColOm : kColOh) + k * 8, desc_add(pd, (x == 1 ? kTile64 : 0) + k * 32), kIdesc64, x + k > 0);
+            tc_mma_ta(tmem + kCol1Q, tmem + (x == 2 ? kColOm : kColOh) + k * 8, desc_add(pd, (x == 1 ? kTile64 : 0) + k * 32), kIdesc64, 1);
         }
         tc_commit(&bars->o_ready);
       }
@@ -976,15 +1078,16 @@ cudaError_t launch_delta_prefill_tc(void* out, const void* q, const void* k, con
                                     const hyb_delta_dims_t* d, int64_t qs, int64_t ks, int64_t vs,
                                     void* ws, unsigned* status, cudaStream_t s) {
   const int Hv = d->num_v_heads, Hk = d->num_qk_heads;
-  CUtensorMap mq, mk, mv;
-  const uint32_t box[3] = {64, 1, 64};
+  CUtensorMap mq, mk, mv, mo;
   const uint64_t rows = T > 0 ? T : 1;
-  auto encode = [&](CUtensorMap* m, const void* base, int heads, int64_t stride) {
+  auto encode = [&](CUtensorMap* m, const void* base, int heads, int64_t stride, bool store = false) {
     const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)heads, rows};
     const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)stride * 2};
-    return encode_tmap_bf16(m, base, 3, dims, strides, box);
+    const uint32_t box[3] = {store ? 128u : 64u, 1, kC};
+    return encode_tmap_bf16(m, base, 3, dims, strides, box, !store);
   };
-  if (!encode(&mq, q, Hk, qs) || !encode(&mk, k, Hk, ks) || !encode(&mv, v, Hv, vs))
+  if (!encode(&mq, q, Hk, qs) || !encode(&mk, k, Hk, ks) || !encode(&mv, v, Hv, vs) ||
+      !encode(&mo, out, Hv, (int64_t)Hv * kD, true))
     return cudaErrorInvalidValue;
   cudaError_t e = set_smem((const void*)delta_prefill_tc_kernel, kSmem);
   if (e != cudaSuccess) return e;
@@ -1009,7 +1112,7 @@ cudaError_t launch_delta_prefill_tc(void* out, const void* q, const void* k, con
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const In in{cu, slots, reset, pool, NS, T, max_len, Hv};
-  e = cudaLaunchKernelEx(&cfg, delta_prefill_tc_kernel, mq, mk, mv, static_cast<__nv_bfloat16*>(out),
+  e = cudaLaunchKernelEx(&cfg, delta_prefill_tc_kernel, mq, mk, mv, mo, static_cast<__nv_bfloat16*>(out),
                          g, beta, in, B, Hv / Hk, d->scale, d->qk_norm_eps,
                          static_cast<unsigned long long*>(ws), cut_chains, status);
   count_launch();

@@ -21,9 +21,10 @@ namespace hyb {
 
 // ---------------------------------------------------------------- host: tensor maps
 // Encodes a tiled bf16 tensor map with 128-byte swizzle (rank 2 or 3). dims/box are
-// innermost first; strides are in bytes for dims 1.. . Returns false on failure.
+// innermost first; strides are in bytes for dims 1.. . Returns false on failure. swizzle = false:
+// the box lies in shared memory as plain rows.
 bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                      const uint64_t* strides_bytes, const uint32_t* box);
+                      const uint64_t* strides_bytes, const uint32_t* box, bool swizzle = true);
 
 #ifdef __CUDACC__
 // ---------------------------------------------------------------- device: descriptors
@@ -206,6 +207,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+// shared -> global; a commit and a wait of the issuing thread's bulk group complete it
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
