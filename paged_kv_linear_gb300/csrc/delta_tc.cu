@@ -416,7 +416,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       {                                      // lengths: thread r, row r of the stacked [K; Q]
         const uint8_t* kq = sm + kOffKQ + st * kStageKQ + gt * 128;
         f32x2 s2 = pair(0.f, 0.f);
-#pragma unroll
+#pragma unroll 4
         for (int ch = 0; ch < 16; ++ch) {
           const uint4 u = *reinterpret_cast<const uint4*>(kq + (ch >> 3) * kSubKQ + (((ch & 7) ^ (gt & 7)) << 4));
           const uint32_t x[4] = {u.x, u.y, u.z, u.w};
@@ -466,36 +466,36 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         const float ghi = G.hi[t], glo = G.lo[t], f = is_p ? G.pq[t] : G.cA[t];
         const f32x2 neg = pair(-1.f, -1.f), gh2 = pair(ghi, ghi), gl2 = pair(glo, glo), f2 = pair(f, f);
 #pragma unroll 1
-        for (int part = 0; part <= (t >> 5); ++part) {
-          float v[32];
-          tmem_ld32(tl + kCol0 + part * 32, v);
+        for (int s0 = 0; s0 <= (t & 32) + 16; s0 += 16) {
+          float v[16];
+          tmem_ld16(tl + kCol0 + s0, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[part * 32 + e]);
-            const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[part * 32 + e]);
+          for (int e = 0; e < 16; e += 4) {
+            const float4 h4 = *reinterpret_cast<const float4*>(&G.hi[s0 + e]);
+            const float4 l4 = *reinterpret_cast<const float4*>(&G.lo[s0 + e]);
             float d[4];
             unpair(add2(fma2(pair(h4.x, h4.y), neg, gh2), fma2(pair(l4.x, l4.y), neg, gl2)), d[0], d[1]);
             unpair(add2(fma2(pair(h4.z, h4.w), neg, gh2), fma2(pair(l4.z, l4.w), neg, gl2)), d[2], d[3]);
             unpair(mul2(mul2(pair(fast_exp2(d[0]), fast_exp2(d[1])), f2), pair(v[e], v[e + 1])), v[e], v[e + 1]);
             unpair(mul2(mul2(pair(fast_exp2(d[2]), fast_exp2(d[3])), f2), pair(v[e + 2], v[e + 3])), v[e + 2], v[e + 3]);
           }
-          if (part == (t >> 5)) {            // at the diagonal: s < t, or s <= t for P
-            const int most = lane + (is_p ? 1 : 0);
+          if (s0 >= (t & 32)) {              // at the diagonal: s < t, or s <= t for P
+            const int most = t - s0 + (is_p ? 1 : 0);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = e < most ? v[e] : 0.f;
+            for (int e = 0; e < 16; ++e) v[e] = e < most ? v[e] : 0.f;
           }
           if (!is_p) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) A[(part * 32 + e) * kLdA + t] = v[e];
+            for (int e = 0; e < 16; ++e) A[(s0 + e) * kLdA + t] = v[e];
           } else {
             uint8_t* dst = sm + kOffP + st * 2 * kTile64 + t * 128;
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
+            for (int ch = 0; ch < 2; ++ch) {
               uint32_t h[4], m[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) split2(v[ch * 8 + 2 * e], v[ch * 8 + 2 * e + 1], h[e], m[e]);
-              const int off = ((part * 4 + ch) ^ (t & 7)) << 4;
+              const int off = ((s0 / 8 + ch) ^ (t & 7)) << 4;
               *reinterpret_cast<uint4*>(dst + off) = make_uint4(h[0], h[1], h[2], h[3]);
               *reinterpret_cast<uint4*>(dst + kTile64 + off) = make_uint4(m[0], m[1], m[2], m[3]);
             }
@@ -585,9 +585,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         FragA fa;
         FragB fb;
         float y[2][4] = {}, z[2][4] = {};
-#pragma unroll
-        for (int m = 0; m < 32; m += 8) {
-          if (m < j0) continue;
+#pragma unroll 1
+        for (int m = j0; m < 32; m += 8) {
           fa.load<1, kLdA>(A + m * kLdA + 32 + r0, lane);
           fb.load(A + m * kLdA + j0, lane);
           mma_tf32(y[0], fa, fb);
@@ -599,9 +598,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
         for (int i = 0; i < 2; ++i) store_c(A + (32 + r0) * kLdA + j0 + 8 * i, y[i], 1.f, lane);
         bar_group(bar);
-#pragma unroll
-        for (int m = 0; m < 32; m += 8) {
-          if (m > r0 + 8) continue;
+#pragma unroll 1
+        for (int m = 0; m <= r0 + 8; m += 8) {
           fa.load<kLdA, 1>(A + (32 + r0) * kLdA + 32 + m, lane, m <= r0);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -621,7 +619,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         const float* src = A + (half == (gw >> 1) ? t * kLdA + 32 * half : lane * kLdA + 32);
         const bool diag = half == (gw >> 1);
         uint8_t* dst = sm + kOffW + st * 3 * kTile64 + t * 128;
-#pragma unroll
+#pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           float v[8];
 #pragma unroll
@@ -750,7 +748,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       ok = HYB_WAIT(bars->x_ready, c & 1);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < 32; x += 16) {
         float d[16];
         tmem_ld16(tl + kColX + x0 + x, d);
@@ -833,7 +831,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       tc_fence_after();
       // rows of 256 bytes in the place of P, which (o) has used up, and from there to global memory
       uint8_t* rows = sm + kOffP + st * 2 * kTile64;
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < 64; x += 16) {
         float d[16];
         tmem_ld16(tl + kCol1Q + x, d);
