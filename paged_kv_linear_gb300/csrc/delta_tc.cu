@@ -52,9 +52,10 @@ constexpr int kSubV = 64 * 128;
 constexpr int kStageV = 2 * kSubV;
 constexpr int kTile64 = 64 * 128;              // [64][64] bf16
 constexpr int kOffKQ = 0;
-constexpr int kOffV = kOffKQ + 2 * kStageKQ;
-constexpr int kOffW = kOffV + 2 * kStageV;     // [buffer][term]
-constexpr int kOffP = kOffW + 2 * 3 * kTile64;
+constexpr int kNKQ = 3;                        // stages of K and Q; one of V
+constexpr int kOffV = kOffKQ + kNKQ * kStageKQ;
+constexpr int kOffW = kOffV + kStageV;         // [term]
+constexpr int kOffP = kOffW + 3 * kTile64;     // [buffer][term]
 constexpr int kOffA = kOffP + 2 * 2 * kTile64; // [group] the system, fp32, then its inverse
 constexpr int kLdA = 72;                       // floats per row: fragments of 4 x 8 hit 32 banks
 constexpr int kOffG = kOffA + 2 * kC * kLdA * 4;
@@ -67,7 +68,7 @@ struct Gates {                                 // factors of a chunk's rows
   float dec, pad[3];                           // e^(G_C)
 };
 // What the warps need to know of a chunk. The feeding warp walks the CTA's runs and writes these,
-// four chunks deep as the gates: chunk c's place is free once (s) of chunk c - 2 is done, which
+// four chunks deep as the gates: chunk c's place is free once (s) of chunk c - 3 is done, which
 // implies that everybody has left chunk c - 4. n = 0 ends them.
 struct Chunk {
   float* S;                                    // the chain's state in the pool
@@ -80,10 +81,11 @@ constexpr int kOffChunk = kOffG + 4 * (int)sizeof(Gates);
 constexpr int kOffBar = kOffChunk + 4 * (int)sizeof(Chunk);
 
 struct Bars {
-  uint64_t full_kq[2], full_v[2], free_kq[2], free_v[2];
+  uint64_t full_kq[kNKQ], free_kq[kNKQ], full_v, free_v;
   uint64_t info[4], gates[4];                  // their readers may lag by more than a chunk
   uint64_t w_ready[2], o_free[2];
-  uint64_t d0_ready[2], d0_free, sa_ready, d1k_ready, d1q_ready, ra_ready, x_ready, xa_ready, s_ready;
+  uint64_t sa_ready[2], ra_ready[2], xa_ready[2];   // an operand's first and second half
+  uint64_t d0_ready[2], d0_free, d1k_ready, d1q_ready, x_ready, s_ready;
   uint64_t q_scaled, o_ready, d1q_free, published, drain;
 };
 constexpr int kSmem = kOffBar + 512 + 1024;    // + slack for 1024-byte alignment
@@ -361,26 +363,28 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
   fence_async_smem();
   if (warp == kWarpMma) {
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kNKQ; ++i) {
         mbar_init(&bars->full_kq[i], 1);
-        mbar_init(&bars->full_v[i], 1);
         mbar_init(&bars->free_kq[i], 1);
-        mbar_init(&bars->free_v[i], 256);
-        mbar_init(&bars->w_ready[i], 128);
-        mbar_init(&bars->o_free[i], 128);
-        mbar_init(&bars->d0_ready[i], 1);
       }
+      mbar_init(&bars->full_v, 1);
+      mbar_init(&bars->free_v, 256);
       for (int i = 0; i < 4; ++i) {
         mbar_init(&bars->info[i], 32);
         mbar_init(&bars->gates[i], 128);
       }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars->w_ready[i], 128);
+        mbar_init(&bars->o_free[i], 128);
+        mbar_init(&bars->sa_ready[i], 256);
+        mbar_init(&bars->ra_ready[i], 256);
+        mbar_init(&bars->xa_ready[i], 256);
+        mbar_init(&bars->d0_ready[i], 1);
+      }
       mbar_init(&bars->d0_free, 128);
-      mbar_init(&bars->sa_ready, 256);
       mbar_init(&bars->d1k_ready, 1);
       mbar_init(&bars->d1q_ready, 1);
-      mbar_init(&bars->ra_ready, 256);
       mbar_init(&bars->x_ready, 1);
-      mbar_init(&bars->xa_ready, 256);
       mbar_init(&bars->s_ready, 1);
       mbar_init(&bars->q_scaled, 128);
       mbar_init(&bars->d1q_free, 128);
@@ -412,9 +416,9 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       if (!ok) break;
       const int n = chunks[c & 3].n;
       if (n == 0) break;
-      ok = HYB_WAIT(bars->full_kq[st], (c >> 1) & 1);
+      ok = HYB_WAIT(bars->full_kq[c % kNKQ], (c / kNKQ) & 1);
       {                                      // lengths: thread r, row r of the stacked [K; Q]
-        const uint8_t* kq = sm + kOffKQ + st * kStageKQ + gt * 128;
+        const uint8_t* kq = sm + kOffKQ + (c % kNKQ) * kStageKQ + gt * 128;
         f32x2 s2 = pair(0.f, 0.f);
 #pragma unroll 4
         for (int ch = 0; ch < 16; ++ch) {
@@ -448,7 +452,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       if (!ok) break;
       mbar_arrive(&bars->gates[c & 3]);
       ok = HYB_WAIT(bars->d0_ready[st], (c >> 1) & 1);
-      if (c >= 2) ok = HYB_WAIT(bars->o_free[st], ((c - 2) >> 1) & 1) && ok;   // W's and P's buffers
+      if (c >= 2) ok = HYB_WAIT(bars->o_free[st], ((c - 2) >> 1) & 1) && ok;   // P's buffer
       tc_fence_after();
       {
         // warps 0, 1: row t of K K^T -> column t of A^T; warps 2, 3: row t of Q K^T -> row t of P.
@@ -611,14 +615,16 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
         for (int i = 0; i < 2; ++i) store_c(A + r0 * kLdA + 32 + j0 + 8 * i, z[i], -1.f, lane);
       }
-      bar_group(bar);
+      // W has one buffer: (w) of the last chunk must have read it
+      ok = bar_group_all(bar, c == 0 || HYB_WAIT(bars->x_ready, (c - 1) & 1));
+      if (!ok) break;
       // W's columns times beta / |k|, as three bf16 terms: a warp 32 rows of one half of the columns
       // (the upper right block is zero from the start)
       if (gw != 1) {
         const int half = gw & 1, t = 32 * (gw >> 1) + lane;
         const float* src = A + (half == (gw >> 1) ? t * kLdA + 32 * half : lane * kLdA + 32);
         const bool diag = half == (gw >> 1);
-        uint8_t* dst = sm + kOffW + st * 3 * kTile64 + t * 128;
+        uint8_t* dst = sm + kOffW + t * 128;
 #pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           float v[8];
@@ -660,8 +666,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       n = chunks[c & 3].n;
       flags = chunks[c & 3].flags;
       if (n == 0) return true;
-      if (!HYB_WAIT(bars->full_v[c & 1], (c >> 1) & 1)) return false;
-      const uint8_t* vs = sm + kOffV + (c & 1) * kStageV + (j >> 6) * kSubV + (j & 7) * 2;
+      if (!HYB_WAIT(bars->full_v, c & 1)) return false;
+      const uint8_t* vs = sm + kOffV + (j >> 6) * kSubV + (j & 7) * 2;
       const int cj = (j & 63) >> 3;
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
@@ -678,7 +684,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           else if (t + 1 >= n) v[e / 2] &= 0xffffu;
         }
       }
-      mbar_arrive(&bars->free_v[c & 1]);
+      mbar_arrive(&bars->free_v);
       return HYB_WAIT(bars->gates[c & 3], (c >> 2) & 1);
     };
     ok = fetch(0);
@@ -699,27 +705,29 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
             __nanosleep(100);
           }
         }
-#pragma unroll 1
-        for (int i = i0; i < i0 + 64; i += 16) {
-          float v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            v[e] = flags & kZero ? 0.f : __ldcg(S + (i + e) * kD + j);
-          put_state(tl, i, v, G.dec);
-        }
-      } else {
+      }
+      {
+        const bool from_tmem = !(flags & kFirst), from_pool = !(flags & kZero);
         const float dec = G.dec;
 #pragma unroll 1
-        for (int i = i0; i < i0 + 64; i += 16) {
+        for (int x = 0; x < 4; ++x) {        // pieces of 16 key dims; (k) starts with the first two
+          const int i = i0 + 16 * x;
           float s[16];
-          tmem_ld16(tl + kColS + i, s);
-          tmem_ld_wait();
+          if (from_tmem) {
+            tmem_ld16(tl + kColS + i, s);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = from_pool ? __ldcg(S + (i + e) * kD + j) : 0.f;
+          }
           put_state(tl, i, s, dec);
+          if (x & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars->sa_ready[x >> 1]);
+          }
         }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&bars->sa_ready);
       // R = V - e^G K S (beta is in W)
       ok = HYB_WAIT(bars->d1k_ready, c & 1);
       if (!ok) break;
@@ -740,10 +748,10 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           unpair(fma2(pair(-a.z, -a.w), pair(d[e + 2], d[e + 3]), pair(bf16_lo(v1), bf16_hi(v1))), d[e + 2], d[e + 3]);
         }
         put_terms(tl + kColRh + t0 / 2, tl + kColRm + t0 / 2, tl + kColRl + t0 / 2, d);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->ra_ready[x]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&bars->ra_ready);
       // X: times its way to the chunk's end for the state, and as it is for the outputs
       ok = HYB_WAIT(bars->x_ready, c & 1);
       if (!ok) break;
@@ -766,10 +774,10 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           unpair(mul2(pair(a.z, a.w), pair(d[e + 2], d[e + 3])), d[e + 2], d[e + 3]);
         }
         put_terms(tl + kColXh + at, tl + kColXm + at, tl + kColXl + at, d);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->xa_ready[x >> 4]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&bars->xa_ready);
       ok = fetch(c + 1);
       if (!ok) break;
       // the chunk's last state
@@ -869,7 +877,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     bool more = first_chunk(in, plan_sh, w), ended = false;
     int ckq = 0, cv = 0;                     // chunks requested
     for (int c = 0;; ++c) {
-      const int st = c & 1, row = w.sg.t0 + w.ci * kC;
+      const int st = c % kNKQ, row = w.sg.t0 + w.ci * kC;
       const int n = more ? min(kC, w.sg.n - w.ci * kC) : 0;
       // gates and betas of rows lane and lane + 32
       const int64_t at = (int64_t)row * in.H + w.sg.h + (int64_t)lane * in.H, at2 = at + 32ll * in.H;
@@ -890,7 +898,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       float h0, l0, h1, l1;
       from_fixed(a, (na & upto) != 0, h0, l0);
       from_fixed(b, na != 0 || (nb & upto) != 0, h1, l1);
-      if (c >= 2) ok = HYB_WAIT(bars->free_kq[st], ((c - 2) >> 1) & 1);
+      if (c >= kNKQ) ok = HYB_WAIT(bars->free_kq[c % kNKQ], (c / kNKQ - 1) & 1);
       if (!ok) break;
       Gates& G = gates[c & 3];
       G.hi[lane] = h0;
@@ -918,13 +926,13 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       mbar_arrive(&bars->info[c & 3]);
       if (n > 0) {
-        if (c >= 2) ok = HYB_WAIT(bars->free_v[st], ((c - 2) >> 1) & 1);
+        if (c >= 1) ok = HYB_WAIT(bars->free_v, (c - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
-          uint8_t* vs = sm + kOffV + st * kStageV;
-          mbar_expect_tx(&bars->full_v[st], kStageV);
+          uint8_t* vs = sm + kOffV;
+          mbar_expect_tx(&bars->full_v, kStageV);
           for (int sb = 0; sb < 2; ++sb)
-            tma_load_3d(vs + sb * kSubV, &tv, sb * 64, w.sg.h, row, &bars->full_v[st]);
+            tma_load_3d(vs + sb * kSubV, &tv, sb * 64, w.sg.h, row, &bars->full_v);
         }
         cv = c + 1;
       }
@@ -934,23 +942,26 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     }
     if (!ok && lane == 0) {                  // let the loads in flight land before exiting
       flag(status, HYB_DEVERR_TIMEOUT);
-      for (int i = max(0, ckq - 2); i < ckq; ++i) mbar_wait(&bars->full_kq[i & 1], (i >> 1) & 1, 100000000ull);
-      for (int i = max(0, cv - 2); i < cv; ++i) mbar_wait(&bars->full_v[i & 1], (i >> 1) & 1, 100000000ull);
+      for (int i = max(0, ckq - kNKQ); i < ckq; ++i)
+        mbar_wait(&bars->full_kq[i % kNKQ], (i / kNKQ) & 1, 100000000ull);
+      if (cv > 0) mbar_wait(&bars->full_v, (cv - 1) & 1, 100000000ull);
     }
   } else {
     // ------------------------------------------------------------ MMAs
     const uint32_t sm0 = smem_u32(sm);
     const uint64_t km0 = sw128_desc(sm0, 16, 1024);            // K-major operands
     const uint64_t mn0 = sw128_desc(sm0, kSubKQ, 1024);        // K as [t][i], i-major: two 64-wide blocks
-    bool more = true;
+    int end = 0x7fffffff;                    // number of chunks, once it is known
     // (0) of chunk cn, if there is one: rows past the request become zero rows of K first
     auto issue0 = [&](int cn) -> bool {
-      const int st = cn & 1;
+      if (cn >= end) return true;
       if (!HYB_WAIT(bars->info[cn & 3], (cn >> 2) & 1)) return false;
-      const int n = chunks[cn & 3].n;
-      more = n > 0;
-      if (!more) return true;
-      if (!HYB_WAIT(bars->full_kq[st], (cn >> 1) & 1)) return false;
+      const int n = chunks[cn & 3].n, st = cn % kNKQ;
+      if (n == 0) {
+        end = cn;
+        return true;
+      }
+      if (!HYB_WAIT(bars->full_kq[st], (cn / kNKQ) & 1)) return false;
       if (n < kC) {
         uint8_t* ks = sm + kOffKQ + st * kStageKQ;
         for (int e = lane; e < (kC - n) * 16; e += 32)
@@ -968,27 +979,29 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           const uint64_t d = desc_add(km0, kq + (k >> 2) * kSubKQ + (k & 3) * 32);
           tc_mma(tmem + kCol0, d, d, kIdesc64, k > 0);
         }
-        tc_commit(&bars->d0_ready[st]);
+        tc_commit(&bars->d0_ready[cn & 1]);
       }
       __syncwarp();
       return true;
     };
-    ok = issue0(0);
-    for (int c = 0; ok && more; ++c) {
-      const int st = c & 1;
-      const uint32_t kq = kOffKQ + st * kStageKQ;
-      ok = HYB_WAIT(bars->sa_ready, c & 1);
-      if (!ok) break;
-      if (elect_one()) {
-        tc_fence_after();
+    ok = issue0(0) && issue0(1);             // two chunks ahead
+    for (int c = 0; ok && c < end; ++c) {
+      const uint32_t kq = kOffKQ + (c % kNKQ) * kStageKQ;
+      for (int x = 0; x < 2; ++x) {          // (k): key dims 0-31 and 64-95, then the others
+        ok = HYB_WAIT(bars->sa_ready[x], c & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < 24; ++x) {       // (k)
-          const int k = x & 7;
-          tc_mma_ta(tmem + kCol1K, tmem + kColSA + x * 8, desc_add(km0, kq + (k >> 2) * kSubKQ + (k & 3) * 32), kIdesc64, x > 0);
+          for (int y = 0; y < 12; ++y) {
+            const int k = (y & 1) + ((y & 2) << 1) + 2 * x, term = y >> 2;
+            tc_mma_ta(tmem + kCol1K, tmem + kColSA + term * 64 + k * 8, desc_add(km0, kq + (k >> 2) * kSubKQ + (k & 3) * 32), kIdesc64, x + y > 0);
+          }
+          if (x == 1) tc_commit(&bars->d1k_ready);
         }
-        tc_commit(&bars->d1k_ready);
+        __syncwarp();
       }
-      __syncwarp();
+      if (!ok) break;
       if (c >= 1) ok = HYB_WAIT(bars->d1q_free, (c - 1) & 1);
       if (!ok) break;
       if (elect_one()) {
@@ -1001,43 +1014,53 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         tc_commit(&bars->d1q_ready);
       }
       __syncwarp();
-      ok = issue0(c + 1);
+      ok = HYB_WAIT(bars->w_ready[c & 1], (c >> 1) & 1);
       if (!ok) break;
-      ok = HYB_WAIT(bars->w_ready[st], (c >> 1) & 1) && HYB_WAIT(bars->ra_ready, c & 1);
-      if (!ok) break;
-      if (elect_one()) {
-        tc_fence_after();
-        const uint64_t wd = desc_add(km0, kOffW + st * 3 * kTile64);
+      for (int x = 0; x < 2; ++x) {          // (w): rows 16-47, then the others
+        ok = HYB_WAIT(bars->ra_ready[x], c & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t wd = desc_add(km0, kOffW);
 #pragma unroll
-        for (int x = 0; x < 6; ++x) {        // (w): R h W h, h m, m h, h l, m m, l h
-          const int r = x == 2 || x == 4 ? 1 : x == 5 ? 2 : 0, t = x == 1 || x == 4 ? 1 : x == 3 ? 2 : 0;
-          const uint32_t ra = r == 0 ? kColRh : r == 1 ? kColRm : kColRl;
+          for (int y = 0; y < 6; ++y) {      // R h W h, h m, m h, h l, m m, l h
+            const int r = y == 2 || y == 4 ? 1 : y == 5 ? 2 : 0, t = y == 1 || y == 4 ? 1 : y == 3 ? 2 : 0;
+            const uint32_t ra = r == 0 ? kColRh : r == 1 ? kColRm : kColRl;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_ta(tmem + kColX, tmem + ra + k * 8, desc_add(wd, t * kTile64 + k * 32), kIdesc64, x + k > 0);
+            for (int z = 0; z < 2; ++z) {
+              const int k = x == 0 ? 1 + z : 3 * z;
+              tc_mma_ta(tmem + kColX, tmem + ra + k * 8, desc_add(wd, t * kTile64 + k * 32), kIdesc64, x + y + z > 0);
+            }
+          }
+          if (x == 1) tc_commit(&bars->x_ready);
         }
-        tc_commit(&bars->x_ready);
+        __syncwarp();
       }
-      __syncwarp();
-      ok = HYB_WAIT(bars->xa_ready, c & 1);
+      ok = ok && issue0(c + 2);
       if (!ok) break;
-      if (elect_one()) {
-        tc_fence_after();
+      for (int x = 0; x < 2; ++x) {          // (s): rows 0-15 and 32-47, then the others
+        ok = HYB_WAIT(bars->xa_ready[x], c & 1);
+        if (!ok) break;
+        if (elect_one()) {
+          tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {        // (s)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_ta(tmem + kColS, tmem + kColXh + x * 32 + k * 8, desc_add(mn0, kq + k * 2048), kIdescS, 1);
+          for (int y = 0; y < 6; ++y) {
+            const int k = x + 2 * (y & 1);
+            tc_mma_ta(tmem + kColS, tmem + kColXh + (y >> 1) * 32 + k * 8, desc_add(mn0, kq + k * 2048), kIdescS, 1);
+          }
+          if (x == 1) {
+            tc_commit(&bars->s_ready);
+            tc_commit(&bars->free_kq[c % kNKQ]);   // the last use of K and Q
+          }
         }
-        tc_commit(&bars->s_ready);
-        tc_commit(&bars->free_kq[st]);       // the last use of K and Q
+        __syncwarp();
       }
-      __syncwarp();
+      if (!ok) break;
       ok = HYB_WAIT(bars->q_scaled, c & 1);
       if (!ok) break;
       if (elect_one()) {
         tc_fence_after();
-        const uint64_t pd = desc_add(km0, kOffP + st * 2 * kTile64);
+        const uint64_t pd = desc_add(km0, kOffP + (c & 1) * 2 * kTile64);
 #pragma unroll
         for (int x = 0; x < 3; ++x) {        // (o): X h P h, h m, m h
 #pragma unroll
