@@ -38,13 +38,19 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
 }
 
 // Run by one whole warp; every lane returns the same plan for CTA p of P. chunks_of(b): the
-// chunks of request b's chains.
-template <typename F>
+// chunks of request b's chains. kCost: what a chain costs beside its chunks (its state's way in and
+// out), in chunks; it lies before the chain's first chunk, and a chain of whose chunks none would
+// come before the cut is not cut.
+template <int kCost = 0, typename F>
 __device__ Plan make_plan(const F& chunks_of, int B, int H, int P, int p, int lane) {
+  auto span = [&](int b) {
+    const int nc = chunks_of(b);
+    return nc > 0 ? nc + kCost : 0;
+  };
   long long total = 0;
   int longest = 0;
   for (int b0 = 0; b0 < B; b0 += 32) {
-    const int nc = b0 + lane < B ? chunks_of(b0 + lane) : 0;
+    const int nc = b0 + lane < B ? span(b0 + lane) : 0;
     total += __reduce_add_sync(0xffffffffu, (unsigned)nc);
     longest = max(longest, (int)__reduce_max_sync(0xffffffffu, (unsigned)nc));
   }
@@ -58,7 +64,7 @@ __device__ Plan make_plan(const F& chunks_of, int B, int H, int P, int p, int la
   long long base = 0;
   for (int b0 = 0; b0 < B; b0 += 32) {
     const int b = b0 + lane;
-    const int nc = b < B ? chunks_of(b) : 0;
+    const int nc = b < B ? span(b) : 0;
     const int incl = warp_incl_scan(nc, lane);
     const long long lo = base + (long long)H * (incl - nc), hi = base + (long long)H * incl;
     const bool in_s = nc > 0 && s >= lo && s < hi, in_e = nc > 0 && e >= lo && e < hi;
@@ -78,8 +84,11 @@ __device__ Plan make_plan(const F& chunks_of, int B, int H, int P, int p, int la
     base += (long long)H * __shfl_sync(0xffffffffu, incl, 31);
   }
   if (offs > 0) {
-    pl.head_u = us;
-    pl.head_end = chunks_of(us / H) - offs;
+    const int end = span(us / H) - offs - kCost;
+    if (end > 0) {
+      pl.head_u = us;
+      pl.head_end = end;
+    }
     pl.full_u0 = us + 1;
   } else {
     pl.full_u0 = us;
@@ -88,7 +97,7 @@ __device__ Plan make_plan(const F& chunks_of, int B, int H, int P, int p, int la
     pl.full_u1 = B * H;
   } else if (offe > 0) {
     pl.tail_u = ue;
-    pl.tail_begin = chunks_of(ue / H) - offe;
+    pl.tail_begin = max(0, span(ue / H) - offe - kCost);
     pl.full_u1 = ue;
   } else {
     pl.full_u1 = ue;

@@ -93,6 +93,7 @@ static_assert(sizeof(Bars) <= 512 && kOffG % 16 == 0 && kOffBar % 8 == 0 && kSme
 
 constexpr int kWarpMain = 8, kWarpOut = 16, kWarpFeed = 20, kWarpMma = 21;
 constexpr int kThreads = 22 * 32;
+constexpr int kChainCost = 1;                  // chunks that a chain's state costs (work split)
 constexpr uint32_t kTmemCols = 512;
 // D0 | D1K | D1Q | S fp32 | operand terms of S. Once (k) and (q) have read the terms, R, X and X'
 // take their places: R's h and m over S's l, R's l inside D1K (each thread over columns that only
@@ -339,7 +340,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
   }
   if (warp == 0) {
     Plan pl{-1, 0, p, p + 1, -1, 0};      // chain p
-    if (cut_chains) pl = make_plan([&](int b) { return chunks_of(in, b); }, B, in.H, P, p, lane);
+    if (cut_chains) pl = make_plan<kChainCost>([&](int b) { return chunks_of(in, b); }, B, in.H, P, p, lane);
     if (lane == 0) plan_sh = pl;
   }
   __syncthreads();
