@@ -145,10 +145,16 @@ def _d(d):
     return None if d is None else C.byref(d)
 
 
+_current_stream = None      # torch.cuda.current_stream, from the first call that needs it
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            _current_stream = torch.cuda.current_stream
+        return _current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -30,8 +30,9 @@ __device__ __forceinline__ float inv_len(float ss, float eps) {
 // Bound by HBM: each state is read and written once (2 x 64 KiB at D = 128), against 7 flops an
 // element. A CTA owns 32 columns of one state, 8 threads x float4 to a row and 32 rows a pass; all
 // loads of a thread (PASSES x 16 bytes) are in flight before the first use, and columns do not
-// depend on one another, so no CTA waits for another. The sums over the 128 rows go through
-// shuffles (4 rows of a warp) and shared memory (8 warps), one barrier in all.
+// depend on one another, so no CTA waits for another. k and q go through shared memory, and so
+// do the sums over the 128 rows after a shuffle over the 4 rows of a warp: registers stay few, and
+// five CTAs per SM keep the loads of some while others store.
 template <int D>
 struct DeltaStep {
   static constexpr int COLS = D < 32 ? D : 32;
@@ -40,11 +41,12 @@ struct DeltaStep {
   static constexpr int RPP = THREADS / TPR;                 // rows per pass
   static constexpr int PASSES = D / RPP;
   static constexpr int NW = THREADS / 32;
+  static constexpr int CTAS = PASSES > 4 ? 3 : 5;           // per SM
   static_assert(PASSES * RPP == D && NW * 32 == THREADS, "shape");
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(DeltaStep<D>::THREADS)
+__global__ void __launch_bounds__(DeltaStep<D>::THREADS, DeltaStep<D>::CTAS)
 delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restrict__ k,
                   const T* __restrict__ v, const float* __restrict__ g,
                   const float* __restrict__ beta, float* __restrict__ pool, int NS,
@@ -52,7 +54,8 @@ delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
                   int64_t vs, float scale, float eps, unsigned* status) {
   using Sh = DeltaStep<D>;
   constexpr int COLS = Sh::COLS, TPR = Sh::TPR, RPP = Sh::RPP, PASSES = Sh::PASSES, NW = Sh::NW;
-  __shared__ __align__(16) float red_k[NW][COLS], red_q[NW][COLS], red_s[NW][4];
+  __shared__ __align__(16) float sh_k[D], sh_q[D];
+  __shared__ __align__(16) float red_k[NW][COLS], red_q[NW][COLS], sums[4];
 
   pdl_wait();
   const int h = blockIdx.y, b = blockIdx.z;
@@ -64,73 +67,86 @@ delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tc = threadIdx.x % TPR, rg = threadIdx.x / TPR;
   const int col = blockIdx.x * COLS + tc * 4;
-  float* S = pool + ((int64_t)slot * Hv + h) * D * D;
+  float* S = pool + ((int64_t)slot * Hv + h) * D * D + rg * D + col;
 
   float4 st[PASSES];
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p)
-    st[p] = __ldcs(reinterpret_cast<const float4*>(S + (int64_t)(rg + p * RPP) * D + col));
+  for (int p = 0; p < PASSES; ++p) st[p] = __ldcs(reinterpret_cast<const float4*>(S + p * RPP * D));
   pdl_trigger();                           // the next kernel may launch (it waits for this one)
-  const T* kr = k + b * ks + (int64_t)(h / rep) * D;
-  const T* qr = q + b * qs + (int64_t)(h / rep) * D;
-  const T* vr = v + b * vs + (int64_t)h * D + col;
-  float ki[PASSES], qi[PASSES], vv[4];
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    ki[p] = to_f(kr[rg + p * RPP]);
-    qi[p] = to_f(qr[rg + p * RPP]);
+  for (int i = threadIdx.x; i < D; i += Sh::THREADS) {
+    sh_k[i] = to_f(k[b * ks + (int64_t)(h / rep) * D + i]);
+    sh_q[i] = to_f(q[b * qs + (int64_t)(h / rep) * D + i]);
   }
+  const T* vr = v + b * vs + (int64_t)h * D + col;
+  const float eg = expf(g[(int64_t)b * Hv + h]), be = beta[(int64_t)b * Hv + h];
+  float vv[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) vv[e] = to_f(vr[e]);
-  const float eg = expf(g[(int64_t)b * Hv + h]), be = beta[(int64_t)b * Hv + h];
+  __syncthreads();
 
-  float a[11] = {};                        // S^T k (4 columns), S^T q (4), k.k, q.q, q.k
+  float a[8] = {};                         // S^T k and S^T q, 4 columns each
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const float s[4] = {st[p].x, st[p].y, st[p].z, st[p].w};
+    const float ki = sh_k[rg + p * RPP], qi = sh_q[rg + p * RPP];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      a[e] = fmaf(ki[p], s[e], a[e]);
-      a[4 + e] = fmaf(qi[p], s[e], a[4 + e]);
+      a[e] = fmaf(ki, s[e], a[e]);
+      a[4 + e] = fmaf(qi, s[e], a[4 + e]);
     }
-    a[8] = fmaf(ki[p], ki[p], a[8]);
-    a[9] = fmaf(qi[p], qi[p], a[9]);
-    a[10] = fmaf(qi[p], ki[p], a[10]);
   }
 #pragma unroll
   for (int o = TPR; o < 32; o <<= 1)
 #pragma unroll
-    for (int e = 0; e < 11; ++e) a[e] += __shfl_xor_sync(0xffffffffu, a[e], o);
+    for (int e = 0; e < 8; ++e) a[e] += __shfl_xor_sync(0xffffffffu, a[e], o);
   if (lane < TPR) {
     *reinterpret_cast<float4*>(&red_k[warp][lane * 4]) = make_float4(a[0], a[1], a[2], a[3]);
     *reinterpret_cast<float4*>(&red_q[warp][lane * 4]) = make_float4(a[4], a[5], a[6], a[7]);
-    if (lane == 0) *reinterpret_cast<float4*>(red_s[warp]) = make_float4(a[8], a[9], a[10], 0.f);
+  }
+  if (warp == NW - 1) {                    // k.k, q.q, q.k
+    float kk = 0.f, qq = 0.f, qk = 0.f;
+    for (int i = lane; i < D; i += 32) {
+      kk = fmaf(sh_k[i], sh_k[i], kk);
+      qq = fmaf(sh_q[i], sh_q[i], qq);
+      qk = fmaf(sh_q[i], sh_k[i], qk);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      kk += __shfl_xor_sync(0xffffffffu, kk, o);
+      qq += __shfl_xor_sync(0xffffffffu, qq, o);
+      qk += __shfl_xor_sync(0xffffffffu, qk, o);
+    }
+    if (lane == 0) *reinterpret_cast<float4*>(sums) = make_float4(kk, qq, qk, 0.f);
   }
   __syncthreads();
-  float sk[4] = {}, sq[4] = {}, kk = 0.f, qq = 0.f, qk = 0.f;
+  const float rk = inv_len(sums[0], eps);
+  float u[4] = {};                         // S^T k, then the correction, times rk for the state's k
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     const float4 x = *reinterpret_cast<const float4*>(&red_k[w][tc * 4]);
-    const float4 y = *reinterpret_cast<const float4*>(&red_q[w][tc * 4]);
-    const float4 z = *reinterpret_cast<const float4*>(red_s[w]);
-    sk[0] += x.x; sk[1] += x.y; sk[2] += x.z; sk[3] += x.w;
-    sq[0] += y.x; sq[1] += y.y; sq[2] += y.z; sq[3] += y.w;
-    kk += z.x; qq += z.y; qk += z.z;
-  }
-  const float rk = inv_len(kk, eps), rq = inv_len(qq, eps);
-  float u[4];                              // the correction, times rk for the state's k
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float x = be * (vv[e] - eg * (rk * sk[e]));
-    if (rg == 0)
-      put(out + ((int64_t)b * Hv + h) * D + col + e, scale * rq * fmaf(rk * qk, x, eg * sq[e]));
-    u[e] = rk * x;
+    u[0] += x.x; u[1] += x.y; u[2] += x.z; u[3] += x.w;
   }
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p)
-    __stcs(reinterpret_cast<float4*>(S + (int64_t)(rg + p * RPP) * D + col),
-           make_float4(fmaf(ki[p], u[0], eg * st[p].x), fmaf(ki[p], u[1], eg * st[p].y),
-                       fmaf(ki[p], u[2], eg * st[p].z), fmaf(ki[p], u[3], eg * st[p].w)));
+  for (int e = 0; e < 4; ++e) u[e] = be * (vv[e] - eg * (rk * u[e])) * rk;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const float ki = sh_k[rg + p * RPP];
+    __stcs(reinterpret_cast<float4*>(S + p * RPP * D),
+           make_float4(fmaf(ki, u[0], eg * st[p].x), fmaf(ki, u[1], eg * st[p].y),
+                       fmaf(ki, u[2], eg * st[p].z), fmaf(ki, u[3], eg * st[p].w)));
+  }
+  if (rg == 0) {
+    const float rq = scale * inv_len(sums[1], eps), qk = sums[2];
+    float o[4] = {};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(&red_q[w][tc * 4]);
+      o[0] += y.x; o[1] += y.y; o[2] += y.z; o[3] += y.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      put(out + ((int64_t)b * Hv + h) * D + col + e, rq * fmaf(qk, u[e], eg * o[e]));
+  }
 }
 
 // ------------------------------------------------------------------ prefill on the CUDA cores

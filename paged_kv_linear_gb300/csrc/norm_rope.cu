@@ -6,8 +6,9 @@
 // as two groups of 4 that hold both elements of each pair: 4 at x[e] and 4 at x[e + rot/2] in the
 // half layout, so that neither layout needs a shuffle to rotate; the part behind rot_dim is cut
 // in two the same way. The token's rot_dim / 2 cosines and sines are computed once per warp, by
-// all lanes, and kept in registers for all of its rows; the loads of kU rounds of rows are in
-// flight together.
+// all lanes; a lane folds those of its pairs and the weights into 16 factors, so that a row's
+// element takes two products and the norm's one. The loads of kU rounds of rows are in flight
+// together.
 //
 // Angles. p f loses its fraction in fp32 once p f passes some thousand turns, so the
 // frequency is kept in turns, f / 2 pi = hi + lo (two fp32, from one fp64 product per warp), and
@@ -17,13 +18,13 @@
 
 #include <cmath>
 
-#include "hyb_internal.cuh"
+#include "tc.cuh"
 
 namespace hyb {
 namespace {
 
 constexpr int kWarps = 8;                  // warps per CTA
-constexpr int kU = 4;                      // rounds of rows in flight
+constexpr int kU = 4;                      // rounds of rows in a batch; two batches in flight
 constexpr int kMaxPos = 1 << 24;           // positions are exact in fp32
 
 // Four elements: the raw bits as loaded, their values, and the way back.
@@ -56,13 +57,13 @@ struct RopeArgs {
   const float *inv_freq, *qw, *kw;
   int64_t qs, ks, vs;                      // elements between tokens
   int64_t n_slots;
-  int T_, Hq, Hk, bs, rot, parts, rounds;  // parts: warps per token; rounds: row rounds of a part
+  int T_, Hq, Hk, bs_log2, rot, parts, rounds;  // parts: warps per token; rounds: row rounds of a part
   float eps, w_off, m;
   unsigned* status;
 };
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
 norm_rope_kernel(const __grid_constant__ RopeArgs<T> a) {
   using F = Four<T>;
   using Raw = typename F::Raw;
@@ -76,18 +77,11 @@ norm_rope_kernel(const __grid_constant__ RopeArgs<T> a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % LPR, rr = lane / LPR;
   float2* cs = cs_sh[warp];
-  // this lane's two groups of 4 elements, and where the group's pairs find their angle
+  // this lane's two groups of 4 elements: 4 pairs (x[i], x[i + 4]), or (x[2i], x[2i + 1])
   const int nrot = a.rot / 8;              // lanes of a row with turning elements
   const bool turns = c < nrot;
   const int e0 = INTER ? 8 * c : turns ? 4 * c : a.rot + 4 * (c - nrot);
   const int e1 = INTER ? e0 + 4 : e0 + (turns ? a.rot / 2 : (D - a.rot) / 2);
-  float wq[8], wk[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int at = (e < 4 ? e0 : e1 - 4) + e;
-    wq[e] = a.qw ? a.qw[at] + a.w_off : 1.f;
-    wk[e] = a.kw ? a.kw[at] + a.w_off : 1.f;
-  }
   float fhi[NF], flo[NF];                  // frequencies in turns per position
 #pragma unroll
   for (int n = 0; n < NF; ++n) {
@@ -96,117 +90,163 @@ norm_rope_kernel(const __grid_constant__ RopeArgs<T> a) {
     fhi[n] = (float)f;
     flo[n] = (float)(f - (double)fhi[n]);
   }
-  const int rows = a.Hq + 2 * a.Hk;        // a token's rows: q, k, v
-  const int64_t items = (int64_t)a.T_ * a.parts;
-  for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items; it += (int64_t)gridDim.x * kWarps) {
-    const int t = (int)(it / a.parts), part = (int)(it - (int64_t)t * a.parts);
-    const int p = a.positions[t];
+  // a token's rounds: those of q, of k, of v
+  const int nq = (a.Hq + RPR - 1) / RPR, nk = (a.Hk + RPR - 1) / RPR;
+  // items of one warp: (token, part) from here on in steps of the grid's warps
+  const int step = gridDim.x * kWarps, step_t = step / a.parts, step_p = step - step_t * a.parts;
+  const int it0 = blockIdx.x * kWarps + warp;
+  int t_next = it0 / a.parts, part_next = it0 - t_next * a.parts;
+  int p_next = t_next < a.T_ ? a.positions[t_next] : -1;
+  int64_t slot_next = t_next < a.T_ && a.slot ? a.slot[t_next] : -1;
+#pragma unroll 1
+  while (t_next < a.T_) {
+    const int64_t t = t_next;
+    const int part = part_next, p = p_next;
+    int64_t slot = slot_next;
+    part_next += step_p;
+    const bool over = part_next >= a.parts;
+    part_next -= over ? a.parts : 0;
+    t_next = a.T_ - t_next > step_t + over ? t_next + step_t + over : a.T_;
+    if (t_next < a.T_) {
+      p_next = a.positions[t_next];
+      if (a.slot) slot_next = a.slot[t_next];
+    }
     if (p < 0) continue;
     if (p > kMaxPos) {
       if (lane == 0) flag(a.status, HYB_DEVERR_BAD_LENGTH);
       continue;
     }
-    int64_t slot = a.slot ? a.slot[t] : -1;
     if (slot >= a.n_slots) {
       if (lane == 0) flag(a.status, HYB_DEVERR_BAD_SLOT);
       slot = -1;
     }
-    const int64_t blk = slot >= 0 ? slot / a.bs : 0, off = slot - blk * a.bs;
-    const int row_end = min(rows, (part + 1) * a.rounds * RPR);
-    float2 ang[4];                         // (cos, sin) of this lane's pairs
-    bool first = true;
-    for (int row0 = part * a.rounds * RPR; row0 < row_end; row0 += kU * RPR) {
+    // where the token's first head lies in the caches, and from head to head
+    const int64_t blk = slot >> a.bs_log2;   // (no slot: not used)
+    const int64_t cache0 = (((blk * a.Hk) << a.bs_log2) + (slot - (blk << a.bs_log2))) * D;
+    const int cache_h = D << a.bs_log2;
+    const int begin = part * a.rounds, end = min(nq + 2 * nk, begin + a.rounds);
+
+    // Batches of kU rounds of q's, then k's, then v's rows (section 0, 1, 2; 3: none left). The next
+    // batch is on its way while one is worked on.
+    int sec = -1, r = 0, r1 = 0;
+    Raw next[kU][2];
+    auto load_next = [&] {
+      r += kU;
+#pragma unroll 1
+      while (r >= r1 && sec < 3) {
+        ++sec;
+        const int off = sec == 0 ? 0 : sec == 1 ? nq : nq + nk;
+        r = max(begin - off, 0);
+        r1 = sec == 3 || (sec == 2 && slot < 0) ? r : min(end - off, sec == 0 ? nq : nk);
+      }
+      if (sec == 3) return;
+      const int heads = sec == 0 ? a.Hq : a.Hk, h0 = r * RPR + rr;
+      const T* src = (sec == 0 ? a.q + t * a.qs : sec == 1 ? a.k + t * a.ks : a.v + t * a.vs) + h0 * D;
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (h0 + u * RPR < min(heads, r1 * RPR)) {
+          next[u][0] = *reinterpret_cast<const Raw*>(src + e0 + u * RPR * D);
+          next[u][1] = *reinterpret_cast<const Raw*>(src + e1 + u * RPR * D);
+        }
+    };
+    load_next();
+    {                                      // the token's angles
+      const float pf = (float)p;
+      __syncwarp();
+#pragma unroll
+      for (int n = 0; n < NF; ++n) {
+        const float x = pf * fhi[n];
+        const float y = (x - rintf(x)) + (fmaf(pf, fhi[n], -x) + pf * flo[n]);
+        float sn, cn;
+        sincospif(2.f * y, &sn, &cn);
+        if (lane + 32 * n < a.rot / 2) cs[lane + 32 * n] = make_float2(a.m * cn, a.m * sn);
+      }
+      __syncwarp();
+    }
+    // pair i: (u, v) -> (u c0 - v s1, v c1 + u s0), c and s times the weights of u (0) and v (1)
+    f32x2 c0[2], s0[2], c1[2], s1[2];
+    int have = -1;                         // the section that these are for
+#pragma unroll 1
+    while (sec < 3) {
+      const int now = sec, h0 = r * RPR + rr, most = min(now == 0 ? a.Hq : a.Hk, r1 * RPR);
       Raw raw[kU][2];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int row = row0 + u * RPR + rr;
-        if (row >= row_end) continue;
-        const T* src = row < a.Hq ? a.q + t * a.qs + (int64_t)row * D
-                       : row < a.Hq + a.Hk ? a.k + t * a.ks + (int64_t)(row - a.Hq) * D
-                                           : a.v + t * a.vs + (int64_t)(row - a.Hq - a.Hk) * D;
-        if (row >= a.Hq + a.Hk && slot < 0) continue;        // v goes nowhere
-        raw[u][0] = *reinterpret_cast<const Raw*>(src + e0);
-        raw[u][1] = *reinterpret_cast<const Raw*>(src + e1);
+        raw[u][0] = next[u][0];
+        raw[u][1] = next[u][1];
       }
-      if (first) {                         // the token's angles, while the first rows arrive
-        first = false;
-        const float pf = (float)p;
-        __syncwarp();
+      load_next();
+      const float* w = now == 0 ? a.qw : a.kw;
+      if (now < 2 && have != now) {
+        have = now;
+        float x[4][4];
 #pragma unroll
-        for (int n = 0; n < NF; ++n) {
-          const float x = pf * fhi[n];
-          const float r = (x - rintf(x)) + (fmaf(pf, fhi[n], -x) + pf * flo[n]);
-          float sn, cn;
-          sincospif(2.f * r, &sn, &cn);
-          if (lane + 32 * n < a.rot / 2) cs[lane + 32 * n] = make_float2(a.m * cn, a.m * sn);
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = turns ? cs[4 * c + i] : make_float2(1.f, 0.f);
+          const int iu = INTER ? e0 + 2 * i : e0 + i, iv = INTER ? e0 + 2 * i + 1 : e1 + i;
+          const float wu = w ? w[iu] + a.w_off : 1.f, wv = w ? w[iv] + a.w_off : 1.f;
+          x[0][i] = wu * f.x; x[1][i] = wu * f.y; x[2][i] = wv * f.x; x[3][i] = -wv * f.y;
         }
-        __syncwarp();
-        if (turns) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ang[e] = cs[4 * c + e];
+        for (int i = 0; i < 2; ++i) {
+          c0[i] = pair(x[0][2 * i], x[0][2 * i + 1]);
+          s0[i] = pair(x[1][2 * i], x[1][2 * i + 1]);
+          c1[i] = pair(x[2][2 * i], x[2][2 * i + 1]);
+          s1[i] = pair(x[3][2 * i], x[3][2 * i + 1]);
         }
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int row = row0 + u * RPR + rr;
-        float x[8], ss = 0.f;
-        const bool is_q = row < a.Hq, is_v = row >= a.Hq + a.Hk;
-        if (row < row_end && !is_v) {
-          F::get(raw[u][0], x);
-          F::get(raw[u][1], x + 4);
+        const int h = h0 + u * RPR;
+        const bool in = h < most;
+        Raw y0 = raw[u][0], y1 = raw[u][1];
+        if (now < 2) {
+          float x[8];
+          F::get(y0, x);
+          F::get(y1, x + 4);
+          f32x2 xu[2], xv[2];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        }
-#pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (row >= row_end) continue;
-        if (is_v) {
-          if (slot >= 0) {
-            T* dst = a.vc + ((blk * a.Hk + (row - a.Hq - a.Hk)) * a.bs + off) * D;
-            *reinterpret_cast<Raw*>(dst + e0) = raw[u][0];
-            *reinterpret_cast<Raw*>(dst + e1) = raw[u][1];
+          for (int i = 0; i < 2; ++i) {
+            xu[i] = INTER ? pair(x[4 * i], x[4 * i + 2]) : pair(x[2 * i], x[2 * i + 1]);
+            xv[i] = INTER ? pair(x[4 * i + 1], x[4 * i + 3]) : pair(x[4 + 2 * i], x[5 + 2 * i]);
           }
-          continue;
-        }
-        if (is_q ? a.qw != nullptr : a.kw != nullptr) {
-          const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+          float inv = 1.f;
+          if (w) {
+            float ss, s2;
+            unpair(fma2(xv[1], xv[1], fma2(xv[0], xv[0], fma2(xu[1], xu[1], mul2(xu[0], xu[0])))), ss, s2);
+            ss += s2;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= inv * (is_q ? wq[e] : wk[e]);
-        }
-        if (turns) {
-          if (INTER) {                     // pairs (0, 1), (2, 3), ...
+            for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            inv = rsqrtf(ss * (1.f / D) + a.eps);
+          }
+          const f32x2 inv2 = pair(inv, inv);
+          float y[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float u0 = x[2 * e], u1 = x[2 * e + 1];
-              x[2 * e] = u0 * ang[e].x - u1 * ang[e].y;
-              x[2 * e + 1] = u1 * ang[e].x + u0 * ang[e].y;
-            }
-          } else {                         // pairs (0, 4), (1, 5), ...: the two groups
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float u0 = x[e], u1 = x[e + 4];
-              x[e] = u0 * ang[e].x - u1 * ang[e].y;
-              x[e + 4] = u1 * ang[e].x + u0 * ang[e].y;
+          for (int i = 0; i < 2; ++i) {
+            const f32x2 yu = mul2(inv2, fma2(xv[i], s1[i], mul2(xu[i], c0[i])));
+            const f32x2 yv = mul2(inv2, fma2(xu[i], s0[i], mul2(xv[i], c1[i])));
+            if (INTER) {
+              unpair(yu, y[4 * i], y[4 * i + 2]);
+              unpair(yv, y[4 * i + 1], y[4 * i + 3]);
+            } else {
+              unpair(yu, y[2 * i], y[2 * i + 1]);
+              unpair(yv, y[4 + 2 * i], y[5 + 2 * i]);
             }
           }
+          y0 = F::pack(y);
+          y1 = F::pack(y + 4);
         }
-        const Raw y0 = F::pack(x), y1 = F::pack(x + 4);
-        if (is_q) {
-          T* dst = a.q_out + ((int64_t)t * a.Hq + row) * D;
-          *reinterpret_cast<Raw*>(dst + e0) = y0;
-          *reinterpret_cast<Raw*>(dst + e1) = y1;
-        } else {
-          const int h = row - a.Hq;
-          if (a.k_out) {
-            T* dst = a.k_out + ((int64_t)t * a.Hk + h) * D;
-            *reinterpret_cast<Raw*>(dst + e0) = y0;
-            *reinterpret_cast<Raw*>(dst + e1) = y1;
-          }
-          if (slot >= 0) {
-            T* dst = a.kc + ((blk * a.Hk + h) * a.bs + off) * D;
-            *reinterpret_cast<Raw*>(dst + e0) = y0;
-            *reinterpret_cast<Raw*>(dst + e1) = y1;
-          }
+        if (!in) continue;
+        T* d0 = now == 0 ? a.q_out + (t * a.Hq + h) * D
+                : now == 1 && a.k_out ? a.k_out + (t * a.Hk + h) * D : nullptr;
+        if (d0) {
+          *reinterpret_cast<Raw*>(d0 + e0) = y0;
+          *reinterpret_cast<Raw*>(d0 + e1) = y1;
+        }
+        if (now > 0 && slot >= 0) {
+          T* d1 = (now == 1 ? a.kc : a.vc) + cache0 + (int64_t)h * cache_h;
+          *reinterpret_cast<Raw*>(d1 + e0) = y0;
+          *reinterpret_cast<Raw*>(d1 + e1) = y1;
         }
       }
     }
@@ -216,7 +256,7 @@ norm_rope_kernel(const __grid_constant__ RopeArgs<T> a) {
 template <typename T, int D>
 cudaError_t launch_typed(RopeArgs<T> a, bool inter, cudaStream_t s) {
   constexpr int RPR = 32 / (D / 8);
-  const int total = (a.Hq + 2 * a.Hk + RPR - 1) / RPR;     // rounds of rows per token
+  const int total = (a.Hq + RPR - 1) / RPR + 2 * ((a.Hk + RPR - 1) / RPR);   // rounds of rows per token
   // A warp's share of a token: the whole token (its angles computed once) when there are
   // tokens enough to fill the GPU's warps, down to kU rounds when there are few.
   const int64_t warps = (int64_t)num_sms() * 4 * kWarps;
@@ -225,7 +265,7 @@ cudaError_t launch_typed(RopeArgs<T> a, bool inter, cudaStream_t s) {
   a.rounds = (a.rounds + kU - 1) / kU * kU;
   a.parts = (total + a.rounds - 1) / a.rounds;
   const int64_t items = (int64_t)a.T_ * a.parts;
-  const int64_t blocks = std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)num_sms() * 8);
+  const int64_t blocks = std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)num_sms() * 2);
   const cudaError_t e = launch_pdl(inter ? norm_rope_kernel<T, D, true> : norm_rope_kernel<T, D, false>,
                                    dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, a);
   count_launch();
@@ -247,7 +287,7 @@ cudaError_t launch(void* q_out, void* k_out, const void* q, const void* k, const
   a.ks = r->k_stride ? r->k_stride : (int64_t)Hk * D;
   a.vs = r->v_stride ? r->v_stride : (int64_t)Hk * D;
   a.n_slots = (int64_t)d->num_blocks * d->block_size;
-  a.T_ = T_; a.Hq = Hq; a.Hk = Hk; a.bs = d->block_size; a.rot = r->rot_dim;
+  a.T_ = T_; a.Hq = Hq; a.Hk = Hk; a.bs_log2 = log2_int(d->block_size); a.rot = r->rot_dim;
   a.eps = r->eps; a.w_off = r->weight_offset; a.m = r->attn_factor;
   a.status = status;
   switch (D) {
