@@ -154,22 +154,38 @@ delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
 // sizes): fp32 throughout. Columns of a state do not depend on one another, so a CTA carries 32
 // columns of one (request, head) in registers for the whole prompt, and D / 32 CTAs share a
 // state. A column's D rows lie with RG lanes of one warp, so a token takes two sums over registers
-// and one round of shuffles, and no barrier; barriers come with each batch of kTB tokens, whose
-// rows and scalars are staged in shared memory. Bound by the latency of that chain when there are
-// few chains, by fp32 arithmetic (4 D^2 fma per token and head) when there are many.
+// and one round of shuffles, and no barrier. Tokens come in batches of kTB, whose rows and scalars
+// are staged in shared memory; the next batch's rows are on their way to registers meanwhile. Bound
+// by the latency of that chain when there are few chains, by fp32 arithmetic (4 D^2 fma per token
+// and head) when there are many.
 template <int D>
 struct DeltaScan {
   static constexpr int COLS = D < 32 ? D : 32;              // columns per CTA
   static constexpr int RG = D < 32 ? 2 : D / 32;            // lanes per column
   static constexpr int R = D / RG;                          // rows per lane
-  static constexpr int THREADS = COLS * RG;
+  static constexpr int NT = COLS * RG;                      // threads
   static constexpr int CW = 32 / RG;                        // columns per warp
-  static_assert(R % 4 == 0 && THREADS % 32 == 0, "shape");
+  static constexpr int TB = 16;                             // tokens per batch
+  static constexpr int LQ = TB * D / 4 / NT;                // 4-element loads of q (and of k) per thread
+  static constexpr int LV = (TB * COLS / 4 + NT - 1) / NT;  // of v (D = 256: half of the threads)
+  static constexpr int LT = NT / TB < 8 ? NT / TB : 8;      // lanes that work out a token's lengths
+  static_assert(R % 4 == 0 && NT % 32 == 0 && LQ * 4 * NT == TB * D, "shape");
 };
-constexpr int kTB = 16;                                     // tokens per batch
+
+struct Quad {
+  float x[4];
+};
+__device__ __forceinline__ Quad load4(const float* p) {
+  const float4 u = *reinterpret_cast<const float4*>(p);
+  return {u.x, u.y, u.z, u.w};
+}
+__device__ __forceinline__ Quad load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(DeltaScan<D>::THREADS)
+__global__ void __launch_bounds__(DeltaScan<D>::NT)
 delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restrict__ k,
                   const T* __restrict__ v, const float* __restrict__ g,
                   const float* __restrict__ beta, const int32_t* __restrict__ cu,
@@ -177,10 +193,11 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
                   const uint8_t* __restrict__ reset, int rows_total, int max_len, int Hv, int rep,
                   int64_t qs, int64_t ks, int64_t vs, float scale, float eps, unsigned* status) {
   using Sh = DeltaScan<D>;
-  constexpr int COLS = Sh::COLS, RG = Sh::RG, R = Sh::R, CW = Sh::CW, NT = Sh::THREADS;
-  __shared__ __align__(16) float sq[kTB][D], sk[kTB][D];    // unit (or given) rows; q times scale
-  __shared__ float sv[kTB][COLS];
-  __shared__ float s_eg[kTB], s_be[kTB], s_qk[kTB];
+  constexpr int COLS = Sh::COLS, RG = Sh::RG, R = Sh::R, CW = Sh::CW, NT = Sh::NT, TB = Sh::TB;
+  constexpr int LQ = Sh::LQ, LV = Sh::LV, LT = Sh::LT;
+  __shared__ __align__(16) float sq[TB][D], sk[TB][D];      // unit (or given) rows; q times scale
+  __shared__ __align__(16) float sv[TB][COLS];
+  __shared__ __align__(16) float4 s_f[TB];                  // e^g, beta, q.k
 
   const int c0 = blockIdx.x * COLS, h = blockIdx.y, b = blockIdx.z;
   const bool first = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
@@ -198,6 +215,32 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
   float* S = pool + ((int64_t)slot * Hv + h) * D * D + c0 + c;
   const bool zero = reset && reset[b];
   if (t0 == t1 && !zero) return;
+  q += (int64_t)(h / rep) * D;
+  k += (int64_t)(h / rep) * D;
+  v += (int64_t)h * D + c0;
+
+  // rows of the batch at tb, zeros behind the last; token and scalars of this thread
+  Quad nq[LQ], nk[LQ], nv[LV];
+  float ng = 0.f, nb = 0.f;
+  const int lt = threadIdx.x / LT;         // this thread's token in the lengths (if < TB)
+  auto fetch = [&](int tb) {
+    const Quad none = {};
+#pragma unroll
+    for (int e = 0; e < LQ; ++e) {
+      const int i = (threadIdx.x + e * NT) * 4, t = tb + i / D;
+      nq[e] = t < t1 ? load4(q + t * qs + i % D) : none;
+      nk[e] = t < t1 ? load4(k + t * ks + i % D) : none;
+    }
+#pragma unroll
+    for (int e = 0; e < LV; ++e) {
+      const int i = (threadIdx.x + e * NT) * 4, t = tb + i / COLS;
+      nv[e] = i < TB * COLS && t < t1 ? load4(v + t * vs + i % COLS) : none;
+    }
+    const bool in = lt < TB && tb + lt < t1;
+    ng = in ? g[(int64_t)(tb + lt) * Hv + h] : 0.f;
+    nb = in ? beta[(int64_t)(tb + lt) * Hv + h] : 0.f;
+  };
+  fetch(t0);
   // rows 4 (m RG + rg) + e: the RG lanes' 16-byte reads of a staged row lie side by side
   float s[R];
 #pragma unroll
@@ -205,57 +248,66 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
     const int i = 4 * ((m / 4) * RG + rg) + m % 4;
     s[m] = zero ? 0.f : S[(int64_t)i * D];
   }
-  for (int tb = t0; tb < t1; tb += kTB) {
-    const int nt = min(kTB, t1 - tb);
+#pragma unroll 1
+  for (int tb = t0; tb < t1; tb += TB) {
     __syncthreads();                       // the last batch is used up
-    for (int e = threadIdx.x; e < nt * D; e += NT) {
-      const int t = e / D, i = e - t * D;
-      sq[t][i] = to_f(q[(tb + t) * qs + (int64_t)(h / rep) * D + i]);
-      sk[t][i] = to_f(k[(tb + t) * ks + (int64_t)(h / rep) * D + i]);
+#pragma unroll
+    for (int e = 0; e < LQ; ++e) {
+      const int i = (threadIdx.x + e * NT) * 4;
+      *reinterpret_cast<float4*>(&sq[0][0] + i) = make_float4(nq[e].x[0], nq[e].x[1], nq[e].x[2], nq[e].x[3]);
+      *reinterpret_cast<float4*>(&sk[0][0] + i) = make_float4(nk[e].x[0], nk[e].x[1], nk[e].x[2], nk[e].x[3]);
     }
-    for (int e = threadIdx.x; e < nt * COLS; e += NT) {
-      const int t = e / COLS, j = e - t * COLS;
-      sv[t][j] = to_f(v[(tb + t) * vs + (int64_t)h * D + c0 + j]);
+#pragma unroll
+    for (int e = 0; e < LV; ++e) {
+      const int i = (threadIdx.x + e * NT) * 4;
+      if (i < TB * COLS)
+        *reinterpret_cast<float4*>(&sv[0][0] + i) = make_float4(nv[e].x[0], nv[e].x[1], nv[e].x[2], nv[e].x[3]);
     }
+    const float fg = ng, fb = nb;
     __syncthreads();
-    for (int t = warp; t < nt; t += NT / 32) {              // a warp per token: lengths, q.k
+    if (lt < TB) {                         // lengths and q.k: LT lanes a token
+      const int l = threadIdx.x % LT;
       float kk = 0.f, qq = 0.f, qk = 0.f;
-      for (int i = lane; i < D; i += 32) {
-        const float x = sk[t][i], y = sq[t][i];
+#pragma unroll 4
+      for (int i = l; i < D; i += LT) {
+        const float x = sk[lt][i], y = sq[lt][i];
         kk = fmaf(x, x, kk);
         qq = fmaf(y, y, qq);
         qk = fmaf(x, y, qk);
       }
+      const unsigned mask = __activemask();
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {
-        kk += __shfl_xor_sync(0xffffffffu, kk, o);
-        qq += __shfl_xor_sync(0xffffffffu, qq, o);
-        qk += __shfl_xor_sync(0xffffffffu, qk, o);
+      for (int o = LT / 2; o >= 1; o >>= 1) {
+        kk += __shfl_xor_sync(mask, kk, o);
+        qq += __shfl_xor_sync(mask, qq, o);
+        qk += __shfl_xor_sync(mask, qk, o);
       }
       const float rk = inv_len(kk, eps), rq = scale * inv_len(qq, eps);
-      for (int i = lane; i < D; i += 32) {
-        sk[t][i] *= rk;
-        sq[t][i] *= rq;
+#pragma unroll 4
+      for (int i = l; i < D; i += LT) {
+        sk[lt][i] *= rk;
+        sq[lt][i] *= rq;
       }
-      if (lane == 0) {
-        const int64_t at = (int64_t)(tb + t) * Hv + h;
-        s_eg[t] = expf(g[at]);
-        s_be[t] = beta[at];
-        s_qk[t] = qk * rk * rq;
-      }
+      if (l == 0) s_f[lt] = make_float4(expf(fg), fb, qk * rk * rq, 0.f);
     }
     __syncthreads();
+    if (tb + TB < t1) fetch(tb + TB);
+    const int nt = min(TB, t1 - tb);
+#pragma unroll 1
     for (int t = 0; t < nt; ++t) {
+      const float4 f = s_f[t];
+      const float vt = sv[t][c];
+      float4 x[R / 4];
       float pk[4] = {}, pq[4] = {};        // four partial sums each: a shorter chain
 #pragma unroll
       for (int m = 0; m < R; m += 4) {
         const int i = 4 * ((m / 4) * RG + rg);
-        const float4 x = *reinterpret_cast<const float4*>(&sk[t][i]);
         const float4 y = *reinterpret_cast<const float4*>(&sq[t][i]);
-        pk[0] = fmaf(x.x, s[m], pk[0]); pq[0] = fmaf(y.x, s[m], pq[0]);
-        pk[1] = fmaf(x.y, s[m + 1], pk[1]); pq[1] = fmaf(y.y, s[m + 1], pq[1]);
-        pk[2] = fmaf(x.z, s[m + 2], pk[2]); pq[2] = fmaf(y.z, s[m + 2], pq[2]);
-        pk[3] = fmaf(x.w, s[m + 3], pk[3]); pq[3] = fmaf(y.w, s[m + 3], pq[3]);
+        x[m / 4] = *reinterpret_cast<const float4*>(&sk[t][i]);
+        pk[0] = fmaf(x[m / 4].x, s[m], pk[0]); pq[0] = fmaf(y.x, s[m], pq[0]);
+        pk[1] = fmaf(x[m / 4].y, s[m + 1], pk[1]); pq[1] = fmaf(y.y, s[m + 1], pq[1]);
+        pk[2] = fmaf(x[m / 4].z, s[m + 2], pk[2]); pq[2] = fmaf(y.z, s[m + 2], pq[2]);
+        pk[3] = fmaf(x[m / 4].w, s[m + 3], pk[3]); pq[3] = fmaf(y.w, s[m + 3], pq[3]);
       }
       float dk = (pk[0] + pk[1]) + (pk[2] + pk[3]), dq = (pq[0] + pq[1]) + (pq[2] + pq[3]);
 #pragma unroll
@@ -263,16 +315,14 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
         dk += __shfl_xor_sync(0xffffffffu, dk, o);
         dq += __shfl_xor_sync(0xffffffffu, dq, o);
       }
-      const float eg = s_eg[t], u = s_be[t] * (sv[t][c] - eg * dk);
-      if (rg == 0)
-        put(out + ((int64_t)(tb + t) * Hv + h) * D + c0 + c, fmaf(s_qk[t], u, eg * dq));
+      const float u = f.y * (vt - f.x * dk);
+      if (rg == 0) put(out + ((int64_t)(tb + t) * Hv + h) * D + c0 + c, fmaf(f.z, u, f.x * dq));
 #pragma unroll
       for (int m = 0; m < R; m += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&sk[t][4 * ((m / 4) * RG + rg)]);
-        s[m] = fmaf(x.x, u, eg * s[m]);
-        s[m + 1] = fmaf(x.y, u, eg * s[m + 1]);
-        s[m + 2] = fmaf(x.z, u, eg * s[m + 2]);
-        s[m + 3] = fmaf(x.w, u, eg * s[m + 3]);
+        s[m] = fmaf(x[m / 4].x, u, f.x * s[m]);
+        s[m + 1] = fmaf(x[m / 4].y, u, f.x * s[m + 1]);
+        s[m + 2] = fmaf(x[m / 4].z, u, f.x * s[m + 2]);
+        s[m + 3] = fmaf(x[m / 4].w, u, f.x * s[m + 3]);
       }
     }
   }
@@ -316,7 +366,7 @@ cudaError_t scan_typed(void* out, const void* q, const void* k, const void* v, c
   using Sh = DeltaScan<D>;
   const Strides st = strides_of(d);
   const dim3 grid(D / Sh::COLS, d->num_v_heads, B);
-  delta_scan_kernel<T, D><<<grid, Sh::THREADS, 0, s>>>(
+  delta_scan_kernel<T, D><<<grid, Sh::NT, 0, s>>>(
       (T*)out, (const T*)q, (const T*)k, (const T*)v, g, beta, cu, pool, NS, slots, reset, rows,
       max_len, d->num_v_heads, d->num_v_heads / d->num_qk_heads, st.q, st.k, st.v, d->scale,
       d->qk_norm_eps, status);
