@@ -151,36 +151,32 @@ __device__ __forceinline__ bool make_run(const In& in, int unit, int c0, int c1,
 // chain's part.
 struct Walk {
   Seg sg;
-  int ci;
-  int stage, u;
+  int ci = 0, stage = 0, u = 0;
 };
-__device__ __forceinline__ bool next_run(const In& in, const Plan& pl, Walk& w) {
-  while (w.stage < 3) {
-    bool ok = false;
+__device__ __forceinline__ bool next_chunk(const In& in, const Plan& pl, Walk& w) {
+  if (w.stage > 0 && ++w.ci < w.sg.c1) return true;
+#pragma unroll 1
+  while (true) {
+    int unit = -1, c0 = 0, c1 = -1;
     if (w.stage == 0) {
       w.stage = 1;
       w.u = pl.full_u0;
-      ok = pl.head_u >= 0 && make_run(in, pl.head_u, 0, pl.head_end, w.sg);
+      unit = pl.head_u;
+      c1 = pl.head_end;
+    } else if (w.stage == 1 && w.u < pl.full_u1) {
+      unit = w.u++;
     } else if (w.stage == 1) {
-      if (w.u < pl.full_u1) ok = make_run(in, w.u++, 0, -1, w.sg);
-      else w.stage = 2;
+      w.stage = 2;
+      unit = pl.tail_u;
+      c0 = pl.tail_begin;
     } else {
-      w.stage = 3;
-      ok = pl.tail_u >= 0 && make_run(in, pl.tail_u, pl.tail_begin, -1, w.sg);
+      return false;
     }
-    if (ok) {
+    if (unit >= 0 && make_run(in, unit, c0, c1, w.sg)) {
       w.ci = w.sg.c0;
       return true;
     }
   }
-  return false;
-}
-__device__ __forceinline__ bool first_chunk(const In& in, const Plan& pl, Walk& w) {
-  w.stage = 0;
-  return next_run(in, pl, w);
-}
-__device__ __forceinline__ bool next_chunk(const In& in, const Plan& pl, Walk& w) {
-  return ++w.ci < w.sg.c1 || next_run(in, pl, w);
 }
 
 // ------------------------------------------------------------------ three-term splits
@@ -344,10 +340,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     if (lane == 0) plan_sh = pl;
   }
   __syncthreads();
-  {
-    Walk any;
-    if (!first_chunk(in, plan_sh, any)) return;
-  }
+  if (plan_sh.head_u < 0 && plan_sh.tail_u < 0 && plan_sh.full_u0 >= plan_sh.full_u1) return;
   unsigned long long tag = 0;
   if (cut_chains)
     tag = (*reinterpret_cast<volatile unsigned long long*>(hs) << 32) | (grid_id() & 0xffffffffull);
@@ -875,13 +868,15 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       tma_prefetch_desc(&tv);
     }
     Walk w;
-    bool more = first_chunk(in, plan_sh, w), ended = false;
+    bool more = true, ended = false;
     int ckq = 0, cv = 0;                     // chunks requested
     for (int c = 0;; ++c) {
-      const int st = c % kNKQ, row = w.sg.t0 + w.ci * kC;
+      if (more) more = next_chunk(in, plan_sh, w);
+      const int st = c % kNKQ, row = more ? w.sg.t0 + w.ci * kC : 0;
       const int n = more ? min(kC, w.sg.n - w.ci * kC) : 0;
       // gates and betas of rows lane and lane + 32
-      const int64_t at = (int64_t)row * in.H + w.sg.h + (int64_t)lane * in.H, at2 = at + 32ll * in.H;
+      const int head = more ? w.sg.h : 0;
+      const int64_t at = (int64_t)row * in.H + head + (int64_t)lane * in.H, at2 = at + 32ll * in.H;
       const float ga = lane < n ? g[at] : 0.f, gb = lane + 32 < n ? g[at2] : 0.f;
       const float ba = lane < n ? beta[at] : 0.f, bb = lane + 32 < n ? beta[at2] : 0.f;
       // running sum in units of log 2, exact in integer steps of 2^-36 (fp32 would lose the
@@ -909,12 +904,12 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       G.bt[lane] = ba;
       G.bt[lane + 32] = bb;
       if (lane == 0) {
-        const int flags = (w.ci == w.sg.c0 ? kFirst | (w.sg.zero_start ? kZero : 0) | (w.sg.wait_handoff ? kTake : 0) : 0) |
+        const int flags = !more ? 0 : (w.ci == w.sg.c0 ? kFirst | (w.sg.zero_start ? kZero : 0) | (w.sg.wait_handoff ? kTake : 0) : 0) |
                           (w.ci == w.sg.c1 - 1 ? kLast | (w.sg.publish ? kHand : 0) : 0);
-        chunks[c & 3] = Chunk{w.sg.S, row, n, w.sg.h, flags, {0, 0}};
+        chunks[c & 3] = Chunk{more ? w.sg.S : nullptr, row, n, head, flags, {0, 0}};
       }
       if (n > 0) {
-        const int hk = w.sg.h / rep;
+        const int hk = head / rep;
         if (lane == 0) {
           uint8_t* kq = sm + kOffKQ + st * kStageKQ;
           mbar_expect_tx(&bars->full_kq[st], kStageKQ);
@@ -933,13 +928,12 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           uint8_t* vs = sm + kOffV;
           mbar_expect_tx(&bars->full_v, kStageV);
           for (int sb = 0; sb < 2; ++sb)
-            tma_load_3d(vs + sb * kSubV, &tv, sb * 64, w.sg.h, row, &bars->full_v);
+            tma_load_3d(vs + sb * kSubV, &tv, sb * 64, head, row, &bars->full_v);
         }
         cv = c + 1;
       }
-      if (n > 0) more = next_chunk(in, plan_sh, w);
-      else if (ended) break;               // two end marks: each preparing group gets one
-      else ended = true;
+      if (ended) break;                      // two end marks: each preparing group gets one
+      ended = n == 0;
     }
     if (!ok && lane == 0) {                  // let the loads in flight land before exiting
       flag(status, HYB_DEVERR_TIMEOUT);
