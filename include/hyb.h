@@ -329,7 +329,8 @@ typedef struct {
 /* One token per request: row b of q, k, v, g, beta and out is request b's, its state
  * state_pool[state_slots[b]] is updated in place. A slot outside [0, num_state_slots) sets
  * HYB_DEVERR_BAD_STATE and that request is skipped (its out row is left as it was). Two
- * requests of one call must not share a slot. B = 0 is a no-op; B, num_v_heads <= 65535. */
+ * requests of one call must not share a slot. B = 0 is a no-op; B, num_v_heads <= 65535
+ * and B x num_v_heads < 2^31 (HYB_ERR_UNSUPPORTED beyond), here and in the call below. */
 hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const void* v,
                                   const float* g, const float* beta, float* state_pool,
                                   int32_t num_state_slots, const int32_t* state_slots, int32_t B,
@@ -343,7 +344,7 @@ hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const
  * reset). T (host) is the number of rows of q, k, v, g, beta and out, max_len (host) a bound on
  * every request's rows. A request whose rows are not within [0, T), or more than max_len, sets
  * HYB_DEVERR_BAD_LENGTH, one with a bad slot HYB_DEVERR_BAD_STATE; it is skipped. Rows that
- * belong to no request are left as they were.
+ * belong to no request are left as they were. With T = 0 the rows' pointers may be NULL.
  * bf16 with D = 128 runs the tensor-core kernel (chunks of 64 rows), other shapes the token
  * recurrence on the CUDA cores. `workspace`: device memory, 8-byte aligned, of
  * hyb_gated_delta_chunked_prefill_workspace_size() bytes (a short, misaligned or missing one is

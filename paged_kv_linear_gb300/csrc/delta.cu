@@ -7,12 +7,15 @@
 //     u = beta (v - e^g S^T k),   out = scale (e^g S^T q + (q.k) u),
 // so the two sums over i share their pass and their reduction, and the new state needs no second
 // one. q and k brought to unit length are q / |q| and k / |k|: factors of the sums, never
-// rounded rows.
+// rounded rows. Where the decay is slow, the state decays as S + (e^g - 1) S: e^g rounded to
+// fp32 would be off by the same 2^-25 at every token of a constant gate, and the state by the sum of
+// that over the tokens it keeps. (Where it is fast, that form would lose what is left of S.)
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
-#include "hyb_internal.cuh"
+#include "tc.cuh"
 
 namespace hyb {
 namespace {
@@ -78,7 +81,8 @@ delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
     sh_q[i] = to_f(q[b * qs + (int64_t)(h / rep) * D + i]);
   }
   const T* vr = v + b * vs + (int64_t)h * D + col;
-  const float eg = expf(g[(int64_t)b * Hv + h]), be = beta[(int64_t)b * Hv + h];
+  const float gate = g[(int64_t)b * Hv + h], be = beta[(int64_t)b * Hv + h];
+  const float eg = expf(gate), em1 = expm1f(gate);
   float vv[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) vv[e] = to_f(vr[e]);
@@ -128,12 +132,17 @@ delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) u[e] = be * (vv[e] - eg * (rk * u[e])) * rk;
+  const bool slow = em1 >= -0.5f;
+  const float fade = slow ? em1 : eg;
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const float ki = sh_k[rg + p * RPP];
-    __stcs(reinterpret_cast<float4*>(S + p * RPP * D),
-           make_float4(fmaf(ki, u[0], eg * st[p].x), fmaf(ki, u[1], eg * st[p].y),
-                       fmaf(ki, u[2], eg * st[p].z), fmaf(ki, u[3], eg * st[p].w)));
+    float4 x = st[p];
+    x.x = fmaf(ki, u[0], fmaf(fade, x.x, slow ? x.x : 0.f));
+    x.y = fmaf(ki, u[1], fmaf(fade, x.y, slow ? x.y : 0.f));
+    x.z = fmaf(ki, u[2], fmaf(fade, x.z, slow ? x.z : 0.f));
+    x.w = fmaf(ki, u[3], fmaf(fade, x.w, slow ? x.w : 0.f));
+    __stcs(reinterpret_cast<float4*>(S + p * RPP * D), x);
   }
   if (rg == 0) {
     const float rq = scale * inv_len(sums[1], eps), qk = sums[2];
@@ -195,9 +204,10 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
   using Sh = DeltaScan<D>;
   constexpr int COLS = Sh::COLS, RG = Sh::RG, R = Sh::R, CW = Sh::CW, NT = Sh::NT, TB = Sh::TB;
   constexpr int LQ = Sh::LQ, LV = Sh::LV, LT = Sh::LT;
-  __shared__ __align__(16) float sq[TB][D], sk[TB][D];      // unit (or given) rows; q times scale
+  constexpr int LD = D + 4;                // rows of different tokens start at different banks
+  __shared__ __align__(16) float sq[TB][LD], sk[TB][LD];    // unit (or given) rows; q times scale
   __shared__ __align__(16) float sv[TB][COLS];
-  __shared__ __align__(16) float4 s_f[TB];                  // e^g, beta, q.k
+  __shared__ __align__(16) float4 s_f[TB];                  // e^g, beta, q.k, e^g - 1
 
   const int c0 = blockIdx.x * COLS, h = blockIdx.y, b = blockIdx.z;
   const bool first = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
@@ -242,11 +252,11 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
   };
   fetch(t0);
   // rows 4 (m RG + rg) + e: the RG lanes' 16-byte reads of a staged row lie side by side
-  float s[R];
+  f32x2 s[R / 2];
 #pragma unroll
-  for (int m = 0; m < R; ++m) {
+  for (int m = 0; m < R; m += 2) {
     const int i = 4 * ((m / 4) * RG + rg) + m % 4;
-    s[m] = zero ? 0.f : S[(int64_t)i * D];
+    s[m / 2] = zero ? pair(0.f, 0.f) : pair(S[(int64_t)i * D], S[(int64_t)(i + 1) * D]);
   }
 #pragma unroll 1
   for (int tb = t0; tb < t1; tb += TB) {
@@ -254,8 +264,8 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
 #pragma unroll
     for (int e = 0; e < LQ; ++e) {
       const int i = (threadIdx.x + e * NT) * 4;
-      *reinterpret_cast<float4*>(&sq[0][0] + i) = make_float4(nq[e].x[0], nq[e].x[1], nq[e].x[2], nq[e].x[3]);
-      *reinterpret_cast<float4*>(&sk[0][0] + i) = make_float4(nk[e].x[0], nk[e].x[1], nk[e].x[2], nk[e].x[3]);
+      *reinterpret_cast<float4*>(&sq[i / D][i % D]) = make_float4(nq[e].x[0], nq[e].x[1], nq[e].x[2], nq[e].x[3]);
+      *reinterpret_cast<float4*>(&sk[i / D][i % D]) = make_float4(nk[e].x[0], nk[e].x[1], nk[e].x[2], nk[e].x[3]);
     }
 #pragma unroll
     for (int e = 0; e < LV; ++e) {
@@ -265,6 +275,7 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
     }
     const float fg = ng, fb = nb;
     __syncthreads();
+    bool slow = true;
     if (lt < TB) {                         // lengths and q.k: LT lanes a token
       const int l = threadIdx.x % LT;
       float kk = 0.f, qq = 0.f, qk = 0.f;
@@ -288,48 +299,63 @@ delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
         sk[lt][i] *= rk;
         sq[lt][i] *= rq;
       }
-      if (l == 0) s_f[lt] = make_float4(expf(fg), fb, qk * rk * rq, 0.f);
+      const float em1 = expm1f(fg);
+      slow = em1 >= -0.5f;
+      if (l == 0) s_f[lt] = make_float4(expf(fg), fb, qk * rk * rq, em1);
     }
-    __syncthreads();
+    slow = __syncthreads_and(slow);        // of the whole batch: within a faster one less than half is kept
     if (tb + TB < t1) fetch(tb + TB);
     const int nt = min(TB, t1 - tb);
-#pragma unroll 1
+    T* o_row = out + ((int64_t)tb * Hv + h) * D + c0 + c;
+    auto tokens = [&](auto is_slow) {
+#pragma unroll 2
     for (int t = 0; t < nt; ++t) {
       const float4 f = s_f[t];
       const float vt = sv[t][c];
-      float4 x[R / 4];
-      float pk[4] = {}, pq[4] = {};        // four partial sums each: a shorter chain
+      f32x2 x[R / 2], pk[2], pq[2];        // two sums of pairs each: a shorter chain
 #pragma unroll
-      for (int m = 0; m < R; m += 4) {
-        const int i = 4 * ((m / 4) * RG + rg);
+      for (int e = 0; e < 2; ++e) pk[e] = pq[e] = pair(0.f, 0.f);
+#pragma unroll
+      for (int m = 0; m < R / 2; m += 2) {
+        const int i = 4 * ((m / 2) * RG + rg);
         const float4 y = *reinterpret_cast<const float4*>(&sq[t][i]);
-        x[m / 4] = *reinterpret_cast<const float4*>(&sk[t][i]);
-        pk[0] = fmaf(x[m / 4].x, s[m], pk[0]); pq[0] = fmaf(y.x, s[m], pq[0]);
-        pk[1] = fmaf(x[m / 4].y, s[m + 1], pk[1]); pq[1] = fmaf(y.y, s[m + 1], pq[1]);
-        pk[2] = fmaf(x[m / 4].z, s[m + 2], pk[2]); pq[2] = fmaf(y.z, s[m + 2], pq[2]);
-        pk[3] = fmaf(x[m / 4].w, s[m + 3], pk[3]); pq[3] = fmaf(y.w, s[m + 3], pq[3]);
+        const float4 z = *reinterpret_cast<const float4*>(&sk[t][i]);
+        x[m] = pair(z.x, z.y);
+        x[m + 1] = pair(z.z, z.w);
+        pk[0] = fma2(x[m], s[m], pk[0]);
+        pk[1] = fma2(x[m + 1], s[m + 1], pk[1]);
+        pq[0] = fma2(pair(y.x, y.y), s[m], pq[0]);
+        pq[1] = fma2(pair(y.z, y.w), s[m + 1], pq[1]);
       }
-      float dk = (pk[0] + pk[1]) + (pk[2] + pk[3]), dq = (pq[0] + pq[1]) + (pq[2] + pq[3]);
+      float dk, dk1, dq, dq1;
+      unpair(add2(pk[0], pk[1]), dk, dk1);
+      unpair(add2(pq[0], pq[1]), dq, dq1);
+      dk += dk1;
+      dq += dq1;
 #pragma unroll
       for (int o = CW; o < 32; o <<= 1) {
         dk += __shfl_xor_sync(0xffffffffu, dk, o);
         dq += __shfl_xor_sync(0xffffffffu, dq, o);
       }
       const float u = f.y * (vt - f.x * dk);
-      if (rg == 0) put(out + ((int64_t)(tb + t) * Hv + h) * D + c0 + c, fmaf(f.z, u, f.x * dq));
+      if (rg == 0) put(o_row + (int64_t)t * Hv * D, fmaf(f.z, u, f.x * dq));
+      const float fade = is_slow ? f.w : f.x;
+      const f32x2 u2 = pair(u, u), f2 = pair(fade, fade);
 #pragma unroll
-      for (int m = 0; m < R; m += 4) {
-        s[m] = fmaf(x[m / 4].x, u, f.x * s[m]);
-        s[m + 1] = fmaf(x[m / 4].y, u, f.x * s[m + 1]);
-        s[m + 2] = fmaf(x[m / 4].z, u, f.x * s[m + 2]);
-        s[m + 3] = fmaf(x[m / 4].w, u, f.x * s[m + 3]);
-      }
+      for (int m = 0; m < R / 2; ++m)
+        s[m] = fma2(x[m], u2, is_slow ? fma2(s[m], f2, s[m]) : mul2(s[m], f2));
     }
+    };
+    if (slow) tokens(std::true_type());
+    else tokens(std::false_type());
   }
 #pragma unroll
-  for (int m = 0; m < R; ++m) {
+  for (int m = 0; m < R; m += 2) {
     const int i = 4 * ((m / 4) * RG + rg) + m % 4;
-    S[(int64_t)i * D] = s[m];
+    float a, b;
+    unpair(s[m / 2], a, b);
+    S[(int64_t)i * D] = a;
+    S[(int64_t)(i + 1) * D] = b;
   }
 }
 
@@ -424,17 +450,18 @@ hyb_status_t check_delta_dims(const hyb_delta_dims_t* d) {
   return HYB_OK;
 }
 
+// rows: whether the call has any (their pointers may be null otherwise)
 hyb_status_t check_delta(const void* out, const void* q, const void* k, const void* v,
                          const float* g, const float* beta, const float* pool, int NS,
-                         const int32_t* slots, int B, const hyb_delta_dims_t* d) {
+                         const int32_t* slots, int B, bool rows, const hyb_delta_dims_t* d) {
   const hyb_status_t st = check_delta_dims(d);
   if (st != HYB_OK) return st;
   if (B < 0 || NS <= 0) return HYB_ERR_INVALID_ARG;
-  if (B > 65535) return HYB_ERR_UNSUPPORTED;               // grid.z
+  if (B > 65535 || (int64_t)B * d->num_v_heads > INT32_MAX) return HYB_ERR_UNSUPPORTED;   // grid.z; chains
   if ((int64_t)NS * d->num_v_heads * d->head_dim * d->head_dim > ((int64_t)1 << 40))
     return HYB_ERR_UNSUPPORTED;
   if (B == 0) return HYB_OK;
-  if (!out || !q || !k || !v || !g || !beta || !pool || !slots) return HYB_ERR_INVALID_ARG;
+  if (!pool || !slots || (rows && (!out || !q || !k || !v || !g || !beta))) return HYB_ERR_INVALID_ARG;
   if (!al(out, 16) || !al(q, 16) || !al(k, 16) || !al(v, 16) || !al(pool, 16) || !al(g, 4) ||
       !al(beta, 4) || !al(slots, 4))
     return HYB_ERR_INVALID_ARG;
@@ -453,7 +480,7 @@ hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const
                                   int32_t num_state_slots, const int32_t* state_slots, int32_t B,
                                   const hyb_delta_dims_t* d, void* stream) {
   const hyb_status_t st =
-      check_delta(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, d);
+      check_delta(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, true, d);
   if (st != HYB_OK || B == 0) return st;
   unsigned* sw = status_word();
   if (!sw) return HYB_ERR_CUDA;
@@ -475,7 +502,7 @@ hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const voi
                                              int32_t max_len, const hyb_delta_dims_t* d,
                                              void* workspace, size_t ws_bytes, void* stream) {
   const hyb_status_t st =
-      check_delta(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, d);
+      check_delta(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, T > 0, d);
   if (st != HYB_OK) return st;
   if (T < 0 || max_len < 0 || max_len > T) return HYB_ERR_INVALID_ARG;
   if (B == 0) return HYB_OK;
@@ -483,7 +510,7 @@ hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const voi
   if (!workspace || !al(workspace, 8) || ws_bytes < kLinPrefillWsBytes) return HYB_ERR_INVALID_ARG;
   unsigned* sw = status_word();
   if (!sw) return HYB_ERR_CUDA;
-  if (delta_prefill_tc_supported(d)) {
+  if (delta_prefill_tc_supported(d) && T > 0) {   // (no rows: only the resets are left)
     const Strides x = strides_of(d);
     return cuda_status(launch_delta_prefill_tc(out, q, k, v, g, beta, cu_seqlens, state_pool,
                                                num_state_slots, state_slots, reset, B, T, max_len,

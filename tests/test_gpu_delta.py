@@ -151,6 +151,31 @@ def test_step_bad_slot_is_flagged_and_skipped(hyb, devstatus):
     assert np.array_equal(host(c.pool)[[0, 1, 3]], before[[0, 1, 3]])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gate", [-12.0, -0.75, -0.6, -1e-3])
+def test_decay_alone_keeps_its_precision(hyb, D, gate):
+    """With beta 0 the state only fades: every element to a few roundings of its own value, after one
+    token and after many of the same gate (T tokens: T of them, at most u T in all)."""
+    for T in (1, 3, 200):
+        c = Case(5, T, 1, 1, D, torch.float32, 1, gate="none")
+        c.g.fill_(gate)
+        c.beta.zero_()
+        g32 = float(c.g[0, 0])
+        S0 = host(c.pool)[0, 0]
+        out = torch.empty(T, 1, D, device="cuda")
+        slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+        if T == 1:
+            step(hyb, c, out, slots, 1)
+        else:
+            prefill(hyb, c, out, torch.tensor([0, T], dtype=torch.int32, device="cuda"), slots, None)
+        ref = S0 * math.exp(g32 * T)
+        live = np.abs(ref) > 1e-30          # below, fp32 itself loses bits
+        err = np.abs(host(c.pool)[0, 0] - ref)[live]
+        # a token rounds once (half an ulp is at most u of the value) and, in the slow form, e^g - 1 is off
+        # by 2 u |e^g - 1| / e^g, in the fast one e^g by 2 u: 4 u T covers both
+        assert (err <= 4 * R.U * T * np.abs(ref)[live]).all(), (gate, T, (err / np.abs(ref)[live]).max() / R.U)
+
+
 # -------------------------------------------------------------------------------- prefill
 @pytest.mark.parametrize("D,dt", [(16, torch.float32), (32, torch.bfloat16), (64, torch.float32), (64, torch.bfloat16), (128, torch.float32), (256, torch.bfloat16), (128, torch.bfloat16)])
 @pytest.mark.parametrize("lens,reset", [([1], None), ([64, 0, 63, 65, 0], [0, 0, 1, 0, 1]), ([17, 130, 1], None)])
@@ -243,6 +268,47 @@ def test_prefill_bad_requests_are_flagged_and_skipped(hyb, devstatus, D, dt):
     for _ in range(2):                                      # the good request ran twice
         o, S, mag, norm = c.ref(slice(10, 30), S)
     R.check_out(got[10:30], o, mag, HALF[dt], 40, "out", split=dt == torch.bfloat16)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_prefill_without_rows_resets_and_keeps(hyb, devstatus, dt):
+    c = Case(20, 1, 2, 2, 128, dt, 3)
+    before = host(c.pool)
+    d = c.dims(hyb)
+    ws = torch.empty(hyb.hyb_gated_delta_chunked_prefill_workspace_size(2, 0, d), dtype=torch.uint8, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([2, 0], dtype=torch.int32, device="cuda")
+    reset = torch.tensor([1, 0], dtype=torch.uint8, device="cuda")
+    hyb.check(hyb.hyb_gated_delta_chunked_prefill(None, None, None, None, None, None, cu, c.pool, 3, slots, reset, 2, 0, 0, d, ws, ws.numel()))
+    assert devstatus() == (0, 0)
+    assert (host(c.pool)[2] == 0).all() and np.array_equal(host(c.pool)[:2], before[:2])
+
+
+def test_prefill_one_chain_per_sm_and_more(hyb):
+    """Chains at and around the number of SMs: the boundary between one chain a CTA and the cut
+    work split."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for chains in (sms - 1, sms, sms + 1, 2 * sms + 1):
+        lens = [int(n) for n in np.random.RandomState(chains).randint(1, 140, chains)]
+        c = Case(chains, sum(lens), 1, 1, 128, torch.bfloat16, chains)
+        check_prefill(hyb, c, lens, None, f"{chains} chains")
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_prefill_nan_gate_and_growth(hyb, dt):
+    """A NaN gate makes its head's state NaN from its row on; a gate above 0 lets it grow."""
+    c = Case(21, 100, 1, 2, 128, dt, 1)
+    c.g[:, 0] = 0.02
+    c.g[70, 1] = math.nan
+    S0 = host(c.pool)[0]
+    out = torch.empty(100, 2, 128, device="cuda", dtype=dt)
+    prefill(hyb, c, out, torch.tensor([0, 100], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), None)
+    with np.errstate(invalid="ignore"):
+        o, S, mag, norm = c.ref(slice(0, 100), S0)
+    R.check_out(host(out)[:, :1], o[:, :1], mag[:, :1], HALF[dt], 100, "head 0", split=dt == torch.bfloat16)
+    R.check_state(host(c.pool)[0, :1], S[:1], norm[:1], 100, "head 0")
+    assert np.isnan(host(out)[70:, 1]).all() and np.isnan(host(c.pool)[0, 1]).all()
+    assert np.isfinite(host(out)[:64, 1]).all()
 
 
 def test_prefill_nan_stays_in_its_request(hyb):

@@ -69,6 +69,12 @@ def test_delta_arguments_refused(hyb):
     assert pre(ws=None) == inv and pre(ws=F + 4) == inv and pre(nb=n - 1) == inv
     assert pre(B=65536) == uns and pre(NS=0) == inv and pre(sl=None) == inv
     assert pre(B=0, ws=None, nb=0) == ok
+    # more chains than the work split counts
+    many = hyb.delta_dims(1, 65535, 128)
+    assert hyb.hyb_gated_delta_step(*(F,) * 7, 4, F, 65535, many, 0) == uns
+    # rows may be missing only where there are none
+    rows = lambda T: hyb.hyb_gated_delta_chunked_prefill(None, F, F, F, F, F, F, F, 4, F, None, 2, T, 0, d, F, n, 0)
+    assert rows(1) == inv
 
 
 def test_rope_refused(hyb):
