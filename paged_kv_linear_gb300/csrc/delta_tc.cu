@@ -989,7 +989,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           tc_fence_after();
 #pragma unroll
           for (int y = 0; y < 12; ++y) {
-            const int k = (y & 1) + ((y & 2) << 1) + 2 * x, term = y >> 2;
+            const int k = (y & 1) + ((y & 2) << 1) + 2 * x, term = 2 - (y >> 2);
             tc_mma_ta(tmem + kCol1K, tmem + kColSA + term * 64 + k * 8, desc_add(km0, kq + (k >> 2) * kSubKQ + (k & 3) * 32), kIdesc64, x + y > 0);
           }
           if (x == 1) tc_commit(&bars->d1k_ready);
@@ -1018,8 +1018,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           tc_fence_after();
           const uint64_t wd = desc_add(km0, kOffW);
 #pragma unroll
-          for (int y = 0; y < 6; ++y) {      // R h W h, h m, m h, h l, m m, l h
-            const int r = y == 2 || y == 4 ? 1 : y == 5 ? 2 : 0, t = y == 1 || y == 4 ? 1 : y == 3 ? 2 : 0;
+          for (int y = 0; y < 6; ++y) {      // R l W h, m m, h l, m h, h m, h h
+            const int r = y == 3 || y == 1 ? 1 : y == 0 ? 2 : 0, t = y == 4 || y == 1 ? 1 : y == 2 ? 2 : 0;
             const uint32_t ra = r == 0 ? kColRh : r == 1 ? kColRm : kColRl;
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
@@ -1041,7 +1041,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
           for (int y = 0; y < 6; ++y) {
             const int k = x + 2 * (y & 1);
-            tc_mma_ta(tmem + kColS, tmem + kColXh + (y >> 1) * 32 + k * 8, desc_add(mn0, kq + k * 2048), kIdescS, 1);
+            tc_mma_ta(tmem + kColS, tmem + kColXh + (2 - (y >> 1)) * 32 + k * 8, desc_add(mn0, kq + k * 2048), kIdescS, 1);
           }
           if (x == 1) {
             tc_commit(&bars->s_ready);
