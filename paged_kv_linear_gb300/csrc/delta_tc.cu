@@ -86,7 +86,7 @@ struct Bars {
   uint64_t w_ready[2], o_free[2];
   uint64_t sa_ready[2], ra_ready[2], xa_ready[2];   // an operand's first and second half
   uint64_t d0_ready[2], d0_free, d1k_ready, d1q_ready, x_ready, s_ready;
-  uint64_t q_scaled, o_ready, d1q_free, published, drain;
+  uint64_t om_ready, q_scaled, o_ready, d1q_free, published, drain;
 };
 constexpr int kSmem = kOffBar + 512 + 1024;    // + slack for 1024-byte alignment
 static_assert(sizeof(Bars) <= 512 && kOffG % 16 == 0 && kOffBar % 8 == 0 && kSmem <= 227 * 1024, "smem");
@@ -95,14 +95,17 @@ constexpr int kWarpMain = 8, kWarpOut = 16, kWarpFeed = 20, kWarpMma = 21;
 constexpr int kThreads = 22 * 32;
 constexpr int kChainCost = 1;                  // chunks that a chain's state costs (work split)
 constexpr uint32_t kTmemCols = 512;
-// D0 | D1K | D1Q | S fp32 | operand terms of S. Once (k) and (q) have read the terms, R, X and X'
-// take their places: R's h and m over S's l, R's l inside D1K (each thread over columns that only
-// it reads); X over S's h; X' over S's m and R's h; X's two terms for (o) over D1K.
+// D0 | D1K | D1Q | S fp32 | operand terms of S (per 16 key dims 8 columns of h and 8 of m; l).
+// Once (k) and (q) have read the terms, others take their places: R's h and m over S's l, R's l
+// inside D1K (each thread over columns that only it reads); X over the first half of S's h and m.
+// After (w), X' goes over R's h and m and over D1K's second half, X's h for (o) over its first;
+// the state's change over all of S's h and m, each 16 columns of it where the same thread's next
+// terms will be. X's m takes the place of the l of X' when (s) has used that.
 constexpr uint32_t kCol0 = 0, kCol1K = 64, kCol1Q = 128, kColS = 192, kColSA = 320;
 constexpr uint32_t kColRh = kColSA + 128, kColRm = kColSA + 160, kColRl = kCol1K + 16;
-constexpr uint32_t kColX = kColSA;
-constexpr uint32_t kColXh = kColSA + 64, kColXm = kColSA + 96, kColXl = kColSA + 128;
-constexpr uint32_t kColOh = kCol1K, kColOm = kCol1K + 32;
+constexpr uint32_t kColX = kColSA, kColDS = kColSA;
+constexpr uint32_t kColXh = kColSA + 128, kColXm = kColSA + 160, kColXl = kCol1K + 32;
+constexpr uint32_t kColOh = kCol1K;
 
 constexpr uint32_t kIdesc64 = idesc_bf16(128, 64, 0, 0);
 constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 1);   // B = K rows as K^T: N (key dim) major
@@ -298,14 +301,16 @@ __device__ __forceinline__ void put_terms(uint32_t h_at, uint32_t m_at, uint32_t
   tmem_st8u(m_at, m);
   tmem_st8u(l_at, l);
 }
-// 16 values of this lane's state (key dims i0 ..): operand terms, and the accumulator times the
-// coming chunk's decay
-__device__ __forceinline__ void put_state(uint32_t tl, int i0, float* v, float dec) {
-  put_terms(tl + kColSA + i0 / 2, tl + kColSA + 64 + i0 / 2, tl + kColSA + 128 + i0 / 2, v);
+// 16 values of this lane's state (key dims i0 ..) as (s) left them: the old ones times the chunk's
+// decay plus their change, rounded to nearest
+__device__ __forceinline__ void get_state(uint32_t tl, int i0, float dec, float* v) {
+  float x[16];
+  tmem_ld16(tl + kColS + i0, v);
+  tmem_ld16(tl + kColDS + i0, x);
+  tmem_ld_wait();
   const f32x2 d2 = pair(dec, dec);
 #pragma unroll
-  for (int e = 0; e < 16; e += 2) unpair(mul2(pair(v[e], v[e + 1]), d2), v[e], v[e + 1]);
-  tmem_st16(tl + kColS + i0, v);
+  for (int e = 0; e < 16; e += 2) unpair(fma2(pair(v[e], v[e + 1]), d2, pair(x[e], x[e + 1])), v[e], v[e + 1]);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -383,6 +388,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       mbar_init(&bars->q_scaled, 128);
       mbar_init(&bars->d1q_free, 128);
       mbar_init(&bars->o_ready, 1);
+      mbar_init(&bars->om_ready, 256);
       mbar_init(&bars->published, 256);
       mbar_init(&bars->drain, 1);
       fence_mbar_init();
@@ -653,6 +659,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     // Rows in two pieces of 16 (the lower half of the rows starts with its second, see R below).
     const int xa = x0 + (half ? 0 : 16), xb = x0 + (half ? 16 : 0);
     int n = 0, flags = 0;
+    float dec = 0.f;                         // of the chunk before
     uint32_t v[16];                          // pairs of rows of V, this column
     // Chunk c's description, gates and V: fetched while the chunk before is under way.
     auto fetch = [&](int c) -> bool {
@@ -679,7 +686,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         }
       }
       mbar_arrive(&bars->free_v);
-      return HYB_WAIT(bars->gates[c & 3], (c >> 2) & 1);
+      return true;
     };
     ok = fetch(0);
     for (int c = 0; ok && n > 0; ++c) {
@@ -702,19 +709,18 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       {
         const bool from_tmem = !(flags & kFirst), from_pool = !(flags & kZero);
-        const float dec = G.dec;
 #pragma unroll 1
         for (int x = 0; x < 4; ++x) {        // pieces of 16 key dims; (k) starts with the first two
           const int i = i0 + 16 * x;
           float s[16];
           if (from_tmem) {
-            tmem_ld16(tl + kColS + i, s);
-            tmem_ld_wait();
+            get_state(tl, i, dec, s);
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = from_pool ? __ldcg(S + (i + e) * kD + j) : 0.f;
           }
-          put_state(tl, i, s, dec);
+          put_terms(tl + kColSA + i, tl + kColSA + i + 8, tl + kColSA + 128 + i / 2, s);
+          tmem_st16(tl + kColS + i, s);
           if (x & 1) {
             tmem_st_wait();
             tc_fence_before();
@@ -723,7 +729,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         }
       }
       // R = V - e^G K S (beta is in W)
-      ok = HYB_WAIT(bars->d1k_ready, c & 1);
+      ok = HYB_WAIT(bars->gates[c & 3], (c >> 2) & 1) && HYB_WAIT(bars->d1k_ready, c & 1);
       if (!ok) break;
       tc_fence_after();
       // R's l goes to columns 16-47 of D1K: the thread's own 16 first rows of d may lie there, so the
@@ -746,34 +752,46 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         tc_fence_before();
         mbar_arrive(&bars->ra_ready[x]);
       }
-      // X: times its way to the chunk's end for the state, and as it is for the outputs
-      ok = HYB_WAIT(bars->x_ready, c & 1);
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int x = 0; x < 32; x += 16) {
-        float d[16];
-        tmem_ld16(tl + kColX + x0 + x, d);
-        tmem_ld_wait();
-        const int at = (x0 + x) / 2;
-        uint32_t h[8], m[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split2(d[2 * e], d[2 * e + 1], h[e], m[e]);
-        tmem_st8u(tl + kColOh + at, h);
-        tmem_st8u(tl + kColOm + at, m);
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(&G.wX[x0 + x + e]);
-          unpair(mul2(pair(a.x, a.y), pair(d[e], d[e + 1])), d[e], d[e + 1]);
-          unpair(mul2(pair(a.z, a.w), pair(d[e + 2], d[e + 3])), d[e + 2], d[e + 3]);
-        }
-        put_terms(tl + kColXh + at, tl + kColXm + at, tl + kColXl + at, d);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bars->xa_ready[x >> 4]);
-      }
+      // X: times its way to the chunk's end for the state, and as it is for the outputs. All of it is
+      // read before the first half is announced: the state's change goes over it.
       ok = fetch(c + 1);
       if (!ok) break;
+      ok = HYB_WAIT(bars->x_ready, c & 1) && HYB_WAIT(bars->free_v, (c + (n > 0)) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      {
+        float d[16];
+        tmem_ld16(tl + kColX + x0, d);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int at = x0 / 2 + 8 * x;
+          uint32_t h[8], m[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) split2(d[2 * e], d[2 * e + 1], h[e], m[e]);
+          tmem_st8u(tl + kColOh + at, h);
+          uint8_t* om = sm + kOffV + j * 128;
+          *reinterpret_cast<uint4*>(om + (((at >> 2) ^ (j & 7)) << 4)) = make_uint4(m[0], m[1], m[2], m[3]);
+          *reinterpret_cast<uint4*>(om + (((at >> 2) + 1 ^ (j & 7)) << 4)) = make_uint4(m[4], m[5], m[6], m[7]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(&G.wX[x0 + 16 * x + e]);
+            unpair(mul2(pair(a.x, a.y), pair(d[e], d[e + 1])), d[e], d[e + 1]);
+            unpair(mul2(pair(a.z, a.w), pair(d[e + 2], d[e + 3])), d[e + 2], d[e + 3]);
+          }
+          put_terms(tl + kColXh + at, tl + kColXm + at, tl + kColXl + at, d);
+          if (x == 0) {
+            tmem_ld16(tl + kColX + x0 + 16, d);
+            tmem_ld_wait();
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bars->xa_ready[x]);
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(&bars->om_ready);
+      dec = G.dec;
       // the chunk's last state
       ok = HYB_WAIT(bars->s_ready, c & 1);
       if (!ok) break;
@@ -782,8 +800,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll 1
         for (int i = i0; i < i0 + 64; i += 16) {
           float s[16];
-          tmem_ld16(tl + kColS + i, s);
-          tmem_ld_wait();
+          get_state(tl, i, dec, s);
 #pragma unroll
           for (int e = 0; e < 16; ++e) S[(i + e) * kD + j] = s[e];
         }
@@ -922,7 +939,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       mbar_arrive(&bars->info[c & 3]);
       if (n > 0) {
-        if (c >= 1) ok = HYB_WAIT(bars->free_v, (c - 1) & 1);
+        if (c == 1) ok = HYB_WAIT(bars->free_v, 0);
+        if (c >= 2) ok = HYB_WAIT(bars->o_ready, c & 1);   // (o) of chunk c - 2 has read X's terms
         if (!ok) break;
         if (lane == 0) {
           uint8_t* vs = sm + kOffV;
@@ -990,7 +1008,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
           for (int y = 0; y < 12; ++y) {
             const int k = (y & 1) + ((y & 2) << 1) + 2 * x, term = 2 - (y >> 2);
-            tc_mma_ta(tmem + kCol1K, tmem + kColSA + term * 64 + k * 8, desc_add(km0, kq + (k >> 2) * kSubKQ + (k & 3) * 32), kIdesc64, x + y > 0);
+            tc_mma_ta(tmem + kCol1K, tmem + kColSA + (term == 2 ? 128 + k * 8 : k * 16 + term * 8), desc_add(km0, kq + (k >> 2) * kSubKQ + (k & 3) * 32), kIdesc64, x + y > 0);
           }
           if (x == 1) tc_commit(&bars->d1k_ready);
         }
@@ -1004,7 +1022,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
         for (int x = 0; x < 16; ++x) {       // (q)
           const int k = x & 7;
-          tc_mma_ta(tmem + kCol1Q, tmem + kColSA + x * 8, desc_add(km0, kq + 64 * 128 + (k >> 2) * kSubKQ + (k & 3) * 32), kIdesc64, x > 0);
+          tc_mma_ta(tmem + kCol1Q, tmem + kColSA + k * 16 + (x >> 3) * 8, desc_add(km0, kq + 64 * 128 + (k >> 2) * kSubKQ + (k & 3) * 32), kIdesc64, x > 0);
         }
         tc_commit(&bars->d1q_ready);
       }
@@ -1041,7 +1059,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
           for (int y = 0; y < 6; ++y) {
             const int k = x + 2 * (y & 1);
-            tc_mma_ta(tmem + kColS, tmem + kColXh + (2 - (y >> 1)) * 32 + k * 8, desc_add(mn0, kq + k * 2048), kIdescS, 1);
+            const uint32_t xt = y < 2 ? kColXl : y < 4 ? kColXm : kColXh;
+            tc_mma_ta(tmem + kColDS, tmem + xt + k * 8, desc_add(mn0, kq + k * 2048), kIdescS, x + y > 0);
           }
           if (x == 1) {
             tc_commit(&bars->s_ready);
@@ -1051,7 +1070,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         __syncwarp();
       }
       if (!ok) break;
-      ok = HYB_WAIT(bars->q_scaled, c & 1);
+      ok = HYB_WAIT(bars->q_scaled, c & 1) && HYB_WAIT(bars->om_ready, c & 1);
       if (!ok) break;
       if (elect_one()) {
         tc_fence_after();
@@ -1059,8 +1078,10 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll
         for (int x = 0; x < 3; ++x) {        // (o): X h P h, h m, m h
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_ta(tmem + kCol1Q, tmem + (x == 2 ? kColOm : kColOh) + k * 8, desc_add(pd, (x == 1 ? kTile64 : 0) + k * 32), kIdesc64, 1);
+          for (int k = 0; k < 4; ++k) {
+            if (x == 2) tc_mma(tmem + kCol1Q, desc_add(km0, kOffV + k * 32), desc_add(pd, k * 32), kIdesc64, 1);
+            else tc_mma_ta(tmem + kCol1Q, tmem + kColOh + k * 8, desc_add(pd, x * kTile64 + k * 32), kIdesc64, 1);
+          }
         }
         tc_commit(&bars->o_ready);
       }

@@ -210,6 +210,27 @@ def test_prefill_same_key_every_token(hyb, dt):
     check_prefill(hyb, c, [140], None, "one key")
 
 
+def test_prefill_long_prompt_of_small_changes_does_not_drift(hyb):
+    """A state that is kept (no decay) and changed little: rounded to nearest once in 64 rows it is
+    off by u sqrt(T / 64) of its norm. Each 64 rows' change is a sum of 12 products cut to 24 bits
+    (2 u each) of corrections that 24 such products make: 2 x 36 u of that change's norm at most.
+    Were the state itself cut 12 times in 64 rows, towards zero, it would be off by 1.5e-5 here."""
+    T, u = 4096, 2.0 ** -24
+    c = Case(22, T, 1, 2, 128, torch.bfloat16, 1, gate="none")
+    c.beta *= 0.01
+    S = host(c.pool)[0]
+    out = torch.empty(T, 2, 128, device="cuda", dtype=torch.bfloat16)
+    prefill(hyb, c, out, torch.tensor([0, T], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), None)
+    change, most = np.zeros(2), np.zeros(2)
+    for t in range(0, T, 64):
+        o, S1, mag, norm = c.ref(slice(t, t + 64), S)
+        change += np.sqrt(((S1 - S) ** 2).sum((1, 2)))
+        most, S = np.maximum(most, norm), S1
+    err = np.sqrt(((host(c.pool)[0] - S) ** 2).sum((1, 2)))
+    lim = u * (math.sqrt(T / 64) * most + 72 * change)
+    assert (lim < 5e-6 * most).all() and (err <= lim).all(), (err / most, lim / most)
+
+
 def test_prefill_many_ragged_chains(hyb):
     """More chains than the GPU has SMs, with empty and short ones: chains are shared out."""
     rs = np.random.RandomState(5)
