@@ -16,27 +16,45 @@
 // bf16 tensor cores: K and Q are bf16 as given (their lengths, decays, beta and scale go into
 // fp32 factors of rows and columns, never into rounded operands), and S, W, the right-hand side R
 // and the corrections are each cut into three bf16 terms, h + m + l, which hold an fp32 number
-// without loss. K S and the state's sum then are exact products; of W R the terms beyond 2^-24 are
-// left out (six of nine products). The outputs, rounded to bf16 in the end, take two terms of S, X
-// and P (about 2^-16). With two terms throughout, states were off by some 3e-6 instead of 3e-7.
+// without loss. K S and the state's change then are exact products; of W R the terms beyond 2^-24
+// are left out (six of nine products). The tensor core's fp32 sums are cut, not rounded, at 24
+// bits: products go in with the smallest terms first, and the state's change is summed by itself
+// and then added to the state times its decay in one fp32 fma. (Summed up in the state's own
+// accumulator, 12 cuts towards zero in 64 rows, 8192 rows of small changes put it off by 3.0e-5;
+// now 3.3e-7, the fp32 recurrence 2.3e-6.) The outputs, rounded to bf16 in the end, take two terms
+// of S, X and P (about 2^-16). With two terms throughout, states were off by some 3e-6; now by
+// 1.5e-7 after 77 rows, 2e-7 after 4096.
 //
 // Layout. Everything on the chain is kept transposed: TMEM lane j is the state's value column j, so
 // each thread owns a column (half of its columns' range), nothing on the chain crosses threads, and
 // the results (accumulators in TMEM) become the next product's A operand by the same thread
-// writing them back as bf16 terms; shared memory holds only what TMA brings (K, Q, V) and W and P.
+// writing them back as bf16 terms; shared memory holds only what TMA brings (K, Q, V), W and P, and
+// X's second term, for which TMEM has no columns left.
 //   (k) D1K[j][t] = S^T K^T     A = S (TMEM, 3 terms),  B = K rows     24 MMAs 128 x 64 x 16
 //   (q) D1Q[j][t] = S^T Q^T     A = S (TMEM, 2 terms),  B = Q rows     16
-//   (0) [K; Q] K^T of the next chunk (128 x 64)                         8
+//   (0) [K; Q] K^T, two chunks ahead (128 x 64)                         8
 //   (w) X^T       = R^T W^T     A = R (TMEM),  B = W rows (6 pairs)    24
-//   (s) S^T      += X'^T K      A = X e^(G_C - G) (TMEM), B = K^T       12 MMAs 128 x 128 x 16
-//   (o) D1Q       = X^T P^T     A = X (TMEM, 2 terms), B = P (3 pairs) 12
-// The state's fp32 accumulator stays in TMEM; whoever reads a chunk's final state to cut it into
-// terms writes it back times the next chunk's decay.
+//   (s) dS^T      = X'^T K      A = X e^(G_C - G) (TMEM), B = K^T      12 MMAs 128 x 128 x 16
+//   (o) D1Q       = X^T P^T     A = X (2 terms), B = P (3 pairs)       12
+// MMAs of N = 64 take 34 cycles of the tensor core, N = 128 67: 3.9K cycles a chunk.
 //
-// Warps: 0-3 prepare a chunk (lengths, gates, W, P), one chunk ahead of 4-11, which carry the
-// chain (two warps to 32 lanes, each half of the columns); 12-15 write outputs; 16 issues TMA
-// loads (two stages), 17 the MMAs. Chains are shared out over the CTAs as in chain_split.cuh: the
-// 256 chains of 8 requests x 32 heads would leave the second wave of 152 CTAs a third full.
+// W = (1 + A)^-1 in fp32 on the warps' own MMAs (tf32, two terms each) by blocks of 8, 16, 32 and 64.
+//
+// Warps: 0-7 prepare chunks (lengths, factors, W, P), two groups of four with a chunk each, so a
+// chunk's preparation may take two chunks' time; 8-15 carry the chain (two warps to 32 lanes, each
+// half of the columns); 16-19 scale and write outputs; 20 walks the CTA's chunks, sums the gates
+// and issues TMA loads (three stages of K and Q, one of V, which the chain keeps in registers); 21
+// issues the MMAs. Chains are shared out over the CTAs as in chain_split.cuh: the 256 chains of 8
+// requests x 32 heads would leave the second wave of 152 CTAs a third full.
+//
+// What bounds it: a chunk's way round its three loops (chain, preparation, outputs), each about 10K
+// cycles of waits for one another; leaving any one piece of work out changes the time by 0-3 %.
+// 8 requests of 8192 rows, 32 heads: 1.19 ms (tensor pipe 38 % busy, issue slots 51 %, 1.9 TB/s;
+// 0.27 of what its bytes take at the copy rate); one request of 4096 rows: 321 us, 5.0 us a
+// chunk; one of 77: 20 us. On the way, 8 x 8192: 13.5 ms token by token -> 2.54 (this design) -> 1.94
+// (elected MMA issue, integer gate sums, chunk descriptors instead of local arrays) -> 1.56 (two
+// preparing groups) -> 1.42 (warp MMAs in W) -> 1.19 (rolled loops: the code no longer fell out of the
+// instruction cache) -> 1.12 (one site for a run's setup) -> 1.19 (the state rounded to nearest).
 #include <cuda_bf16.h>
 
 #include "chain_split.cuh"
@@ -93,14 +111,18 @@ static_assert(sizeof(Bars) <= 512 && kOffG % 16 == 0 && kOffBar % 8 == 0 && kSme
 
 constexpr int kWarpMain = 8, kWarpOut = 16, kWarpFeed = 20, kWarpMma = 21;
 constexpr int kThreads = 22 * 32;
-constexpr int kChainCost = 1;                  // chunks that a chain's state costs (work split)
+// Chunks that a chain's state (a read and a write of 64 KB, nothing under way meanwhile) counts as in
+// the work split: 24 ragged requests of up to 5000 rows take 632 us with 0, 480 with 1, 477 with 2;
+// 8 x 8192 1.21, 1.19 and 1.19 ms.
+constexpr int kChainCost = 1;
 constexpr uint32_t kTmemCols = 512;
-// D0 | D1K | D1Q | S fp32 | operand terms of S (per 16 key dims 8 columns of h and 8 of m; l).
+// D0 | D1K | D1Q | S fp32 | operand terms of S (per 16 key dims 8 columns of h and 8 of m; then l).
 // Once (k) and (q) have read the terms, others take their places: R's h and m over S's l, R's l
 // inside D1K (each thread over columns that only it reads); X over the first half of S's h and m.
-// After (w), X' goes over R's h and m and over D1K's second half, X's h for (o) over its first;
-// the state's change over all of S's h and m, each 16 columns of it where the same thread's next
-// terms will be. X's m takes the place of the l of X' when (s) has used that.
+// After (w), X' goes over R's h and m and over D1K's second half, X's h for (o) over its first; the
+// state's change over all of S's h and m, each 16 columns of it where the same thread's next
+// terms will be. X's m lies in V's buffer, once every thread has V in its registers: the next V
+// is loaded when (o) is done.
 constexpr uint32_t kCol0 = 0, kCol1K = 64, kCol1Q = 128, kColS = 192, kColSA = 320;
 constexpr uint32_t kColRh = kColSA + 128, kColRm = kColSA + 160, kColRl = kCol1K + 16;
 constexpr uint32_t kColX = kColSA, kColDS = kColSA;
@@ -661,7 +683,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     int n = 0, flags = 0;
     float dec = 0.f;                         // of the chunk before
     uint32_t v[16];                          // pairs of rows of V, this column
-    // Chunk c's description, gates and V: fetched while the chunk before is under way.
+    // Chunk c's description and V: fetched while the chunk before is under way.
     auto fetch = [&](int c) -> bool {
       if (!HYB_WAIT(bars->info[c & 3], (c >> 2) & 1)) return false;
       n = chunks[c & 3].n;
@@ -752,10 +774,11 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
         tc_fence_before();
         mbar_arrive(&bars->ra_ready[x]);
       }
-      // X: times its way to the chunk's end for the state, and as it is for the outputs. All of it is
-      // read before the first half is announced: the state's change goes over it.
       ok = fetch(c + 1);
       if (!ok) break;
+      // X: times its way to the chunk's end for the state, and as it is for the outputs. All of it is
+      // read before the first half is announced: the state's change goes over it. V's buffer is
+      // free for X's second term once all have fetched from it.
       ok = HYB_WAIT(bars->x_ready, c & 1) && HYB_WAIT(bars->free_v, (c + (n > 0)) & 1);
       if (!ok) break;
       tc_fence_after();
@@ -772,7 +795,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           tmem_st8u(tl + kColOh + at, h);
           uint8_t* om = sm + kOffV + j * 128;
           *reinterpret_cast<uint4*>(om + (((at >> 2) ^ (j & 7)) << 4)) = make_uint4(m[0], m[1], m[2], m[3]);
-          *reinterpret_cast<uint4*>(om + (((at >> 2) + 1 ^ (j & 7)) << 4)) = make_uint4(m[4], m[5], m[6], m[7]);
+          *reinterpret_cast<uint4*>(om + ((((at >> 2) + 1) ^ (j & 7)) << 4)) = make_uint4(m[4], m[5], m[6], m[7]);
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const float4 a = *reinterpret_cast<const float4*>(&G.wX[x0 + 16 * x + e]);

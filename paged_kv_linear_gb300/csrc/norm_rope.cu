@@ -8,7 +8,11 @@
 // in two the same way. The token's rot_dim / 2 cosines and sines are computed once per warp, by
 // all lanes; a lane folds those of its pairs and the weights into 16 factors, so that a row's
 // element takes two products and the norm's one. The loads of kU rounds of rows are in flight
-// together.
+// together, and the next kU rounds' while these are worked on: 110 registers, two CTAs per SM.
+//
+// 65536 tokens of 32 + 2 x 8 heads of 128, bf16, from rows of a fused projection: 270 us, 6.0 TB/s, 0.88
+// of the copy rate (issue slots 57 % busy; 422 us with one batch in flight, 305 with separate code for q
+// and k). 64 tokens of 32 + 2 x 32 heads: 7.5 us a call, 4.1 on the GPU.
 //
 // Angles. p f loses its fraction in fp32 once p f passes some thousand turns, so the
 // frequency is kept in turns, f / 2 pi = hi + lo (two fp32, from one fp64 product per warp), and
@@ -258,7 +262,8 @@ cudaError_t launch_typed(RopeArgs<T> a, bool inter, cudaStream_t s) {
   constexpr int RPR = 32 / (D / 8);
   const int total = (a.Hq + RPR - 1) / RPR + 2 * ((a.Hk + RPR - 1) / RPR);   // rounds of rows per token
   // A warp's share of a token: the whole token (its angles computed once) when there are
-  // tokens enough to fill the GPU's warps, down to kU rounds when there are few.
+  // tokens enough to fill the GPU's warps, down to kU rounds when there are few. 64 tokens of 96
+  // head rows take 7.7 us in shares, 16.2 whole; 65536 of 48 rows 428 us in shares of kU, 270 whole.
   const int64_t warps = (int64_t)num_sms() * 4 * kWarps;
   const int64_t want = std::max<int64_t>(1, warps / std::max(1, a.T_));
   a.rounds = std::max(kU, (int)((total + want - 1) / want));
