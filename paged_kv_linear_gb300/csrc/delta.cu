@@ -36,7 +36,8 @@ __device__ __forceinline__ float inv_len(float ss, float eps) {
 // depend on one another, so no CTA waits for another. k and q go through shared memory, and so
 // do the sums over the 128 rows after a shuffle over the 4 rows of a warp: registers stay few (48), and
 // five CTAs per SM keep the loads of some while others store (three, at 69 registers: 55.8 us where
-// it takes 46.4; the exact form of slow decays brought it to 47.5).
+// it takes 46.4; the exact form of slow decays brought it to 47.5; of that form, six CTAs take 48.1
+// and four 52.0). States pass the caches as streams: plain stores 54.7, plain loads 48.2.
 // bf16, D = 128: 64 requests x 32 heads 47.5 us, 5.7 TB/s, 0.84 of the copy rate; 256 x 32 heads 193 us,
 // 0.82; one request 6.7 us a call, 2.7 on the GPU.
 template <int D>
