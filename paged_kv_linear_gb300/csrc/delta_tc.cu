@@ -49,12 +49,12 @@
 //
 // What bounds it: a chunk's way round its three loops (chain, preparation, outputs), each about 10K
 // cycles of waits for one another; leaving any one piece of work out changes the time by 0-3 %.
-// 8 requests of 8192 rows, 32 heads: 1.19 ms (tensor pipe 38 % busy, issue slots 51 %, 1.9 TB/s;
-// 0.27 of what its bytes take at the copy rate); one request of 4096 rows: 321 us, 5.0 us a
-// chunk; one of 77: 20 us. On the way, 8 x 8192: 13.5 ms token by token -> 2.54 (this design) -> 1.94
-// (elected MMA issue, integer gate sums, chunk descriptors instead of local arrays) -> 1.56 (two
-// preparing groups) -> 1.42 (warp MMAs in W) -> 1.19 (rolled loops: the code no longer fell out of the
-// instruction cache) -> 1.12 (one site for a run's setup) -> 1.19 (the state rounded to nearest).
+// 8 requests of 8192 rows, 32 heads: 1.17 ms (tensor pipe 38 % busy, issue slots 49 %, 1.9 TB/s;
+// 0.28 of the copy rate); one request of 4096 rows: 311 us, 4.9 us a chunk; one of 77: 20 us. On the way,
+// 8 x 8192: 13.5 ms token by token -> 2.54 (this design) -> 1.94 (elected MMA issue, integer gate
+// sums, chunk descriptors instead of local arrays) -> 1.56 (two preparing groups) -> 1.42 (warp MMAs
+// in W) -> 1.19 (rolled loops: less of the code falls out of the instruction cache) -> 1.12 (one site
+// for a run's setup) -> 1.19 (the state rounded to nearest) -> 1.17 (fewer instructions for W).
 #include <cuda_bf16.h>
 
 #include "chain_split.cuh"
@@ -112,7 +112,7 @@ static_assert(sizeof(Bars) <= 512 && kOffG % 16 == 0 && kOffBar % 8 == 0 && kSme
 constexpr int kWarpMain = 8, kWarpOut = 16, kWarpFeed = 20, kWarpMma = 21;
 constexpr int kThreads = 22 * 32;
 // Chunks that a chain's state (a read and a write of 64 KB, nothing under way meanwhile) counts as in
-// the work split: 24 ragged requests of up to 5000 rows take 632 us with 0, 480 with 1, 477 with 2;
+// the work split: 24 ragged requests of up to 5000 rows take 632 us with 0, 480 with 1, 477 with 2,
 // 8 x 8192 1.21, 1.19 and 1.19 ms.
 constexpr int kChainCost = 1;
 constexpr uint32_t kTmemCols = 512;
