@@ -345,8 +345,9 @@ hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const
  * every request's rows. A request whose rows are not within [0, T), or more than max_len, sets
  * HYB_DEVERR_BAD_LENGTH, one with a bad slot HYB_DEVERR_BAD_STATE; it is skipped. Rows that
  * belong to no request are left as they were. With T = 0 the rows' pointers may be NULL.
- * bf16 with D = 128 runs the tensor-core kernel (chunks of 64 rows) when max_len > 8, other shapes
- * and calls of a few rows the token recurrence on the CUDA cores. `workspace`: device memory, 8-byte aligned, of
+ * bf16 with D = 128 runs the tensor-core kernel (chunks of 64 rows), other shapes and calls of
+ * a few rows (max_len <= 8, or 40 when the requests are few) the token recurrence on the CUDA
+ * cores. `workspace`: device memory, 8-byte aligned, of
  * hyb_gated_delta_chunked_prefill_workspace_size() bytes (a short, misaligned or missing one is
  * HYB_ERR_INVALID_ARG when B > 0); no initialisation, left alone between calls. Calls that may
  * run at the same time need workspaces of their own: see hyb_linear_attn_chunked_prefill, whose

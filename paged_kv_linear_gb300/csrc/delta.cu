@@ -186,7 +186,16 @@ struct DeltaScan {
   static_assert(R % 4 == 0 && NT % 32 == 0 && LQ * 4 * NT == TB * D, "shape");
 };
 
-constexpr int kShortRows = 8;              // rows of a request that the recurrence always takes
+// Whether the recurrence takes a call that the tensor-core kernel could take. That one needs a chunk's
+// time (13 us, and the same again for every SM's next chains) for a few rows too; the recurrence 4 us
+// and some 0.25 us a row, as long as its CTAs, four a chain, find SMs of their own, and in
+// proportion to the chains beyond that. Recurrence / tensor cores in us, heads of 128:
+//     chains     32: 32 rows 11.2 / 14.1, 40 rows 14.3 / 14.2     192: 8 rows 14.4 / 22.2
+//                64: 24 rows 12.7 / 14.0, 32 rows 14.8 / 14.2     512: 8 rows 32 / 36, 12 rows 38 / 36
+//               128: 12 rows 13.3 / 13.9, 16 rows 15.2 / 14.0    2048: 8 rows 122 / 128, 12 rows 144 / 128
+inline bool short_call(int max_len, int64_t chains) {
+  return max_len <= 8 || (max_len <= 40 && max_len * chains <= 1536);
+}
 
 struct Quad {
   float x[4];
@@ -517,10 +526,7 @@ hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const voi
   if (!workspace || !al(workspace, 8) || ws_bytes < kLinPrefillWsBytes) return HYB_ERR_INVALID_ARG;
   unsigned* sw = status_word();
   if (!sw) return HYB_ERR_CUDA;
-  // The tensor-core kernel takes a chunk's time (13 us) for a few rows too; up to 8 rows a request the
-  // recurrence is quicker: at 32 heads, 4.2 us against 13.3 for one request of one row, 120 against 126
-  // for 64 requests of 8 rows; of 16 rows 165 against 127. (Without rows only resets are left.)
-  if (delta_prefill_tc_supported(d) && max_len > kShortRows) {
+  if (delta_prefill_tc_supported(d) && !short_call(max_len, (int64_t)B * d->num_v_heads)) {
     const Strides x = strides_of(d);
     return cuda_status(launch_delta_prefill_tc(out, q, k, v, g, beta, cu_seqlens, state_pool,
                                                num_state_slots, state_slots, reset, B, T, max_len,

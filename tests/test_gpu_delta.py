@@ -184,7 +184,8 @@ def test_prefill_shapes(hyb, D, dt, lens, reset):
     check_prefill(hyb, c, lens, reset, f"D {D} {dt}", gap=3)
 
 
-@pytest.mark.parametrize("lens,reset", [([8, 3, 0, 1], [0, 1, 1, 0]), ([9, 8, 0, 1], [0, 1, 1, 0]), ([8] * 60, None)])
+@pytest.mark.parametrize("lens,reset", [([8, 3, 0, 1], [0, 1, 1, 0]), ([9, 8, 0, 1], [0, 1, 1, 0]), ([8] * 60, None),
+                                        ([40], None), ([41, 2], None), ([12] * 32, None), ([12] * 33, None)])
 def test_prefill_calls_of_a_few_rows(hyb, lens, reset):
     """At both sides of the bound between the recurrence and the tensor-core kernel."""
     c = Case(23, sum(lens) + 2, 2, 4, 128, torch.bfloat16, len(lens) + 1, fused=True)
