@@ -166,16 +166,17 @@ delta_step_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restr
 // The recurrence itself, for the shapes without a tensor-core kernel (fp32 rows, other head
 // sizes): fp32 throughout. Columns of a state do not depend on one another, so a CTA carries 32
 // columns of one (request, head) in registers for the whole prompt, and D / 32 CTAs share a
-// state. A column's D rows lie with RG lanes of one warp, so a token takes two sums over registers
-// and one round of shuffles, and no barrier. Tokens come in batches of kTB, whose rows and scalars
+// state. A column's D rows lie with RG lanes of one warp (see scan_pick), so a token takes two sums over
+// registers and a few shuffles, and no barrier. Tokens come in batches of kTB, whose rows and scalars
 // are staged in shared memory; the next batch's rows are on their way to registers meanwhile. Bound
-// by the latency of that chain when there are few chains (0.25 us a token at D = 64; 24 chains of up to
-// 700 rows: 176 us, 461 without the next batch's rows on their way), by fp32 arithmetic (4 D^2 fma
-// per token and head, in packed pairs) when there are many (2048 chains of 512 tokens at D = 64: 0.97 ms).
-template <int D>
+// by the latency of that chain when there are few chains (0.18 us a token at D = 64; 24 chains of up to
+// 700 rows: 127 us, with 32 rows a lane 176, and 461 without the next batch's rows on their way), by
+// fp32 arithmetic (4 D^2 fma per token and head, in packed pairs) when there are many (2048 chains of
+// 512 tokens at D = 64: 0.97 ms).
+template <int D, int RG_>
 struct DeltaScan {
   static constexpr int COLS = D < 32 ? D : 32;              // columns per CTA
-  static constexpr int RG = D < 32 ? 2 : D / 32;            // lanes per column
+  static constexpr int RG = RG_;                            // lanes per column
   static constexpr int R = D / RG;                          // rows per lane
   static constexpr int NT = COLS * RG;                      // threads
   static constexpr int CW = 32 / RG;                        // columns per warp
@@ -209,15 +210,15 @@ __device__ __forceinline__ Quad load4(const __nv_bfloat16* p) {
   return {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(DeltaScan<D>::NT)
+template <typename T, int D, int RG_>
+__global__ void __launch_bounds__(DeltaScan<D, RG_>::NT)
 delta_scan_kernel(T* __restrict__ out, const T* __restrict__ q, const T* __restrict__ k,
                   const T* __restrict__ v, const float* __restrict__ g,
                   const float* __restrict__ beta, const int32_t* __restrict__ cu,
                   float* __restrict__ pool, int NS, const int32_t* __restrict__ slots,
                   const uint8_t* __restrict__ reset, int rows_total, int max_len, int Hv, int rep,
                   int64_t qs, int64_t ks, int64_t vs, float scale, float eps, unsigned* status) {
-  using Sh = DeltaScan<D>;
+  using Sh = DeltaScan<D, RG_>;
   constexpr int COLS = Sh::COLS, RG = Sh::RG, R = Sh::R, CW = Sh::CW, NT = Sh::NT, TB = Sh::TB;
   constexpr int LQ = Sh::LQ, LV = Sh::LV, LT = Sh::LT;
   constexpr int LD = D + 4;                // rows of different tokens start at different banks
@@ -400,20 +401,34 @@ cudaError_t step_typed(void* out, const void* q, const void* k, const void* v, c
   return e;
 }
 
-template <typename T, int D>
+template <typename T, int D, int RG>
 cudaError_t scan_typed(void* out, const void* q, const void* k, const void* v, const float* g,
                        const float* beta, const int32_t* cu, float* pool, int NS,
                        const int32_t* slots, const uint8_t* reset, int B, int rows, int max_len,
                        const hyb_delta_dims_t* d, unsigned* status, cudaStream_t s) {
-  using Sh = DeltaScan<D>;
+  using Sh = DeltaScan<D, RG>;
   const Strides st = strides_of(d);
   const dim3 grid(D / Sh::COLS, d->num_v_heads, B);
-  delta_scan_kernel<T, D><<<grid, Sh::NT, 0, s>>>(
+  delta_scan_kernel<T, D, RG><<<grid, Sh::NT, 0, s>>>(
       (T*)out, (const T*)q, (const T*)k, (const T*)v, g, beta, cu, pool, NS, slots, reset, rows,
       max_len, d->num_v_heads, d->num_v_heads / d->num_qk_heads, st.q, st.k, st.v, d->scale,
       d->qk_norm_eps, status);
   count_launch();
   return cudaGetLastError();
+}
+
+// Lanes to a column: 32 of its rows each, or 16 for small heads while a token's latency counts, not the
+// arithmetic: as long as two CTAs per SM hold all chains. 16 rows / 32 rows, 256 tokens, us: D = 64, fp32:
+// 72 chains 49 / 66, 152 chains 62 / 68, 304 chains 94 / 93, 1024 chains 310 / 275; D = 32: 72 chains
+// 49 / 60, 304 chains 49 / 62, 1024 chains 88 / 81. At D = 128 the third round of shuffles takes what the
+// shorter sums give (24 chains 72 / 70); 8 rows at D = 64: 62.
+template <typename T, int D, typename... Args>
+cudaError_t scan_pick(int64_t chains, Args... args) {
+  constexpr int RG = D < 32 ? 2 : D / 32;
+  if constexpr (D == 32 || D == 64) {
+    if (chains * (D / 32) <= 2 * num_sms()) return scan_typed<T, D, 2 * RG>(args...);
+  }
+  return scan_typed<T, D, RG>(args...);
 }
 
 #define HYB_DELTA_EACH(CALL)                                                            \
@@ -438,8 +453,8 @@ cudaError_t launch_scan(void* out, const void* q, const void* k, const void* v, 
                         const float* beta, const int32_t* cu, float* pool, int NS,
                         const int32_t* slots, const uint8_t* reset, int B, int rows, int max_len,
                         const hyb_delta_dims_t* d, unsigned* status, cudaStream_t s) {
-#define HYB_CALL(T, DD) \
-  scan_typed<T, DD>(out, q, k, v, g, beta, cu, pool, NS, slots, reset, B, rows, max_len, d, status, s)
+#define HYB_CALL(T, DD)                                                                             \
+  scan_pick<T, DD>((int64_t)B * d->num_v_heads, out, q, k, v, g, beta, cu, pool, NS, slots, reset, B, rows, max_len, d, status, s)
   HYB_DELTA_EACH(HYB_CALL)
 #undef HYB_CALL
 }

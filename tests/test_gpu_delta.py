@@ -239,6 +239,14 @@ def test_prefill_long_prompt_of_small_changes_does_not_drift(hyb):
     assert (lim < 5e-6 * most).all() and (err <= lim).all(), (err / most, lim / most)
 
 
+@pytest.mark.parametrize("D,dt", [(16, torch.bfloat16), (32, torch.bfloat16), (64, torch.float32), (64, torch.bfloat16)])
+def test_prefill_many_chains_of_small_heads(hyb, D, dt):
+    """More chains than the GPU holds at once: the recurrence then keeps 32 rows of a column a lane."""
+    lens = [20, 3, 0, 17, 1] * 20
+    c = Case(24, sum(lens), 4, 4, D, dt, 100, fused=True)
+    check_prefill(hyb, c, lens, None, f"400 chains of {D}")
+
+
 def test_prefill_many_ragged_chains(hyb):
     """More chains than the GPU has SMs, with empty and short ones: chains are shared out."""
     rs = np.random.RandomState(5)
