@@ -368,7 +368,7 @@ def hyb_trace_layer_ms(L: int):
 
 
 def hyb_selftest_bounded_waits(limit_us: int, stream=None):
-    """Runs the bounded-wait self-test kernel: two waits nothing satisfies, each giving up
+    """Runs the bounded-wait self-test kernel: three waits nothing satisfies, each giving up
     after limit_us and setting HYB_DEVERR_TIMEOUT in the device status word."""
     return _lib.hyb_selftest_bounded_waits(limit_us, _s(stream))
 

@@ -11,6 +11,7 @@
 #include <utility>
 #include <vector>
 
+#include "chain_split.cuh"
 #include "hyb_internal.cuh"
 
 // Device-side check word (one per device that loads the library); kernels OR bits in.
@@ -20,33 +21,23 @@ static __device__ unsigned long long g_hyb_never_set;
 
 namespace hyb {
 namespace {
-// Two device-side waits that nothing satisfies, each with the library's bounded-wait
-// mechanism: warp 0 on an mbarrier phase that no thread or copy completes (the helper every
-// TMA and tensor-core wait uses), warp 1 on a global flag that no thread sets (an acquire
-// load, %globaltimer and a back-off, as in the chunked linear prefill's state handoff). Each
-// gives up after limit_ns, reports HYB_DEVERR_TIMEOUT and returns.
+// The library's device-side waits, each by its own helper and on something that never comes: warp 0
+// and 1 on an mbarrier phase that no thread or copy completes (timed by %globaltimer, and by the SM's
+// clock), warp 2 on a handoff flag that no CTA sets. Each gives up after limit_ns (or as many cycles
+// at 2.07 GHz) and reports HYB_DEVERR_TIMEOUT; one that does not report HYB_DEVERR_BAD_STATE.
 __global__ void selftest_bounded_waits_kernel(uint64_t limit_ns, unsigned* status) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar[2];
   if (threadIdx.x == 0) {
-    mbar_init(&bar, 1);
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
     fence_mbar_init();
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    if (!mbar_wait(&bar, 0, limit_ns)) flag(status, HYB_DEVERR_TIMEOUT);
-  } else if (threadIdx.x == 32) {
-    const uint64_t t0 = global_ns();
-    while (true) {
-      unsigned long long v;
-      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(&g_hyb_never_set) : "memory");
-      if (v == ~0ull) break;                   // never true: nothing writes the flag
-      if (global_ns() - t0 > limit_ns) {
-        flag(status, HYB_DEVERR_TIMEOUT);
-        break;
-      }
-      __nanosleep(1000);
-    }
-  }
+  const int warp = threadIdx.x >> 5;
+  const bool met = warp == 0   ? mbar_wait(&bar[0], 0, limit_ns)
+                   : warp == 1 ? mbar_wait_cycles(&bar[1], 0, (unsigned)(limit_ns * 207 / 100))
+                               : take_handoff(&g_hyb_never_set, ~0ull, limit_ns);
+  if (threadIdx.x % 32 == 0) flag(status, met ? HYB_DEVERR_BAD_STATE : HYB_DEVERR_TIMEOUT);
 }
 }  // namespace
 }  // namespace hyb
@@ -622,7 +613,7 @@ hyb_status_t hyb_selftest_bounded_waits(uint32_t limit_us, void* stream) {
   if (limit_us < 1 || limit_us > 1000000) return HYB_ERR_INVALID_ARG;
   unsigned* sw = hyb::status_word();
   if (!sw) return HYB_ERR_CUDA;
-  hyb::selftest_bounded_waits_kernel<<<1, 64, 0, (cudaStream_t)stream>>>(
+  hyb::selftest_bounded_waits_kernel<<<1, 96, 0, (cudaStream_t)stream>>>(
       (uint64_t)limit_us * 1000ull, sw);
   hyb::count_launch();
   return cuda_status(cudaGetLastError());

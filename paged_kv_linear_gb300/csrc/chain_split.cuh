@@ -118,6 +118,22 @@ __device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
+// Waits, as a whole warp, until the CTA that ran a chain's start has handed its state over in this
+// call, and brings the warp together again. False when limit_ns is up: the state may then still be
+// written there, so the caller reads and writes none of it and ends its part of the kernel.
+__device__ __forceinline__ bool take_handoff(const unsigned long long* fl, unsigned long long tag,
+                                             uint64_t limit_ns = 2000000000ull) {
+  const uint64_t t0 = global_ns();
+  bool ok = ld_acquire_u64(fl) == tag;
+#pragma unroll 1
+  while (!ok && global_ns() - t0 <= limit_ns) {
+    __nanosleep(100);
+    ok = ld_acquire_u64(fl) == tag;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  __syncwarp();
+  return ok;
+}
 
 }  // namespace hyb
 #endif

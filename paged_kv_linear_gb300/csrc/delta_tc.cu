@@ -239,15 +239,6 @@ __device__ __forceinline__ void from_fixed(long long x, bool nan, float& hi, flo
   hi = nan ? __int_as_float(0x7fffffff) : h * 0x1p-36f;
   lo = __ll2float_rn(x - __float2ll_rn(h)) * 0x1p-36f;
 }
-// As mbar_wait, timed by the SM's own 32-bit clock (some 2 s of its 2.07), which is cheaper to read.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned t0 = (unsigned)clock();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity))
-    if ((unsigned)clock() - t0 > 4000000000u) return false;
-  return true;
-}
 
 // Operands of a warp's 16 x 8 x 8 product in two tf32 terms, cut: h + l holds 22 bits of x's 24
 // (rounding them instead takes two more instructions an element, one prompt 321 us for 311). The
@@ -425,7 +416,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
   const uint32_t tmem = tmem_base;
   const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);   // this warp's TMEM lanes
 
-#define HYB_WAIT(bar, parity) __all_sync(0xffffffffu, wait(&(bar), (parity)))
+#define HYB_WAIT(bar, parity) __all_sync(0xffffffffu, mbar_wait_cycles(&(bar), (parity)))
   bool ok = true;
   if (warp < kWarpMain) {
     // ------------------------------------------------------------ preparation
@@ -717,18 +708,9 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       float* const S = chunks[c & 3].S;
       const bool last = flags & kLast, hand = flags & kHand;
       // this chunk's first state: the run's from the pool, or what the last chunk left in TMEM
-      if (flags & kFirst) {
-        if (flags & kTake) {
-          const unsigned long long* fl = hs + 1 + (p + 1);
-          const uint64_t t0 = global_ns();
-          while (ld_acquire_u64(fl) != tag) {
-            if (global_ns() - t0 > 2000000000ull) {
-              flag(status, HYB_DEVERR_TIMEOUT);
-              break;
-            }
-            __nanosleep(100);
-          }
-        }
+      if ((flags & (kFirst | kTake)) == (kFirst | kTake)) {
+        ok = take_handoff(hs + 1 + (p + 1), tag);
+        if (!ok) break;
       }
       {
         const bool from_tmem = !(flags & kFirst), from_pool = !(flags & kZero);
@@ -835,6 +817,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
             if (mbar_wait(&bars->published, 0)) st_release_u64(hs + 1 + p, tag);
             else flag(status, HYB_DEVERR_TIMEOUT);
           }
+          __syncwarp();
         }
       }
     }

@@ -209,6 +209,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     if (global_ns() - t0 > limit_ns) return false;
   }
 }
+// The same, timed by the SM's own 32-bit clock, which is cheaper to read; limit in its cycles (some
+// 2 s of its 2.07 as given), at most 4e9.
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* bar, uint32_t parity,
+                                                 unsigned limit = 4000000000u) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned t0 = (unsigned)clock();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if ((unsigned)clock() - t0 > limit) return false;
+  return true;
+}
 
 // ---- bulk copies (TMA engine, non-tensor form): global -> shared, completes on `bar`
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes,

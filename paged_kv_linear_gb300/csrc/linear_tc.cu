@@ -167,20 +167,11 @@ __device__ __forceinline__ void put8(uint8_t* s_t, int row, int ch, const uint4&
 // Starting state of run `sg`, row `row` (one state warp thread) -> TMEM lane `tl`, and its
 // bf16 copy -> the operand s_t (which (b) must no longer be reading). A run that continues
 // a chain first waits until the CTA that ran the chain's start has published it with this
-// call's tag `want` (on expiry: reported, and the pool's contents are used as they are).
-__device__ __forceinline__ void load_start(const Seg& sg, uint8_t* s_t, uint32_t tl, int row,
+// call's tag `want`; false when that wait expires, with nothing read.
+__device__ __forceinline__ bool load_start(const Seg& sg, uint8_t* s_t, uint32_t tl, int row,
                                            const unsigned long long* handoff_flag,
-                                           unsigned long long want, unsigned* status) {
-  if (sg.wait_handoff) {
-    const uint64_t t0 = global_ns();
-    while (ld_acquire_u64(handoff_flag) != want) {
-      if (global_ns() - t0 > 2000000000ull) {
-        flag(status, HYB_DEVERR_TIMEOUT);
-        break;
-      }
-      __nanosleep(100);
-    }
-  }
+                                           unsigned long long want) {
+  if (sg.wait_handoff && !take_handoff(handoff_flag, want)) return false;
 #pragma unroll
   for (int part = 0; part < 4; ++part) {
     const int j0 = part * 32;
@@ -197,6 +188,7 @@ __device__ __forceinline__ void load_start(const Seg& sg, uint8_t* s_t, uint32_t
   }
   tmem_st_wait();
   fence_async_smem();
+  return true;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -419,14 +411,14 @@ linear_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     if (warp < 4) {
       Seg sg;
       bool have = NEXT_RUN(sg);
-      if (have) {
-        load_start(sg, s_hi, tl, row, &handoff[p + 1], tag, status);
+      if (have) ok = load_start(sg, s_hi, tl, row, &handoff[p + 1], tag);
+      if (have && ok) {
         tc_fence_before();
         mbar_arrive(&bars->s_read);
         mbar_arrive(&bars->s_written);
       }
       int ci = sg.c0;
-      for (int c = 0; have; ++c) {
+      for (int c = 0; have && ok; ++c) {
         // ---- tril(P) as bf16 pairs over the first 64 columns of P (row t = this lane); (c)
         // waits for it right after (b), so P goes first
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_ready, c & 1));
@@ -476,13 +468,15 @@ linear_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
               if (mbar_wait(&bars->published, 0)) st_release_u64(&handoff[p], tag);
               else flag(status, HYB_DEVERR_TIMEOUT);
             }
+            __syncwarp();
           }
           have = NEXT_RUN(sg);
           ci = sg.c0;
           if (have) {
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->b_done, c & 1));
             if (!ok) break;
-            load_start(sg, s_hi, tl, row, &handoff[p + 1], tag, status);
+            ok = load_start(sg, s_hi, tl, row, &handoff[p + 1], tag);
+            if (!ok) break;
           }
           tc_fence_before();
           mbar_arrive(&bars->s_read);

@@ -41,3 +41,34 @@ def test_bounded_waits_expire_report_and_return(hyb, devstatus, limit_us):
     assert_out_close(out, o_ref, "linear step after the self-test")
     assert_states_close(to_host(pool_d)[slots], s_ref, "states after the self-test")
     assert devstatus() == (0, 0)
+
+
+def test_gated_delta_prefill_after_expired_waits(hyb, devstatus):
+    """The waits of the gated delta prefill (barriers by the SM's clock, the handoff of a cut chain)
+    are among the self-test's: after they ran out, a call that cuts chains gives the same bits as
+    before."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B, H, D, n = sms // 2 + 1, 2, 128, 130
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (torch.randn(B * n, H, D, generator=gen, device="cuda").bfloat16() for _ in range(3))
+    g = -torch.rand(B * n, H, generator=gen, device="cuda")
+    beta = torch.rand(B * n, H, generator=gen, device="cuda")
+    start = torch.randn(B, H, D, D, generator=gen, device="cuda")
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    slots = torch.arange(B, dtype=torch.int32, device="cuda")
+    d = hyb.delta_dims(H, H, D, qk_norm_eps=1e-6)
+    ws = torch.empty(hyb.hyb_gated_delta_chunked_prefill_workspace_size(B, B * n, d), dtype=torch.uint8, device="cuda")
+
+    def call():
+        out, pool = torch.empty_like(v), start.clone()
+        hyb.check(hyb.hyb_gated_delta_chunked_prefill(out, q, k, v, g, beta, cu, pool, B, slots, None, B, B * n, n, d, ws, ws.numel()))
+        torch.cuda.synchronize()
+        return out, pool
+
+    before = call()
+    assert devstatus() == (0, 0)
+    hyb.check(hyb.hyb_selftest_bounded_waits(1000))
+    assert devstatus() == (hyb.HYB_ERR_DEVICE_CHECK, hyb.HYB_DEVERR_TIMEOUT)
+    after = call()
+    assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
+    assert devstatus() == (0, 0)
