@@ -38,7 +38,9 @@
 //   (o) D1Q       = X^T P^T     A = X (2 terms), B = P (3 pairs)       12
 // MMAs of N = 64 take 34 cycles of the tensor core, N = 128 67: 3.9K cycles a chunk.
 //
-// W = (1 + A)^-1 in fp32 on the warps' own MMAs (tf32, two terms each) by blocks of 8, 16, 32 and 64.
+// W = (1 + A)^-1 in fp32 on the warps' own MMAs (tf32, two terms each) by blocks of 8, 16, 32 and 64. What
+// it is off by adds up over a chunk's rows where keys repeat: see tf32_terms. States against fp64 after
+// 1024 rows, no decay, beta 1: one key 4.6e-7 (fp32 recurrence 8.1e-7), keys of 2 dimensions 4.5e-7.
 //
 // Warps: 0-7 prepare chunks (lengths, factors, W, P), two groups of four with a chunk each, so a
 // chunk's preparation may take two chunks' time; 8-15 carry the chain (two warps to 32 lanes, each
@@ -240,13 +242,14 @@ __device__ __forceinline__ void from_fixed(long long x, bool nan, float& hi, flo
   lo = __ll2float_rn(x - __float2ll_rn(h)) * 0x1p-36f;
 }
 
-// Operands of a warp's 16 x 8 x 8 product in two tf32 terms, cut: h + l holds 22 bits of x's 24
-// (rounding them instead takes two more instructions an element, one prompt 321 us for 311). The
-// low 13 bits of each word are zero.
-__device__ __forceinline__ uint32_t cut_tf32(float x) { return __float_as_uint(x) & 0xffffe000u; }
+// Operands of a warp's 16 x 8 x 8 product in two tf32 terms, the first rounded to nearest, the second
+// cut: h + l is off by at most one ulp of x, and what the products leave out (l l) has either sign.
+// (The first term cut as well loses two bits and all of it towards zero, which adds up over a chunk
+// where keys repeat.) The low 13 bits of each word are zero. A NaN stays one in l.
+__device__ __forceinline__ uint32_t cut_tf32(uint32_t x) { return x & 0xffffe000u; }
 __device__ __forceinline__ void tf32_terms(float x, uint32_t& h, uint32_t& l) {
-  h = cut_tf32(x);
-  l = cut_tf32(x - __uint_as_float(h));
+  h = cut_tf32(__float_as_uint(x) + 0x1000u);
+  l = cut_tf32(__float_as_uint(x - __uint_as_float(h)));
 }
 struct FragA {                                 // 16 x 8, element (r, k) at p[r * RS + k * KS]
   uint32_t h[4], l[4];
@@ -528,7 +531,8 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       // row-major in its place. Two blocks W00, W11 on the diagonal and A10 below give
       // W10 = -W11 (A10 W00); the first product goes where W10 will be. What is left of A^T above the
       // diagonal blocks is never read as W: those products are skipped. The products are warp
-      // MMAs of 16 x 8 x 8 on two tf32 terms (three products, 2^-22): on the CUDA cores their
+      // MMAs of 16 x 8 x 8 on two tf32 terms (three products; the fourth, up to 2^-22, has either
+      // sign): on the CUDA cores their
       // operands, broadcast from shared memory, took two thirds of its bandwidth.
       {
         // 8 x 8: a warp two blocks, a lane a column (lanes 16-31 do the same). Once w_m is final it is

@@ -1,0 +1,66 @@
+"""How near the gated delta rule's tensor-core prefill (bf16, D = 128) comes to the 64-bit recurrence where
+an error of its operands would add up: keys that repeat."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_delta import EPS, Case, host, prefill
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+C = 64          # rows of a chunk
+
+
+def one_request(hyb, c):
+    out = torch.empty(c.T, c.Hv, c.D, device="cuda", dtype=c.dt)
+    prefill(hyb, c, out, torch.tensor([0, c.T], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), None)
+    return out
+
+
+@pytest.mark.parametrize("dims", [1, 2])
+@pytest.mark.parametrize("T", [64, 1024])
+def test_keys_of_few_dimensions(hyb, dims, T):
+    """Keys of one or two dimensions, beta 1, no decay: the corrections' system is as far from the
+    identity as it gets, and what its inverse W is off by adds up over the rows of a chunk. (One key:
+    every entry of A is the same number near 1, and what cutting its tf32 terms loses has one sign in
+    all 2016 entries below the diagonal.) Each chunk replaces the keys' dimensions of the state and
+    changes no others, so the error is the last chunk's. Allowed, as norms over all heads:
+      * 1.5 times what the recurrence is off by in fp32 on the same numbers (fp32 rows take it). The 1.5
+        is for chance: 16 heads x 128 columns carry the error, a spread of 2 %.
+      * the tensor core's fp32 sums, which cut to 24 bits instead of rounding: each cut takes half a
+        unit on average, at most u = 2^-24 of the sum. With S the state at the chunk's start, R = V - K S
+        and X = W R, the sums are of full size from the first half's largest terms on: 16 cuts of K S
+        (4 products, then 12), 14 of X (2 and 12), 8 of the change K^T X (2 and 6). In the state that is
+        u (16 |K^T W K S| + 22 |K^T X|).
+    So nothing is left for W."""
+    H = 16
+    c = Case(30 + dims, T, H, H, 128, torch.bfloat16, 1, gate="none")
+    if dims == 1:                          # a dense key for each head, the same at every row
+        c.k = c.k[:1].expand(T, -1, -1).contiguous()
+    else:
+        c.k[..., 2:] = 0
+    c.beta.fill_(1.0)
+    start = c.pool.clone()
+    last = T - C
+    S = c.ref(slice(0, last), host(start)[0])[1] if last else host(start)[0]
+    want = c.ref(slice(last, T), S)[1]
+    k, v = host(c.k)[last:], host(c.v)[last:]
+    k = k / np.sqrt((k * k).sum(-1, keepdims=True) + EPS)
+    cuts = 0.0
+    for h in range(H):
+        K = k[:, h]
+        W = np.linalg.inv(np.eye(C) + np.tril(K @ K.T, -1))
+        removed, change = K.T @ W @ K @ S[h], K.T @ W @ (v[:, h] - K @ S[h])
+        cuts += (U * (16 * np.linalg.norm(removed) + 22 * np.linalg.norm(change))) ** 2
+    one_request(hyb, c)
+    got = host(c.pool)[0]
+    c.pool.copy_(start)
+    c.q, c.k, c.v, c.dt = c.q.float(), c.k.float(), c.v.float(), torch.float32
+    one_request(hyb, c)
+    here, fp32 = (np.linalg.norm(x - want) / np.linalg.norm(want) for x in (got, host(c.pool)[0]))
+    cuts = math.sqrt(cuts) / np.linalg.norm(want)
+    print(f"dims {dims} T {T}: {here:.2e}, fp32 recurrence {fp32:.2e}, cuts {cuts:.2e}")
+    assert here <= 1.5 * fp32 + cuts
