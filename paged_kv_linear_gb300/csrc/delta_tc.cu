@@ -19,9 +19,9 @@
 // without loss. K S and the state's change then are exact products; of W R the terms beyond 2^-24
 // are left out (six of nine products). The tensor core's fp32 sums are cut, not rounded, at 24
 // bits: products go in with the smallest terms first, and the state's change is summed by itself
-// and then added to the state times its decay in one fp32 fma. (Summed up in the state's own
+// and then added to the decayed state, rounded to nearest. (Summed up in the state's own
 // accumulator, 12 cuts towards zero in 64 rows, 8192 rows of small changes put it off by 3.0e-5;
-// now 3.3e-7, the fp32 recurrence 2.3e-6.) The outputs, rounded to bf16 in the end, take two terms
+// now 3.3e-7, the fp32 recurrence 2.3e-6.) Slow decays are applied as S + (e^G - 1) S: see get_state. The outputs, rounded to bf16 in the end, take two terms
 // of S, X and P (about 2^-16). With two terms throughout, states were off by some 3e-6; now by
 // 1.5e-7 after 77 rows, 2e-7 after 4096.
 //
@@ -85,7 +85,8 @@ struct Gates {                                 // factors of a chunk's rows
   float bt[kC];                                // beta
   float eR[kC], cA[kC], wB[kC];                // e^G / |k|, beta / |k|^2, beta / |k|
   float wX[kC], pq[kC], oq[kC];                // e^(G_C - G), scale / |q|, scale e^G / |q|
-  float dec, pad[3];                           // e^(G_C)
+  float dec, keep, pad[2];                     // of the state, S <- dec S + keep S: e^(G_C) and 0, or,
+                                               // where the decay is slow, e^(G_C) - 1 and 1
 };
 // What the warps need to know of a chunk. The feeding warp walks the CTA's runs and writes these,
 // four chunks deep as the gates: chunk c's place is free once (s) of chunk c - 3 is done, which
@@ -319,15 +320,21 @@ __device__ __forceinline__ void put_terms(uint32_t h_at, uint32_t m_at, uint32_t
   tmem_st8u(l_at, l);
 }
 // 16 values of this lane's state (key dims i0 ..) as (s) left them: the old ones times the chunk's
-// decay plus their change, rounded to nearest
-__device__ __forceinline__ void get_state(uint32_t tl, int i0, float dec, float* v) {
+// decay plus their change, rounded to nearest. Where the decay is slow it is applied as S + (e^G - 1) S:
+// e^G rounded to fp32 would be off alike in every chunk of a constant gate (8192 rows of gate -3e-4
+// put a state off by 8.7e-6).
+__device__ __forceinline__ void get_state(uint32_t tl, int i0, const Gates& G, float* v) {
   float x[16];
   tmem_ld16(tl + kColS + i0, v);
   tmem_ld16(tl + kColDS + i0, x);
   tmem_ld_wait();
-  const f32x2 d2 = pair(dec, dec);
+  const float2 f = *reinterpret_cast<const float2*>(&G.dec);
+  const f32x2 d2 = pair(f.x, f.x), k2 = pair(f.y, f.y);
 #pragma unroll
-  for (int e = 0; e < 16; e += 2) unpair(fma2(pair(v[e], v[e + 1]), d2, pair(x[e], x[e + 1])), v[e], v[e + 1]);
+  for (int e = 0; e < 16; e += 2) {
+    const f32x2 s = pair(v[e], v[e + 1]);
+    unpair(fma2(s, k2, fma2(s, d2, pair(x[e], x[e + 1]))), v[e], v[e + 1]);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -458,7 +465,13 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           G.cA[t] = G.bt[t] * rk * rk;
           G.eR[t] = rk * exp2f(G.hi[t]);     // G.lo is below half an ulp of G.hi
           G.wX[t] = exp2f((G.hi[63] - G.hi[t]) + (G.lo[63] - G.lo[t]));
-          if (t == 63) G.dec = exp2f(G.hi[63]);
+          if (t == 63) {
+            constexpr float kLn2 = 0.693147181f;
+            const float em1 = expm1f(fmaf(G.hi[63], kLn2, G.lo[63] * kLn2));
+            const bool slow = em1 >= -0.5f;
+            G.dec = slow ? em1 : exp2f(G.hi[63]);
+            G.keep = slow ? 1.f : 0.f;
+          }
         } else {
           const float f = t < n ? scale * inv : 0.f;
           G.pq[t] = f;
@@ -677,7 +690,6 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
     // Rows in two pieces of 16 (the lower half of the rows starts with its second, see R below).
     const int xa = x0 + (half ? 0 : 16), xb = x0 + (half ? 16 : 0);
     int n = 0, flags = 0;
-    float dec = 0.f;                         // of the chunk before
     uint32_t v[16];                          // pairs of rows of V, this column
     // Chunk c's description and V: fetched while the chunk before is under way.
     auto fetch = [&](int c) -> bool {
@@ -723,7 +735,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
           const int i = i0 + 16 * x;
           float s[16];
           if (from_tmem) {
-            get_state(tl, i, dec, s);
+            get_state(tl, i, gates[(c - 1) & 3], s);
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = from_pool ? __ldcg(S + (i + e) * kD + j) : 0.f;
@@ -801,7 +813,6 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
       }
       fence_async_smem();
       mbar_arrive(&bars->om_ready);
-      dec = G.dec;
       // the chunk's last state
       ok = HYB_WAIT(bars->s_ready, c & 1);
       if (!ok) break;
@@ -810,7 +821,7 @@ delta_prefill_tc_kernel(const __grid_constant__ CUtensorMap tq,
 #pragma unroll 1
         for (int i = i0; i < i0 + 64; i += 16) {
           float s[16];
-          get_state(tl, i, dec, s);
+          get_state(tl, i, G, s);
 #pragma unroll
           for (int e = 0; e < 16; ++e) S[(i + e) * kD + j] = s[e];
         }

@@ -1,5 +1,5 @@
 """How near the gated delta rule's tensor-core prefill (bf16, D = 128) comes to the 64-bit recurrence where
-an error of its operands would add up: keys that repeat."""
+an error of its operands would add up: keys that repeat, and states that are only slowly lost."""
 import math
 
 import numpy as np
@@ -64,3 +64,24 @@ def test_keys_of_few_dimensions(hyb, dims, T):
     cuts = math.sqrt(cuts) / np.linalg.norm(want)
     print(f"dims {dims} T {T}: {here:.2e}, fp32 recurrence {fp32:.2e}, cuts {cuts:.2e}")
     assert here <= 1.5 * fp32 + cuts
+
+
+@pytest.mark.parametrize("gate", [-1e-2, -1e-3, -3e-4, -1e-4, -1e-5])
+def test_slow_decay_does_not_drift(hyb, gate):
+    """With beta 0 a state only fades, by the same e^(64 g) in every chunk. Applied as S + (e^(64 g) -
+    1) S a chunk rounds the state once (at most u of an element, of either sign: in squares over the
+    chunks), and e^(64 g) - 1 is off by 3 u of itself (its argument by u, the function by 2 u), alike
+    in all of them. e^(64 g) rounded would be off by up to u (more with the function's own error),
+    alike in all of them: 128 u here."""
+    T = 8192
+    n = T // C
+    c = Case(32, T, 1, 1, 128, torch.bfloat16, 1, gate="none")
+    c.g.fill_(gate)
+    c.beta.zero_()
+    S0 = host(c.pool)[0, 0]
+    one_request(hyb, c)
+    ref = S0 * math.exp(float(c.g[0, 0]) * T)
+    err = np.linalg.norm(host(c.pool)[0, 0] - ref) / np.linalg.norm(ref)
+    lim = U * (math.sqrt(n) + 3 * n * abs(math.expm1(C * float(c.g[0, 0]))))
+    print(f"gate {gate}: {err:.2e} of {lim:.2e}")
+    assert err <= lim
