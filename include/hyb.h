@@ -347,7 +347,8 @@ hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const
  * belong to no request are left as they were. With T = 0 the rows' pointers may be NULL.
  * bf16 with D = 128 runs the tensor-core kernel (chunks of 64 rows), other shapes and calls of
  * a few rows (max_len <= 8, or 40 when the requests are few) the token recurrence on the CUDA
- * cores. `workspace`: device memory, 8-byte aligned, of
+ * cores. The states have fp32's accuracy in both; the tensor-core kernel's outputs, before they are
+ * rounded to bf16, about 2^-17 of their sums' terms. `workspace`: device memory, 8-byte aligned, of
  * hyb_gated_delta_chunked_prefill_workspace_size() bytes (a short, misaligned or missing one is
  * HYB_ERR_INVALID_ARG when B > 0); no initialisation, left alone between calls. Calls that may
  * run at the same time need workspaces of their own: see hyb_linear_attn_chunked_prefill, whose

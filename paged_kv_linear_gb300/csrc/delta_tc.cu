@@ -15,15 +15,17 @@
 // Precision. The state is fp32 and what reads or changes it is computed to fp32's accuracy on
 // bf16 tensor cores: K and Q are bf16 as given (their lengths, decays, beta and scale go into
 // fp32 factors of rows and columns, never into rounded operands), and S, W, the right-hand side R
-// and the corrections are each cut into three bf16 terms, h + m + l, which hold an fp32 number
+// and the corrections are each split into three bf16 terms, h + m + l, which hold an fp32 number
 // without loss. K S and the state's change then are exact products; of W R the terms beyond 2^-24
 // are left out (six of nine products). The tensor core's fp32 sums are cut, not rounded, at 24
 // bits: products go in with the smallest terms first, and the state's change is summed by itself
 // and then added to the decayed state, rounded to nearest. (Summed up in the state's own
 // accumulator, 12 cuts towards zero in 64 rows, 8192 rows of small changes put it off by 3.0e-5;
-// now 3.3e-7, the fp32 recurrence 2.3e-6.) Slow decays are applied as S + (e^G - 1) S: see get_state. The outputs, rounded to bf16 in the end, take two terms
-// of S, X and P (about 2^-16). With two terms throughout, states were off by some 3e-6; now by
-// 1.5e-7 after 77 rows, 2e-7 after 4096.
+// now 3.2e-7, the fp32 recurrence 2.3e-6.) Slow decays are applied as S + (e^G - 1) S: see get_state.
+// The outputs, rounded to bf16 in the end, take two terms of S, X and P, 2^-18.5 of each in the mean of
+// squares: TMEM and shared memory have no room for the third. 0.35 % of them come out as the bf16 next to
+// the one that the exact value rounds to (of the fp32 recurrence's 0.03 %). With two terms throughout,
+// states were off by some 3e-6; now by 1.6e-7 after 77 rows, 2e-7 after 1024.
 //
 // Layout. Everything on the chain is kept transposed: TMEM lane j is the state's value column j, so
 // each thread owns a column (half of its columns' range), nothing on the chain crosses threads, and
@@ -208,26 +210,27 @@ __device__ __forceinline__ bool next_chunk(const In& in, const Plan& pl, Walk& w
 }
 
 // ------------------------------------------------------------------ three-term splits
-// x = h + m + l by cutting off 8 bits of significand at a time: each remainder is exact, the
-// last has at most 8 bits left. Pairs are packed as the tensor core reads them.
+// x = h + m + l, h and m rounded to nearest: each remainder is exact, the last has at most 8 bits
+// left. (Cut instead of rounded, remainders are twice as large and have one sign: outputs, which take h
+// and m only, then come out on the other side of a bf16 rounding twice as often, 0.8 % of them for 0.35 %;
+// the time is the same.) Pairs are packed as the tensor core reads them.
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) {        // upper halves of a, b
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-__device__ __forceinline__ void rest(float& a, float& b) {             // x - cut(x) for both
-  unpair(fma2(pair(cut(a), cut(b)), pair(-1.f, -1.f), pair(a, b)), a, b);
+__device__ __forceinline__ void rest(float& a, float& b, uint32_t t) { // less their terms t
+  unpair(fma2(pair(bf16_lo(t), bf16_hi(t)), pair(-1.f, -1.f), pair(a, b)), a, b);
 }
 __device__ __forceinline__ void split3(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
-  h = pack_hi(a, b);
-  rest(a, b);
-  m = pack_hi(a, b);
-  rest(a, b);
+  h = pack_bf16(a, b);
+  rest(a, b, h);
+  m = pack_bf16(a, b);
+  rest(a, b, m);
   l = pack_hi(a, b);
 }
-// two terms, the second rounded: off by at most 2^-16
+// two terms: off by at most 2^-16, 2^-18.5 in the mean of squares
 __device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& m) {
-  h = pack_hi(a, b);
-  rest(a, b);
+  h = pack_bf16(a, b);
+  rest(a, b, h);
   m = pack_bf16(a, b);
 }
 
