@@ -429,3 +429,46 @@ def test_prefill_graph_replay_and_two_streams(hyb):
     step(hyb, cs[1], after, slots, 90)
     assert torch.equal(after, outs[1][:90]) and torch.equal(c.pool, cs[1].pool)
     assert hyb.hyb_device_status(clear=True) == (0, 0)
+
+
+def test_prefill_nan_stays_in_its_request_where_chains_share_ctas(hyb):
+    """More chains than two per SM, short and long ones mixed, so that a CTA runs several and cuts some: NaN
+    or infinity in every third request's rows, gates or state, and in the rows of no request behind the
+    last, changes no bit of the other requests."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B, gap = (2 * sms + 1 + 3) // 4 + 2, 70
+    rs = np.random.RandomState(9)
+    lens = [int(n) for n in np.where(rs.rand(B) < 0.7, rs.randint(1, 90, B), rs.randint(90, 330, B))]
+    lens[1], lens[5] = 0, 64
+    first = np.concatenate([[0], np.cumsum(lens)])
+    c = Case(25, sum(lens) + gap, 2, 4, 128, torch.bfloat16, B)
+    cu = torch.tensor(first, dtype=torch.int32, device="cuda")
+    slots = torch.tensor(rs.permutation(B), dtype=torch.int32, device="cuda")
+    start = c.pool.clone()
+
+    def call():
+        c.pool.copy_(start)
+        out = torch.full((c.T, 4, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+        prefill(hyb, c, out, cu, slots, None)
+        return out, c.pool.clone()
+
+    clean, clean_pool = call()
+    assert clean.isfinite().all() and clean_pool.isfinite().all()
+    bad = [b for b in range(2, B, 3) if lens[b] > 0]
+    what = [c.q, c.k, c.v, c.g, c.beta]
+    for i, b in enumerate(bad):
+        x = start if i % 6 == 5 else what[i % 6]
+        row = int(slots[b]) if i % 6 == 5 else int(first[b]) + int(rs.randint(lens[b]))
+        x[row] = math.inf if i % 12 < 6 and x is not c.g else math.nan
+    for x in what:
+        x[int(first[-1]):] = math.nan
+    out, pool = call()
+    same = torch.ones(c.T, dtype=torch.bool, device="cuda")
+    for b in bad:
+        same[int(first[b]):int(first[b + 1])] = False
+        rows = out[int(first[b]):int(first[b + 1])]
+        assert not (pool[slots[b].long()].isfinite().all() and rows.isfinite().all()), b
+    assert torch.equal(out[same], clean[same])
+    others = slots[[b for b in range(B) if b not in bad]].long()
+    assert torch.equal(pool[others], clean_pool[others])
+    assert hyb.hyb_device_status(clear=True) == (0, 0)
