@@ -240,3 +240,13 @@ def test_hybrid_layers_prefill_then_decode(hyb, devstatus):
         R.check_out(lin, o, mag, 2.0 ** -8, len(q), f"delta rule, request {b}", split=True)
         R.check_state(host(state)[b], S, norm, len(q), f"state {b}")
     assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("share", [2, 3, 5, 6])
+@pytest.mark.parametrize("Hq,Hk", [(32, 8), (32, 32), (5, 3)])
+def test_tokens_in_shares_and_more_than_one_pass(hyb, Hq, Hk, share):
+    """Tokens enough for several items a warp, but few enough that each is shared by several warps: the
+    steps from item to item carry from share to token."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    run(hyb, 32 * sms // share, Hq, Hk, 128, 128, torch.bfloat16, fused=True, seed=share + Hq)
+    run(hyb, 32 * sms // share - 7, Hq, Hk, 64, 32, torch.float32, interleaved=True, seed=share)
