@@ -472,3 +472,22 @@ def test_prefill_nan_stays_in_its_request_where_chains_share_ctas(hyb):
     others = slots[[b for b in range(B) if b not in bad]].long()
     assert torch.equal(pool[others], clean_pool[others])
     assert hyb.hyb_device_status(clear=True) == (0, 0)
+
+
+def test_prefill_request_alone_and_in_a_batch(hyb):
+    """Which kernel and which order of its sums a request gets depends on max_len and the number of
+    chains: alone, in a batch, or with a larger bound on the rows, it equals the recurrence to the same
+    tolerance, not bit by bit."""
+    T, B = 20, 64
+    c = Case(27, T * B, 2, 4, 128, torch.bfloat16, B)
+    start = c.pool.clone()
+    S0 = host(start[3])
+    o, S, mag, norm = c.ref(slice(3 * T, 4 * T), S0)
+    cu = torch.arange(0, T * B + 1, T, dtype=torch.int32, device="cuda")
+    slots = torch.arange(B, dtype=torch.int32, device="cuda")
+    for a, b, bound in ((0, B, None), (3, 4, None), (3, 4, 41)):
+        c.pool.copy_(start)
+        out = torch.zeros(c.T, 4, 128, device="cuda", dtype=torch.bfloat16)
+        prefill(hyb, c, out, cu[a:b + 1], slots[a:b], None, max_len=bound)
+        R.check_out(host(out)[3 * T:4 * T], o, mag, HALF[torch.bfloat16], T, f"{a} to {b}", split=True)
+        R.check_state(host(c.pool)[3], S, norm, T, f"{a} to {b}")
