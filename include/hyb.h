@@ -348,8 +348,8 @@ hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const
  * HYB_DEVERR_BAD_LENGTH, one with a bad slot HYB_DEVERR_BAD_STATE; it is skipped. Rows that
  * belong to no request are left as they were. With T = 0 the rows' pointers may be NULL.
  * bf16 with D = 128 runs the tensor-core kernel (chunks of 64 rows), other shapes and calls of
- * a few rows (max_len <= 8, or 40 when the requests are few) the token recurrence on the CUDA
- * cores. The states have fp32's accuracy in both; the tensor-core kernel's outputs, before they are
+ * a few rows (max_len <= 8, or few rows in all, or many requests of few rows beside a longer one)
+ * the token recurrence on the CUDA cores. The states have fp32's accuracy in both; the tensor-core kernel's outputs, before they are
  * rounded to bf16, about 2^-17 of their sums' terms. `workspace`: device memory, 8-byte aligned, of
  * hyb_gated_delta_chunked_prefill_workspace_size() bytes (a short, misaligned or missing one is
  * HYB_ERR_INVALID_ARG when B > 0); no initialisation, left alone between calls. Calls that may

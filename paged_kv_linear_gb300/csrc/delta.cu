@@ -188,14 +188,24 @@ struct DeltaScan {
 };
 
 // Whether the recurrence takes a call that the tensor-core kernel could take. That one needs a chunk's
-// time (13 us, and the same again for every SM's next chains) for a few rows too; the recurrence 4 us
-// and some 0.25 us a row, as long as its CTAs, four a chain, find SMs of their own, and in
-// proportion to the chains beyond that. Recurrence / tensor cores in us, heads of 128:
-//     chains     32: 32 rows 11.2 / 14.1, 40 rows 14.3 / 14.2     192: 8 rows 14.4 / 22.2
-//                64: 24 rows 12.7 / 14.0, 32 rows 14.8 / 14.2     512: 8 rows 32 / 36, 12 rows 38 / 36
-//               128: 12 rows 13.3 / 13.9, 16 rows 15.2 / 14.0    2048: 8 rows 122 / 128, 12 rows 144 / 128
-inline bool short_call(int max_len, int64_t chains) {
-  return max_len <= 8 || (max_len <= 40 && max_len * chains <= 1536);
+// time (14 us, and 4.5 us a chunk and a state for every SM's further ones) for a few rows too; the
+// recurrence 4 us and some 0.25 to 0.35 us a row of the longest request as long as its CTAs, four a chain,
+// find SMs of their own, and 0.04 us a chain and 0.003 us a row and head beyond that. So it takes
+//   * up to 8 rows a request, in any batch;
+//   * few rows in all, T x heads <= 1536, none of them in a long request;
+//   * more chains than SMs whose requests have few rows in the mean (decode steps beside a prompt), as
+//     long as the longest is over before the others' states have passed.
+// Recurrence / tensor cores in us, heads of 128:
+//     equal requests, chains 32: 32 rows 11.2 / 14.1, 40 rows 14.3 / 14.2    192: 8 rows 14.4 / 22.2
+//                            64: 24 rows 12.7 / 14.0, 32 rows 14.8 / 14.2    512: 8 rows 32 / 36, 12 rows 38 / 36
+//                           128: 12 rows 13.3 / 13.9, 16 rows 15.2 / 14.0   2048: 8 rows 122 / 128, 12 rows 144 / 128
+//     one request of m rows beside others of one row, 32 heads:
+//          3 others: m = 16 11.6 / 14.1, 32 17.6 / 14.3      31 others: m = 32 51 / 57, 64 67 / 59
+//          7 others: m = 16 16.4 / 22.6, 32 22.3 / 22.9     255 others: m = 64 359 / 489, 128 388 / 489
+inline bool short_call(int max_len, int T, int B, int heads) {
+  const int64_t chains = (int64_t)B * heads;
+  return max_len <= 8 || (max_len <= 32 && T * (int64_t)heads <= 1536) ||
+         (chains > num_sms() && T <= 10 * (int64_t)B && max_len <= 16 + chains / 16);
 }
 
 struct Quad {
@@ -541,7 +551,7 @@ hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const voi
   if (!workspace || !al(workspace, 8) || ws_bytes < kLinPrefillWsBytes) return HYB_ERR_INVALID_ARG;
   unsigned* sw = status_word();
   if (!sw) return HYB_ERR_CUDA;
-  if (delta_prefill_tc_supported(d) && !short_call(max_len, (int64_t)B * d->num_v_heads)) {
+  if (delta_prefill_tc_supported(d) && !short_call(max_len, T, B, d->num_v_heads)) {
     const Strides x = strides_of(d);
     return cuda_status(launch_delta_prefill_tc(out, q, k, v, g, beta, cu_seqlens, state_pool,
                                                num_state_slots, state_slots, reset, B, T, max_len,

@@ -491,3 +491,27 @@ def test_prefill_request_alone_and_in_a_batch(hyb):
         prefill(hyb, c, out, cu[a:b + 1], slots[a:b], None, max_len=bound)
         R.check_out(host(out)[3 * T:4 * T], o, mag, HALF[torch.bfloat16], T, f"{a} to {b}", split=True)
         R.check_state(host(c.pool)[3], S, norm, T, f"{a} to {b}")
+
+
+@pytest.mark.parametrize("long_rows", [9, 16, 64, 100])
+@pytest.mark.parametrize("n", [3, 255])
+def test_prefill_decode_rows_beside_a_prompt(hyb, n, long_rows):
+    """A batch of one-row requests and one of more rows, at both sides of the choice of the kernel."""
+    lens = [1] * n
+    lens.insert(n // 2, long_rows)
+    c = Case(26, sum(lens) + 1, 2, 4, 128, torch.bfloat16, n + 2, fused=True)
+    check_prefill(hyb, c, lens, [int(i % 5 == 0) for i in range(n + 1)], f"{n} rows and {long_rows}", gap=1)
+
+
+@pytest.mark.parametrize("lens,heads,launches", [([16], 32, 1), ([64], 32, 1), ([1] * 255 + [64], 4, 1), ([1] * 255 + [100], 4, 2), ([1] * 31 + [32], 32, 1), ([1] * 31 + [200], 32, 2),
+                                                 ([5] * 100 + [9] * 100, 4, 1), ([11] * 200, 4, 2)])
+def test_prefill_rows_of_the_whole_call_choose_the_kernel(hyb, lens, heads, launches):
+    """Decode rows beside a prompt are the recurrence's (one launch) where their states are most of the
+    work; the tensor-core kernel on more chains than SMs takes two launches."""
+    c = Case(28, sum(lens), heads // 2, heads, 128, torch.bfloat16, len(lens))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    slots = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    out = torch.empty(c.T, heads, 128, device="cuda", dtype=torch.bfloat16)
+    hyb.hyb_launch_count(reset=True)
+    prefill(hyb, c, out, cu, slots, None)
+    assert hyb.hyb_launch_count(reset=True) == launches
