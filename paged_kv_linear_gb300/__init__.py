@@ -142,6 +142,9 @@ def _rows(x, stride):
     return x.data_ptr()
 
 
+_PACKED = hyb_delta_dims_t()      # the strides of a call without dims, which the library refuses
+
+
 def _d(d):
     """Pointer to a dims structure (None passes NULL)."""
     return None if d is None else C.byref(d)
@@ -292,8 +295,9 @@ def hyb_gated_delta_step(out, q, k, v, g, beta, state_pool, num_state_slots, sta
                          stream=None):
     """One token per request of the gated delta rule; d: delta_dims(...). q, k and v may be
     views of wider rows whose token stride d gives."""
-    return _lib.hyb_gated_delta_step(_p(out), _rows(q, d.q_stride), _rows(k, d.k_stride),
-                                     _rows(v, d.v_stride), _p(g), _p(beta), _p(state_pool),
+    r = d or _PACKED
+    return _lib.hyb_gated_delta_step(_p(out), _rows(q, r.q_stride), _rows(k, r.k_stride),
+                                     _rows(v, r.v_stride), _p(g), _p(beta), _p(state_pool),
                                      num_state_slots, _p(state_slots), B, _d(d), _s(stream))
 
 
@@ -304,8 +308,9 @@ def hyb_gated_delta_chunked_prefill_workspace_size(B, T, d) -> int:
 def hyb_gated_delta_chunked_prefill(out, q, k, v, g, beta, cu_seqlens, state_pool, num_state_slots,
                                     state_slots, reset, B, T, max_len, d, workspace, ws_bytes,
                                     stream=None):
+    r = d or _PACKED
     return _lib.hyb_gated_delta_chunked_prefill(
-        _p(out), _rows(q, d.q_stride), _rows(k, d.k_stride), _rows(v, d.v_stride), _p(g), _p(beta),
+        _p(out), _rows(q, r.q_stride), _rows(k, r.k_stride), _rows(v, r.v_stride), _p(g), _p(beta),
         _p(cu_seqlens), _p(state_pool), num_state_slots, _p(state_slots), _p(reset), B, T, max_len,
         _d(d), _p(workspace), ws_bytes, _s(stream))
 
@@ -314,8 +319,9 @@ def hyb_qk_norm_rope_append(q_out, k_out, q, k, v, positions, slot_mapping, inv_
                             k_weight, T, k_cache, v_cache, r, d, stream=None):
     """Norm of each q and k head, rotary position and KV append in one pass; r: rope_dims(...),
     d: dims(...) of the cache. q, k and v may be views of wider rows whose token stride r gives."""
+    x = r or _PACKED
     return _lib.hyb_qk_norm_rope_append(
-        _p(q_out), _p(k_out), _rows(q, r.q_stride), _rows(k, r.k_stride), _rows(v, r.v_stride),
+        _p(q_out), _p(k_out), _rows(q, x.q_stride), _rows(k, x.k_stride), _rows(v, x.v_stride),
         _p(positions), _p(slot_mapping), _p(inv_freq), _p(q_weight), _p(k_weight), T, _p(k_cache),
         _p(v_cache), _d(r), _d(d), _s(stream))
 

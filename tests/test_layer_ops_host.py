@@ -130,6 +130,16 @@ def test_rows_of_another_stride_refused_by_the_binding(hyb):
             hyb._rows(Fake(s), 2048)
 
 
+def test_missing_dims_refused(hyb):
+    """Through the binding too, as its other calls do: a status, not a Python error."""
+    inv = hyb.HYB_ERR_INVALID_ARG
+    assert hyb.hyb_gated_delta_step(*(F,) * 7, 4, F, 2, None, 0) == inv
+    assert hyb.hyb_gated_delta_chunked_prefill(*(F,) * 8, 4, F, None, 2, 64, 32, None, F, 1 << 16, 0) == inv
+    d, r = hyb.dims(4, 128, 10, 4), hyb.rope_dims(8, 128)
+    for rr, dd in ((None, d), (r, None), (None, None)):
+        assert hyb.hyb_qk_norm_rope_append(F, None, *(F,) * 8, 4, F, F + 4096, rr, dd, 0) == inv
+
+
 # ----------------------------------------------------------------- pins of the 64-bit forms
 def test_delta_rule_pins():
     rs = np.random.RandomState(0)
