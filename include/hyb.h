@@ -343,7 +343,8 @@ hyb_status_t hyb_gated_delta_step(void* out, const void* q, const void* k, const
  * between calls changes only the rounding. So does the batch that a request comes in: the number
  * of chains (B x num_v_heads), T and max_len choose the kernel and the order of its sums. Equal calls
  * give equal bits. Two requests of one call must not share a slot. A request without rows keeps its state (zero with
- * reset). T (host) is the number of rows of q, k, v, g, beta and out, max_len (host) a bound on
+ * reset). T (host) is the number of rows of q, k, v, g, beta and out, at most 2^31 - 65
+ * (HYB_ERR_UNSUPPORTED beyond), max_len (host) a bound on
  * every request's rows. A request whose rows are not within [0, T), or more than max_len, sets
  * HYB_DEVERR_BAD_LENGTH, one with a bad slot HYB_DEVERR_BAD_STATE; it is skipped. Rows that
  * belong to no request are left as they were. With T = 0 the rows' pointers may be NULL.

@@ -546,6 +546,7 @@ hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const voi
       check_delta(out, q, k, v, g, beta, state_pool, num_state_slots, state_slots, B, T > 0, d);
   if (st != HYB_OK) return st;
   if (T < 0 || max_len < 0 || max_len > T) return HYB_ERR_INVALID_ARG;
+  if (T > INT32_MAX - 64) return HYB_ERR_UNSUPPORTED;      // rows are counted on by up to a chunk
   if (B == 0) return HYB_OK;
   if (!cu_seqlens || !al(cu_seqlens, 4)) return HYB_ERR_INVALID_ARG;
   if (!workspace || !al(workspace, 8) || ws_bytes < kLinPrefillWsBytes) return HYB_ERR_INVALID_ARG;

@@ -140,6 +140,14 @@ def test_missing_dims_refused(hyb):
         assert hyb.hyb_qk_norm_rope_append(F, None, *(F,) * 8, 4, F, F + 4096, rr, dd, 0) == inv
 
 
+def test_more_rows_than_the_kernels_count_refused(hyb):
+    d = hyb.delta_dims(2, 4, 128)
+    for dims in (d, hyb.delta_dims(2, 4, 64), hyb.delta_dims(2, 4, 16, hyb.HYB_F32)):
+        for T in (2 ** 31 - 64, 2 ** 31 - 1):
+            for max_len in (8, T):
+                assert hyb.hyb_gated_delta_chunked_prefill(*(F,) * 8, 4, F, None, 2, T, max_len, dims, F, 1 << 16, 0) == hyb.HYB_ERR_UNSUPPORTED
+
+
 # ----------------------------------------------------------------- pins of the 64-bit forms
 def test_delta_rule_pins():
     rs = np.random.RandomState(0)
