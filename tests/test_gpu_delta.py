@@ -515,3 +515,9 @@ def test_prefill_rows_of_the_whole_call_choose_the_kernel(hyb, lens, heads, laun
     hyb.hyb_launch_count(reset=True)
     prefill(hyb, c, out, cu, slots, None)
     assert hyb.hyb_launch_count(reset=True) == launches
+
+
+@pytest.mark.parametrize("lens,heads", [([32], 4), ([33], 4), ([32, 16], 32), ([32, 17], 32), ([10] * 40, 4), ([10] * 40 + [11], 4), ([1] * 59 + [31], 4), ([1] * 59 + [32], 4), ([1] * 37 + [25], 4)])
+def test_prefill_at_both_sides_of_the_kernel_choice(hyb, lens, heads):
+    c = Case(29, sum(lens), 2, heads, 128, torch.bfloat16, len(lens))
+    check_prefill(hyb, c, lens, None, f"{len(lens)} requests, the longest of {max(lens)}")
