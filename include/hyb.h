@@ -391,7 +391,8 @@ hyb_status_t hyb_gated_delta_chunked_prefill(void* out, const void* q, const voi
  *   k_cache, v_cache, slot_mapping: all three, or all three NULL (no append; v may then be NULL)
  * Apart from those, outputs overlap neither inputs nor one another. d gives the cache's shape
  * (num_heads, head_dim: 16, 32, 64, 128 or 256, block_size, num_blocks) and the type;
- * scale, window and max_blocks_per_seq are not used. T = 0 is a no-op.
+ * scale, window and max_blocks_per_seq are not used, but have to be valid as in the other calls
+ * (and num_blocks without a cache too). T = 0 is a no-op.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t num_q_heads;         /* heads of q; 0: no queries                             */

@@ -34,12 +34,13 @@ __device__ __forceinline__ float inv_len(float ss, float eps) {
 // element. A CTA owns 32 columns of one state, 8 threads x float4 to a row and 32 rows a pass; all
 // loads of a thread (PASSES x 16 bytes) are in flight before the first use, and columns do not
 // depend on one another, so no CTA waits for another. k and q go through shared memory, and so
-// do the sums over the 128 rows after a shuffle over the 4 rows of a warp: registers stay few (48), and
-// five CTAs per SM keep the loads of some while others store (three, at 69 registers: 55.8 us where
+// do the sums over the 128 rows after a shuffle over the 4 rows of a warp: registers stay few (48, two of
+// them spilled at D = 128, which costs less than a CTA), and five CTAs per SM keep the loads of some while others store (three, at 69 registers: 55.8 us where
 // it takes 46.4; the exact form of slow decays brought it to 47.5; of that form, six CTAs take 48.1
 // and four 52.0). States pass the caches as streams: plain stores 54.7, plain loads 48.2.
 // bf16, D = 128: 64 requests x 32 heads 47.5 us, 5.7 TB/s, 0.84 of the copy rate; 256 x 32 heads 193 us,
-// 0.82; one request 6.7 us a call, 2.7 on the GPU.
+// 0.82 (178 in passes over one pool, of which a part stays in L2); one request 6.7 us a call, 2.7 on
+// the GPU.
 template <int D>
 struct DeltaStep {
   static constexpr int COLS = D < 32 ? D : 32;

@@ -18,7 +18,9 @@
 // and the corrections are each split into three bf16 terms, h + m + l, which hold an fp32 number
 // without loss. K S and the state's change then are exact products; of W R the terms beyond 2^-24
 // are left out (six of nine products). The tensor core's fp32 sums are cut, not rounded, at 24
-// bits: products go in with the smallest terms first, and the state's change is summed by itself
+// bits: products go in with the smallest terms first (within each half of a sum, for the halves are
+// issued as their operands come: of K S 16 cuts, of X 14, of the state's change 8 are of a sum of full
+// size), and the state's change is summed by itself
 // and then added to the decayed state, rounded to nearest. (Summed up in the state's own
 // accumulator, 12 cuts towards zero in 64 rows, 8192 rows of small changes put it off by 3.0e-5;
 // now 3.2e-7, the fp32 recurrence 2.3e-6.) Slow decays are applied as S + (e^G - 1) S: see get_state.
@@ -38,11 +40,12 @@
 //   (w) X^T       = R^T W^T     A = R (TMEM),  B = W rows (6 pairs)    24
 //   (s) dS^T      = X'^T K      A = X e^(G_C - G) (TMEM), B = K^T      12 MMAs 128 x 128 x 16
 //   (o) D1Q       = X^T P^T     A = X (2 terms), B = P (3 pairs)       12
-// MMAs of N = 64 take 34 cycles of the tensor core, N = 128 67: 3.9K cycles a chunk.
+// MMAs of N = 64 take 34 cycles of the tensor core, N = 128 67: 3.7K cycles a chunk; with W's warp MMAs
+// the pipe is busy for 3.9K.
 //
 // W = (1 + A)^-1 in fp32 on the warps' own MMAs (tf32, two terms each) by blocks of 8, 16, 32 and 64. What
 // it is off by adds up over a chunk's rows where keys repeat: see tf32_terms. States against fp64 after
-// 1024 rows, no decay, beta 1: one key 4.6e-7 (fp32 recurrence 8.1e-7), keys of 2 dimensions 4.5e-7.
+// 1024 rows, no decay, beta 1: one key 4.4e-7 (fp32 recurrence 8.1e-7), keys of 2 dimensions 4.0e-7.
 //
 // Warps: 0-7 prepare chunks (lengths, factors, W, P), two groups of four with a chunk each, so a
 // chunk's preparation may take two chunks' time; 8-15 carry the chain (two warps to 32 lanes, each
@@ -53,12 +56,14 @@
 //
 // What bounds it: a chunk's way round its three loops (chain, preparation, outputs), each about 10K
 // cycles of waits for one another; leaving any one piece of work out changes the time by 0-3 %.
-// 8 requests of 8192 rows, 32 heads: 1.17 ms (tensor pipe 38 % busy, issue slots 49 %, 1.9 TB/s;
-// 0.28 of the copy rate); one request of 4096 rows: 311 us, 4.9 us a chunk; one of 77: 20 us. On the way,
+// 8 requests of 8192 rows, 32 heads: 1.20 ms (tensor pipe 37 % busy, issue slots 51 %, 1.8 TB/s;
+// 0.27 of the copy rate); one request of 4096 rows: 326 us, 5.1 us a chunk; one of 77: 20 us. On the way,
 // 8 x 8192: 13.5 ms token by token -> 2.54 (this design) -> 1.94 (elected MMA issue, integer gate
 // sums, chunk descriptors instead of local arrays) -> 1.56 (two preparing groups) -> 1.42 (warp MMAs
 // in W) -> 1.19 (rolled loops: less of the code falls out of the instruction cache) -> 1.12 (one site
-// for a run's setup) -> 1.19 (the state rounded to nearest) -> 1.17 (fewer instructions for W).
+// for a run's setup) -> 1.19 (the state rounded to nearest) -> 1.17 (fewer instructions for W, waits on
+// the SM's clock) -> 1.20 (slow decays without a drift, one prompt 318 -> 322 us; W's first terms and the
+// three-term splits rounded to nearest, one prompt 311 -> 318 and 322 -> 326 us).
 #include <cuda_bf16.h>
 
 #include "chain_split.cuh"
