@@ -21,8 +21,9 @@
 // bits: products go in with the smallest terms first (within each half of a sum, for the halves are
 // issued as their operands come: of K S 16 cuts, of X 14, of the state's change 8 are of a sum of full
 // size), and the state's change is summed by itself and then added to the decayed state, rounded to
-// nearest. (Summed up in the state's own accumulator, 12 cuts towards zero in 64 rows, 8192 rows of small changes put it off by 3.0e-5;
-// now 3.2e-7, the fp32 recurrence 2.3e-6.) Slow decays are applied as S + (e^G - 1) S: see get_state.
+// nearest. (Summed up in the state's own accumulator, 12 cuts towards zero in 64 rows, 8192 rows of
+// small changes put it off by 3.0e-5; now 3.2e-7, the fp32 recurrence 2.3e-6.) Slow decays are applied
+// as S + (e^G - 1) S: see get_state.
 // The outputs, rounded to bf16 in the end, take two terms of S, X and P, 2^-18.5 of each in the mean of
 // squares: TMEM and shared memory have no room for the third. 0.35 % of them come out as the bf16 next to
 // the one that the exact value rounds to (of the fp32 recurrence's 0.03 %). With two terms throughout,
