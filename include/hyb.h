@@ -73,6 +73,7 @@ typedef enum { HYB_MODE_DECODE = 0, HYB_MODE_PREFILL = 1 } hyb_mode_t;
 #define HYB_DEVERR_TIMEOUT       0x8u  /* a bounded device-side wait expired              */
 #define HYB_DEVERR_MISALIGNED    0x10u /* prefill start not on a chunk boundary           */
 #define HYB_DEVERR_BAD_LENGTH    0x20u /* a length exceeds the bound given on the host    */
+#define HYB_DEVERR_BAD_VALUE     0x40u /* a NaN or +infinity among logits or scores        */
 
 /* Dimensions of a Full-attention layer and its paged cache. */
 typedef struct {
@@ -414,6 +415,90 @@ hyb_status_t hyb_qk_norm_rope_append(void* q_out, void* k_out, const void* q, co
                                      const hyb_attn_dims_t* d, void* stream);
 
 /* -------------------------------------------------------------------------
+ * Decode attention of requests with a common beginning (the beams or samples of one prompt,
+ * conversations behind one system prompt): the group's common tokens are read once for all of
+ * its requests, each request's own tokens for it alone. Rows [cu_groups[g], cu_groups[g+1]) of
+ * q, out, seq_lens and block_tables are group g's requests; their first P = prefix_lens[g] tokens
+ * are the same. With n = seq_lens[b] (which counts the token appended this step) and query head j
+ * reading key head j / (num_q_heads / d->num_heads):
+ *     out[b][j][:] = sum_{p<n} softmax_p(scale * q[b][j].K_p) V_p
+ * K_p and V_p of p < P are read through the block table of the group's FIRST row, which must
+ * hold the prefix even where that request is shorter; those of p >= P through row b's own. A
+ * prefix may end inside a block: the tokens behind it are then the row's own, in the row's own
+ * block. A request with n < P sees its first n tokens of the prefix, one with n <= 0 gets
+ * zeros. d->window = W > 0 restricts p to n - W <= p < n; table entries of blocks that no
+ * request of the group (of the prefix) or not the request (of its own part) sees are not read.
+ *   q, out      [B][num_q_heads][D] of d->dtype; caches as for hyb_paged_attn_decode
+ *   cu_groups   int32 [G+1], prefix_lens int32 [G]. Rows that belong to no group are left as
+ *               they were. Groups of one request, empty groups and P = 0 are fine.
+ * A group whose rows are not within [0, B), decrease, or are more than max_group, or whose
+ * prefix is negative or above max_prefix_len, sets HYB_DEVERR_BAD_LENGTH; its out rows are left as they were, and
+ * so is a request's with n > P + max_suffix_len or n above the block table's capacity. A bad
+ * block id sets HYB_DEVERR_BAD_BLOCK and its tokens are left out.
+ * `workspace`: device memory, 16-byte aligned, hyb_paged_attn_decode_shared_prefix_workspace_size()
+ * bytes (the parts' partial results); no initialisation, nothing kept between calls. Calls that
+ * may run at the same time need workspaces of their own. The bounds, B and the heads choose how
+ * the keys are split, so the rounding depends on them; equal calls give equal bits. (dtype, D) as for
+ * hyb_paged_attn_decode. Limits: B x num_q_heads < 2^31 / 256, B and num_q_heads <= 65535,
+ * num_groups <= B + 65535, the bounds <= 2^24 and <= the block table's capacity.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t num_q_heads;         /* heads of q and out: a multiple of d->num_heads         */
+  int32_t num_groups;          /* G                                                       */
+  int32_t max_group;           /* a bound on the requests of a group                      */
+  int32_t max_prefix_len;      /* a bound on prefix_lens                                  */
+  int32_t max_suffix_len;      /* a bound on seq_lens[b] - prefix_lens[g]                 */
+} hyb_prefix_dims_t;
+
+size_t hyb_paged_attn_decode_shared_prefix_workspace_size(int32_t B, const hyb_prefix_dims_t* p,
+                                                          const hyb_attn_dims_t* d);
+hyb_status_t hyb_paged_attn_decode_shared_prefix(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* seq_lens, const int32_t* cu_groups,
+    const int32_t* prefix_lens, int32_t B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t* d,
+    void* workspace, size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------------------------
+ * Beam selection. Request r has beams w < W with a score (the log-probability so far) and a row
+ * of logits x over the vocabulary each (row r W + w). Every (w, v) with x_v > -infinity is a
+ * candidate of
+ *     total(w, v) = scores[r][w] + x_v - log sum_u exp(x_u)
+ * and the num_out best, in descending order, give scores_out, parents (w) and tokens (v);
+ * equal totals go by the lowest w V + v. Totals are compared in 64 bits (the sum over the vocabulary is
+ * one of 32-bit terms) and rounded once.
+ *   - A finished beam (finished[r][w] != 0) has one candidate, (w, eos_token), of total
+ *     scores[r][w]; its logits are not read. finished may be NULL (none).
+ *   - A beam of score -infinity has no candidates and its logits are not read: a request's
+ *     first step runs with scores (0, -infinity, ...).
+ *   - finished_out [r][i]: the parent was finished or the token is eos_token (may be NULL).
+ *   - Fewer candidates than num_out: the rest is (-infinity, -1, -1, 0).
+ *   - A row with a NaN or +infinity, or a beam of such a score, has no candidates and sets
+ *     HYB_DEVERR_BAD_VALUE.
+ *   logits      [R W][V] of dtype HYB_BF16 or HYB_F32, row_stride elements between rows (0:
+ *               packed; any value >= V)
+ *   scores, scores_out  fp32 [R][W], [R][num_out]; parents, tokens int32 [R][num_out]
+ * With num_out = W, scores_out may be scores and finished_out may be finished; apart from that
+ * outputs overlap nothing. R = 0 is a no-op. `workspace`: device memory, 16-byte aligned, of
+ * hyb_beam_select_workspace_size() bytes; no initialisation, nothing kept between calls;
+ * calls that may run at the same time need workspaces of their own. Equal calls give equal
+ * bits. Limits: num_beams <= 128, num_out <= 128 and <= W V, W V <= 2^31 - 1, R x W <= 2^20.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t num_beams;           /* W                                                       */
+  int32_t num_out;             /* candidates kept of each request (W, or 2 W, ...)        */
+  int32_t vocab;               /* V                                                       */
+  int32_t dtype;               /* of the logits                                           */
+  int32_t eos_token;           /* ends a beam; -1: none (finished must then be NULL)      */
+  int64_t row_stride;          /* elements between rows of logits; 0: packed              */
+} hyb_beam_dims_t;
+
+size_t hyb_beam_select_workspace_size(int32_t R, const hyb_beam_dims_t* d);
+hyb_status_t hyb_beam_select(float* scores_out, int32_t* parents, int32_t* tokens,
+                             uint8_t* finished_out, const void* logits, const float* scores,
+                             const uint8_t* finished, int32_t R, const hyb_beam_dims_t* d,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------------------------
  * A7. Layer dispatch [KV §2.2: layer types registered from the model config,
  * split memory pools, per-forward metadata of seq lens, block tables and state
  * buffers handed to each op together with the layer type; VL §3.2: an execution
@@ -471,6 +556,45 @@ hyb_status_t hyb_layer_dispatch(const int32_t* layer_types, int32_t L, int32_t m
                                 const hyb_layer_io_t* layers, const hyb_batch_meta_t* meta,
                                 const hyb_attn_dims_t* d, int32_t chunk_size, void* workspace,
                                 size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------------------------
+ * Reordering after a selection: the next beam i of request r goes on from parents[r][i]. Rows b =
+ * r W + w own their state slots and the cache blocks that hold tokens behind the request's
+ * prefix. A beam's first child takes over its row: table row and state slot move, no data does.
+ * The other children (and those of parent -1), in order, get the rows of the beams without
+ * children, in order, and a copy of their parent's data: the state of each Linear layer, tokens
+ * [P, n) of each Full layer (P = prefix_lens[r], n = seq_lens of the parent), of a SLIDING one
+ * those that the next token still sees. In place, with row(i) the old row that i gets:
+ *     block_tables[b][:] <- old block_tables[row(i)][:]      state_slots likewise
+ *     seq_lens[b] <- old seq_lens[parent], or of row(i) for parent -1 (nothing is copied then)
+ *   parents     int32 [R][W], as hyb_beam_select writes them; outside [-1, W): counts as -1 and
+ *               sets HYB_DEVERR_BAD_VALUE
+ *   block_tables [R W][max_blocks_per_seq] and seq_lens [R W]: needed where there is a Full or
+ *               SLIDING layer; either may be NULL otherwise. Whole blocks of the prefix (columns
+ *               below P / bs) are the same in all of a request's rows: they are not touched.
+ *               Where P ends inside a block, every row has the prefix's last tokens in a block of its own.
+ *   prefix_lens int32 [R], or NULL (0). state_slots int32 [R W]: needed where there is a Linear
+ *               layer, may be NULL otherwise
+ *   layer_types, layers  (host, [L]) as for hyb_layer_dispatch: k_cache and v_cache, window, or state_pool
+ *               and num_state_slots of each layer; out, q, k, v are not used. No two layers
+ *               share a pool
+ *   state_size  fp32 elements of one slot of a state pool (num_v_heads D D), a multiple of 4; not used without a Linear layer
+ *   max_suffix_len  a bound on n - P; a longer parent sets HYB_DEVERR_BAD_LENGTH and its tokens
+ *               are not copied, nor where n is above the table's capacity
+ *   d           num_heads (key heads), head_dim, block_size, num_blocks, max_blocks_per_seq and
+ *               dtype of the caches; the rest has to be valid as in the other calls
+ * Bad block ids set HYB_DEVERR_BAD_BLOCK, bad slots HYB_DEVERR_BAD_STATE, and what they name is
+ * not copied. `workspace`: device memory, 4-byte aligned, hyb_beam_reorder_workspace_size()
+ * bytes, no initialisation, nothing kept between calls. R = 0 or L = 0 moves no data (L = 0: tables
+ * and slots move all the same). Limits: W <= 128, R x W <= 65535, L <= 65535.
+ * ------------------------------------------------------------------------- */
+size_t hyb_beam_reorder_workspace_size(int32_t R, int32_t W);
+hyb_status_t hyb_beam_reorder(const int32_t* parents, int32_t* block_tables, int32_t* seq_lens,
+                              const int32_t* prefix_lens, int32_t* state_slots,
+                              const int32_t* layer_types, int32_t L, const hyb_layer_io_t* layers,
+                              int32_t R, int32_t W, int32_t max_suffix_len, int64_t state_size,
+                              const hyb_attn_dims_t* d, void* workspace, size_t ws_bytes,
+                              void* stream);
 
 /* -------------------------------------------------------------------------
  * Memory accounting [KV §2.1, §3.3]. All arguments are host values.

@@ -22,6 +22,7 @@ HYB_FULL, HYB_LINEAR, HYB_SLIDING = 0, 1, 2
 HYB_MODE_DECODE, HYB_MODE_PREFILL = 0, 1
 HYB_DEVERR_BAD_BLOCK, HYB_DEVERR_BAD_SLOT, HYB_DEVERR_BAD_STATE = 0x1, 0x2, 0x4
 HYB_DEVERR_TIMEOUT, HYB_DEVERR_MISALIGNED, HYB_DEVERR_BAD_LENGTH = 0x8, 0x10, 0x20
+HYB_DEVERR_BAD_VALUE = 0x40
 BLOCK_SIZE = 16
 
 
@@ -57,6 +58,16 @@ class hyb_rope_dims_t(C.Structure):
                 ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64)]
 
 
+class hyb_prefix_dims_t(C.Structure):
+    _fields_ = [("num_q_heads", C.c_int32), ("num_groups", C.c_int32), ("max_group", C.c_int32),
+                ("max_prefix_len", C.c_int32), ("max_suffix_len", C.c_int32)]
+
+
+class hyb_beam_dims_t(C.Structure):
+    _fields_ = [("num_beams", C.c_int32), ("num_out", C.c_int32), ("vocab", C.c_int32),
+                ("dtype", C.c_int32), ("eos_token", C.c_int32), ("row_stride", C.c_int64)]
+
+
 class HybError(RuntimeError):
     pass
 
@@ -88,6 +99,12 @@ def _load():
                                             sz, p],
         "hyb_gated_delta_chunked_prefill_workspace_size": ([i32, i32, p], sz),
         "hyb_qk_norm_rope_append": [p, p, p, p, p, p, p, p, p, p, i32, p, p, p, p, p],
+        "hyb_paged_attn_decode_shared_prefix_workspace_size": ([i32, p, p], sz),
+        "hyb_paged_attn_decode_shared_prefix": [p, p, p, p, p, p, p, p, i32, p, p, p, sz, p],
+        "hyb_beam_select_workspace_size": ([i32, p], sz),
+        "hyb_beam_select": [p, p, p, p, p, p, p, i32, p, p, sz, p],
+        "hyb_beam_reorder_workspace_size": ([i32, i32], sz),
+        "hyb_beam_reorder": [p, p, p, p, p, p, i32, p, i32, i32, i32, i64, p, p, sz, p],
         "hyb_layer_dispatch": [p, i32, i32, p, p, p, i32, p, sz, p],
         "hyb_cache_bytes": ([i32, i32, i32, i32, i64, i32, i32, i32, p, p], u64),
         "hyb_device_status": [p, i32],
@@ -201,6 +218,18 @@ def rope_dims(num_q_heads, rot_dim, eps=1e-6, interleaved=False, weight_offset=0
               attn_factor=1.0, q_stride=0, k_stride=0, v_stride=0) -> hyb_rope_dims_t:
     return hyb_rope_dims_t(num_q_heads, rot_dim, 1 if interleaved else 0, eps, weight_offset,
                            attn_factor, q_stride, k_stride, v_stride)
+
+
+def prefix_dims(num_q_heads, num_groups, max_group, max_prefix_len,
+                max_suffix_len) -> hyb_prefix_dims_t:
+    return hyb_prefix_dims_t(num_q_heads, num_groups, max_group, max_prefix_len, max_suffix_len)
+
+
+def beam_dims(num_beams, num_out, vocab, dtype=HYB_F32, eos_token=-1,
+              row_stride=0) -> hyb_beam_dims_t:
+    if not isinstance(dtype, int):
+        dtype = dtype_code(dtype)
+    return hyb_beam_dims_t(num_beams, num_out, vocab, dtype, eos_token, row_stride)
 
 
 def check(status: int, what: str = "hyb call") -> None:
@@ -326,6 +355,45 @@ def hyb_qk_norm_rope_append(q_out, k_out, q, k, v, positions, slot_mapping, inv_
         _p(v_cache), _d(r), _d(d), _s(stream))
 
 
+def hyb_paged_attn_decode_shared_prefix_workspace_size(B, p, d) -> int:
+    return int(_lib.hyb_paged_attn_decode_shared_prefix_workspace_size(B, _d(p), _d(d)))
+
+
+def hyb_paged_attn_decode_shared_prefix(out, q, k_cache, v_cache, block_tables, seq_lens, cu_groups,
+                                        prefix_lens, B, p, d, workspace, ws_bytes, stream=None):
+    """Decode attention of groups of requests with a common prefix, read once for each group;
+    p: prefix_dims(...), d: dims(...) of the cache (num_heads: its key heads)."""
+    return _lib.hyb_paged_attn_decode_shared_prefix(
+        _p(out), _p(q), _p(k_cache), _p(v_cache), _p(block_tables), _p(seq_lens), _p(cu_groups),
+        _p(prefix_lens), B, _d(p), _d(d), _p(workspace), ws_bytes, _s(stream))
+
+
+def _logits(x, row_stride):
+    """Device pointer of logits [rows][V] whose rows lie `row_stride` elements apart (0: packed)."""
+    if x is None or isinstance(x, int) or row_stride == 0:
+        return _p(x)
+    if not x.is_cuda:
+        raise HybError("device argument is not a CUDA tensor")
+    strides = x.stride()
+    if x.dim() != 2 or (x.shape[1] > 1 and strides[1] != 1) or (x.shape[0] > 1 and strides[0] != row_stride):
+        raise HybError(f"logits must have strides ({row_stride}, 1), not {strides}")
+    return x.data_ptr()
+
+
+def hyb_beam_select_workspace_size(R, d) -> int:
+    return int(_lib.hyb_beam_select_workspace_size(R, _d(d)))
+
+
+def hyb_beam_select(scores_out, parents, tokens, finished_out, logits, scores, finished, R, d,
+                    workspace, ws_bytes, stream=None):
+    """The best continuations of each request's beams; d: beam_dims(...). logits may be a
+    [rows][V] view of wider rows whose stride d gives."""
+    return _lib.hyb_beam_select(
+        _p(scores_out), _p(parents), _p(tokens), _p(finished_out),
+        _logits(logits, 0 if d is None else d.row_stride), _p(scores), _p(finished), R, _d(d),
+        _p(workspace), ws_bytes, _s(stream))
+
+
 def layer_io(out=None, q=None, k=None, v=None, k_cache=None, v_cache=None, state_pool=None,
              num_state_slots=0, window=0) -> hyb_layer_io_t:
     return hyb_layer_io_t(_p(out), _p(q), _p(k), _p(v), _p(k_cache), _p(v_cache),
@@ -348,6 +416,21 @@ def hyb_layer_dispatch(layer_types, L, mode, layers, meta, d, chunk_size, worksp
     io = (hyb_layer_io_t * max(L, 1))(*layers)
     return _lib.hyb_layer_dispatch(lt, L, mode, io, C.byref(meta), _d(d), chunk_size,
                                    _p(workspace), ws_bytes, _s(stream))
+
+
+def hyb_beam_reorder_workspace_size(R, W) -> int:
+    return int(_lib.hyb_beam_reorder_workspace_size(R, W))
+
+
+def hyb_beam_reorder(parents, block_tables, seq_lens, prefix_lens, state_slots, layer_types, L,
+                     layers, R, W, max_suffix_len, state_size, d, workspace, ws_bytes, stream=None):
+    """Tables, lengths, slots, states and cached tokens of the next beams, in place. layer_types
+    and layers: host sequences, as for hyb_layer_dispatch."""
+    lt = (C.c_int32 * max(L, 1))(*[int(x) for x in layer_types[:max(L, 0)]])
+    io = (hyb_layer_io_t * max(L, 1))(*layers[:max(L, 0)])
+    return _lib.hyb_beam_reorder(_p(parents), _p(block_tables), _p(seq_lens), _p(prefix_lens),
+                                 _p(state_slots), lt, L, io, R, W, max_suffix_len, state_size,
+                                 _d(d), _p(workspace), ws_bytes, _s(stream))
 
 
 def hyb_cache_bytes(L_full, L_linear, H, D, tokens, batch, kv_elem_bytes, state_elem_bytes):

@@ -1,0 +1,290 @@
+// Decode attention of groups of requests with a common prefix (hyb_paged_attn_decode_shared_prefix).
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "shared_prefix.cuh"
+
+namespace hyb {
+namespace {
+
+template <typename T>
+struct Row;
+template <>
+struct Row<__nv_bfloat16> {
+  static constexpr int VEC = 8;
+  __device__ static void unpack(const uint4& u, float* f) {
+    f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
+    f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+  }
+  __device__ static void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+};
+template <>
+struct Row<float> {
+  static constexpr int VEC = 4;
+  __device__ static void unpack(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  __device__ static void store(float* p, float x) { *p = x; }
+};
+
+// One part of one (row, query head): 4 warps take every fourth key, D / VEC lanes a key.
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+prefix_part_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
+                   const PrefixArgs a) {
+  constexpr int VEC = Row<T>::VEC, LPR = D / VEC, KPW = 32 / LPR;   // keys of a warp's load
+  __shared__ float red[4][D];
+  __shared__ float2 red_ml[4];
+  pdl_wait();
+  pdl_trigger();
+  const int part = blockIdx.x, b = blockIdx.y, h = blockIdx.z, hk = h / (a.Hq / a.Hk);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR, rr = lane / LPR;
+  const RowSpan r = find_row(a, b);
+  if (r.n < 0) return;
+  const bool shared = part < a.Sp;
+  if (shared ? !r.prefix_part(part, a.Lp) : part - a.Sp >= r.own_parts(a.Ls)) return;
+  int lo, hi;
+  if (shared) {
+    lo = max(part * a.Lp, r.lo);
+    hi = min((part + 1) * a.Lp, min(r.P, r.n));
+  } else {
+    const int base = r.own_base() + (part - a.Sp) * a.Ls;
+    lo = max(base, r.own_lo());
+    hi = min(base + a.Ls, r.n);
+  }
+  const int bs = kBlockSize << a.rsh;
+  const int32_t* table = a.bt + (int64_t)(shared ? r.first : b) * a.MB;
+  float qf[VEC], acc[VEC] = {}, m = -INFINITY, l = 0.f;
+  Row<T>::unpack(*reinterpret_cast<const uint4*>(q + ((int64_t)b * a.Hq + h) * D + c * VEC), qf);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) qf[e] *= a.scale_log2;
+  for (int p0 = lo + warp * KPW; p0 < hi; p0 += 4 * KPW) {
+    const int p = p0 + rr;
+    bool ok = p < hi;
+    float s = -INFINITY, vf[VEC] = {};
+    if (ok) {
+      const int pb = table[p / bs];
+      if (pb < 0 || pb >= a.NB) {
+        if (c == 0) flag(a.status, HYB_DEVERR_BAD_BLOCK);
+        ok = false;
+      } else {
+        const int64_t at = (((int64_t)pb * a.Hk + hk) * bs + p % bs) * D + c * VEC;
+        float kf[VEC];
+        Row<T>::unpack(*reinterpret_cast<const uint4*>(kc + at), kf);
+        Row<T>::unpack(*reinterpret_cast<const uint4*>(vc + at), vf);
+        s = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s = fmaf(qf[e], kf[e], s);
+      }
+    }
+#pragma unroll
+    for (int o = LPR / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (ok) {
+      const float mn = fmaxf(m, s);
+      const float al = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+      const float w = s == -INFINITY ? 0.f : fast_exp2(s - mn);
+      l = l * al + w;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = acc[e] * al + w * vf[e];
+      m = mn;
+    }
+  }
+  // the warp's key groups, then the warps
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+    const float M = fmaxf(m, m2);
+    const float x = m == -INFINITY ? 0.f : fast_exp2(m - M), y = m2 == -INFINITY ? 0.f : fast_exp2(m2 - M);
+    l = l * x + l2 * y;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = acc[e] * x + __shfl_xor_sync(0xffffffffu, acc[e], o) * y;
+    m = M;
+  }
+  if (rr == 0)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) red[warp][c * VEC + e] = acc[e];
+  if (lane == 0) red_ml[warp] = make_float2(m, l);
+  __syncthreads();
+  const int64_t o = ((int64_t)b * a.Hq + h) * (a.Sp + a.Ss) + part;
+  const float M = fmaxf(fmaxf(red_ml[0].x, red_ml[1].x), fmaxf(red_ml[2].x, red_ml[3].x));
+  for (int t = threadIdx.x; t < D; t += 128) {
+    float A = 0.f, Lsum = 0.f;
+    for (int w = 0; w < 4; ++w) {
+      const float x = red_ml[w].x == -INFINITY ? 0.f : fast_exp2(red_ml[w].x - M);
+      A += x * red[w][t];
+      Lsum += x * red_ml[w].y;
+    }
+    a.ws_acc[o * D + t] = A;
+    if (t == 0) a.ws_ml[o] = make_float2(M, Lsum);
+  }
+}
+
+// Joins the parts of one (row, query head); the first CTA also reports bad groups.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) prefix_join_kernel(T* __restrict__ out, const PrefixArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x, h = blockIdx.y;
+  if (b == 0 && h == 0)
+    for (int g = threadIdx.x; g < a.G; g += 128) {
+      int b0, b1, P;
+      if (!group_ok(a, g, b0, b1, P)) flag(a.status, HYB_DEVERR_BAD_LENGTH);
+    }
+  const int g = group_of(a, b);
+  int b0, b1, P;
+  if (g < 0 || !group_ok(a, g, b0, b1, P)) return;
+  const RowSpan r = row_span(a, b, b0, P);
+  if (r.n < 0) {
+    if (h == 0 && threadIdx.x == 0) flag(a.status, HYB_DEVERR_BAD_LENGTH);
+    return;
+  }
+  const int64_t bh = (int64_t)b * a.Hq + h, S = a.Sp + a.Ss;
+  const int own = r.own_parts(a.Ls);
+  const float2* ml = a.ws_ml + bh * S;
+  float M = -INFINITY;
+  for (int s = 0; s < a.Sp; ++s)
+    if (r.prefix_part(s, a.Lp)) M = fmaxf(M, ml[s].x);
+  for (int s = 0; s < own; ++s) M = fmaxf(M, ml[a.Sp + s].x);
+  for (int t = threadIdx.x; t < D; t += 128) {
+    float L = 0.f, A = 0.f;
+    auto add = [&](int s) {
+      const float2 v = ml[s];
+      const float x = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
+      L += x * v.y;
+      A += x * a.ws_acc[(bh * S + s) * D + t];
+    };
+    for (int s = 0; s < a.Sp; ++s)
+      if (r.prefix_part(s, a.Lp)) add(s);
+    for (int s = 0; s < own; ++s) add(a.Sp + s);
+    // M is -infinity where no key was seen; NaN comes through
+    Row<T>::store(out + bh * D + t, L == 0.f ? 0.f : A / L);
+  }
+}
+
+PrefixPlan plan_prefix(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t* d) {
+  PrefixPlan r;
+  r.Lp = r.Ls = 512;
+  r.Sp = (p->max_prefix_len + r.Lp - 1) / r.Lp;
+  int own = p->max_suffix_len;
+  if (d->window > 0) own = std::min(own, d->window);
+  r.Ss = own > 0 ? (own + kBlockSize - 1 + r.Ls - 1) / r.Ls : 0;
+  r.ws_bytes = (size_t)B * p->num_q_heads * (r.Sp + r.Ss) * ((size_t)d->head_dim * 4 + 8);
+  return r;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(void* out, const void* q, const void* kc, const void* vc, const PrefixArgs& a,
+                         cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (a.Sp + a.Ss > 0) {
+    e = launch_pdl(prefix_part_kernel<T, D>, dim3(a.Sp + a.Ss, a.B, a.Hq), dim3(128), 0, s, (const T*)q,
+                   (const T*)kc, (const T*)vc, a);
+    count_launch();
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_pdl(prefix_join_kernel<T, D>, dim3(a.B, a.Hq), dim3(128), 0, s, (T*)out, a);
+  count_launch();
+  return e;
+}
+
+cudaError_t launch_prefix(int dtype, int D, void* out, const void* q, const void* kc, const void* vc,
+                          const PrefixArgs& a, cudaStream_t s) {
+#define HYB_PRE(T, DD) \
+  if (D == DD) return launch_typed<T, DD>(out, q, kc, vc, a, s);
+  if (dtype == HYB_BF16) {
+    HYB_PRE(__nv_bfloat16, 16)
+    HYB_PRE(__nv_bfloat16, 32)
+    HYB_PRE(__nv_bfloat16, 64)
+    HYB_PRE(__nv_bfloat16, 128)
+    HYB_PRE(__nv_bfloat16, 256)
+  } else {
+    HYB_PRE(float, 16)
+    HYB_PRE(float, 32)
+    HYB_PRE(float, 64)
+    HYB_PRE(float, 128)
+  }
+#undef HYB_PRE
+  return cudaErrorInvalidValue;
+}
+
+bool al(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+hyb_status_t check_prefix_dims(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t* d) {
+  const hyb_status_t st = check_dims(d);
+  if (st != HYB_OK) return st;
+  if (!p || B < 0 || p->num_q_heads <= 0 || p->num_groups < 0 || p->max_group < 0 ||
+      p->max_prefix_len < 0 || p->max_suffix_len < 0)
+    return HYB_ERR_INVALID_ARG;
+  if (p->num_q_heads % d->num_heads != 0) return HYB_ERR_INVALID_ARG;
+  if (!decode_supported(d->dtype, d->head_dim)) return HYB_ERR_UNSUPPORTED;
+  if (B > 65535 || p->num_q_heads > 65535 || (int64_t)B * p->num_q_heads >= ((int64_t)1 << 23) ||
+      p->num_groups > B + 65535)
+    return HYB_ERR_UNSUPPORTED;
+  const int64_t cap = (int64_t)d->max_blocks_per_seq * d->block_size;
+  if (p->max_prefix_len > cap || p->max_suffix_len > cap || p->max_group > B) return HYB_ERR_INVALID_ARG;
+  if (p->max_prefix_len > (1 << 24) || p->max_suffix_len > (1 << 24)) return HYB_ERR_UNSUPPORTED;
+  return HYB_OK;
+}
+
+}  // namespace
+}  // namespace hyb
+
+using namespace hyb;
+
+extern "C" {
+
+size_t hyb_paged_attn_decode_shared_prefix_workspace_size(int32_t B, const hyb_prefix_dims_t* p,
+                                                          const hyb_attn_dims_t* d) {
+  if (B <= 0 || check_prefix_dims(B, p, d) != HYB_OK) return 0;
+  return plan_prefix(B, p, d).ws_bytes;
+}
+
+hyb_status_t hyb_paged_attn_decode_shared_prefix(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* seq_lens, const int32_t* cu_groups,
+    const int32_t* prefix_lens, int32_t B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t* d,
+    void* workspace, size_t ws_bytes, void* stream) {
+  const hyb_status_t st = check_prefix_dims(B, p, d);
+  if (st != HYB_OK) return st;
+  if (B == 0 || p->num_groups == 0) return HYB_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !cu_groups || !prefix_lens)
+    return HYB_ERR_INVALID_ARG;
+  if (!al(out, 16) || !al(q, 16) || !al(k_cache, 16) || !al(v_cache, 16) || !al(block_tables, 4) ||
+      !al(seq_lens, 4) || !al(cu_groups, 4) || !al(prefix_lens, 4))
+    return HYB_ERR_INVALID_ARG;
+  const PrefixPlan plan = plan_prefix(B, p, d);
+  if (plan.ws_bytes > 0 && (!workspace || !al(workspace, 16) || ws_bytes < plan.ws_bytes))
+    return HYB_ERR_INVALID_ARG;
+  unsigned* sw = status_word();
+  if (!sw) return HYB_ERR_CUDA;
+  PrefixArgs a;
+  a.bt = block_tables;
+  a.lens = seq_lens;
+  a.cu = cu_groups;
+  a.pre = prefix_lens;
+  a.B = B;
+  a.G = p->num_groups;
+  a.Hq = p->num_q_heads;
+  a.Hk = d->num_heads;
+  a.NB = d->num_blocks;
+  a.MB = d->max_blocks_per_seq;
+  a.rsh = log2_int(d->block_size / kBlockSize);
+  a.window = d->window;
+  a.max_group = p->max_group;
+  a.max_prefix = p->max_prefix_len;
+  a.max_suffix = p->max_suffix_len;
+  a.scale_log2 = d->scale * 1.4426950408889634f;
+  a.Lp = plan.Lp;
+  a.Sp = plan.Sp;
+  a.Ls = plan.Ls;
+  a.Ss = plan.Ss;
+  a.ws_acc = static_cast<float*>(workspace);
+  a.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
+                                      (size_t)B * a.Hq * (plan.Sp + plan.Ss) * d->head_dim * 4);
+  a.status = sw;
+  return cuda_status(launch_prefix(d->dtype, d->head_dim, out, q, k_cache, v_cache, a, (cudaStream_t)stream));
+}
+
+}  // extern "C"
