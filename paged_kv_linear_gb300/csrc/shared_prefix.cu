@@ -178,7 +178,10 @@ template <typename T, int D>
 cudaError_t launch_typed(void* out, const void* q, const void* kc, const void* vc, const PrefixArgs& a,
                          cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  if (a.Sp + a.Ss > 0) {
+  if constexpr (sizeof(T) == 2 && (D == 64 || D == 128 || D == 256)) {
+    e = launch_prefix_mma(D, q, kc, vc, a, true, s);
+    if (e != cudaSuccess) return e;
+  } else if (a.Sp + a.Ss > 0) {
     e = launch_pdl(prefix_part_kernel<T, D>, dim3(a.Sp + a.Ss, a.B, a.Hq), dim3(128), 0, s, (const T*)q,
                    (const T*)kc, (const T*)vc, a);
     count_launch();

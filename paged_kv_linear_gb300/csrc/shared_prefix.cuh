@@ -26,6 +26,11 @@ struct PrefixArgs {
   unsigned* status;
 };
 
+bool prefix_mma_supported(int dtype, int D);
+// prefix: the prefixes' parts too, not only those of the rows' own tokens
+cudaError_t launch_prefix_mma(int D, const void* q, const void* kc, const void* vc, const PrefixArgs& a,
+                              bool prefix, cudaStream_t s);
+
 #ifdef __CUDACC__
 // Rows [b0, b1) and prefix of a group; false where the call has to leave the group out.
 __device__ __forceinline__ bool group_ok(const PrefixArgs& a, int g, int& b0, int& b1, int& P) {
@@ -43,7 +48,7 @@ struct RowSpan {
   // tokens of its own are cut from here
   __device__ __forceinline__ int own_base() const { return own_lo() & ~(kBlockSize - 1); }
   __device__ __forceinline__ bool prefix_part(int s, int Lp) const {
-    return s * Lp < min(P, n) && (s + 1) * Lp > lo;
+    return max(s * Lp, lo) < min(min(P, n), (s + 1) * Lp);
   }
   __device__ __forceinline__ int own_parts(int Ls) const {
     return n > own_lo() ? (n - own_base() + Ls - 1) / Ls : 0;
