@@ -59,7 +59,7 @@ prefix_part_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
   float qf[VEC], acc[VEC] = {}, m = -INFINITY, l = 0.f;
   Row<T>::unpack(*reinterpret_cast<const uint4*>(q + ((int64_t)b * a.Hq + h) * D + c * VEC), qf);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) qf[e] *= a.scale_log2;
+  for (int e = 0; e < VEC; ++e) qf[e] *= a.q_sign ? -a.scale_log2 : a.scale_log2;
   for (int p0 = lo + warp * KPW; p0 < hi; p0 += 4 * KPW) {
     const int p = p0 + rr;
     bool ok = p < hi;
@@ -121,65 +121,123 @@ prefix_part_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
   }
 }
 
-// Joins the parts of one (row, query head); the first CTA also reports bad groups.
+constexpr int kJoinWarps = 4, kBatch = 8;   // parts whose loads are in flight together
+
+// Joins the parts of a (row, query head), one a warp, D / 32 columns a lane. What says which parts a row has was there before the
+// parts' kernel began, so it is read before that kernel ends. The first CTA also reports bad groups.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) prefix_join_kernel(T* __restrict__ out, const PrefixArgs a) {
-  pdl_wait();
+__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(T* __restrict__ out, const PrefixArgs a) {
+  constexpr int E = D / 32 > 0 ? D / 32 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x, h = blockIdx.y * kJoinWarps + warp;
   pdl_trigger();
-  const int b = blockIdx.x, h = blockIdx.y;
-  if (b == 0 && h == 0)
-    for (int g = threadIdx.x; g < a.G; g += 128) {
+  if (b == 0 && blockIdx.y == 0)
+    for (int g = threadIdx.x; g < a.G; g += kJoinWarps * 32) {
       int b0, b1, P;
       if (!group_ok(a, g, b0, b1, P)) flag(a.status, HYB_DEVERR_BAD_LENGTH);
     }
-  const int g = group_of(a, b);
-  int b0, b1, P;
-  if (g < 0 || !group_ok(a, g, b0, b1, P)) return;
-  const RowSpan r = row_span(a, b, b0, P);
+  bool bad;
+  const RowSpan r = find_row(a, b, &bad);
+  pdl_wait();
   if (r.n < 0) {
-    if (h == 0 && threadIdx.x == 0) flag(a.status, HYB_DEVERR_BAD_LENGTH);
+    if (bad && h == 0 && lane == 0) flag(a.status, HYB_DEVERR_BAD_LENGTH);
     return;
   }
+  if (h >= a.Hq) return;
   const int64_t bh = (int64_t)b * a.Hq + h, S = a.Sp + a.Ss;
-  const int own = r.own_parts(a.Ls);
+  // the used parts: [s0, s0 + np) of the prefix, then the row's own
+  const int p1 = min(r.P, r.n), s0 = r.lo / a.Lp, np = p1 > r.lo ? (p1 - 1) / a.Lp - s0 + 1 : 0;
+  const int used = np + r.own_parts(a.Ls);
   const float2* ml = a.ws_ml + bh * S;
-  float M = -INFINITY;
-  for (int s = 0; s < a.Sp; ++s)
-    if (r.prefix_part(s, a.Lp)) M = fmaxf(M, ml[s].x);
-  for (int s = 0; s < own; ++s) M = fmaxf(M, ml[a.Sp + s].x);
-  for (int t = threadIdx.x; t < D; t += 128) {
-    float L = 0.f, A = 0.f;
-    auto add = [&](int s) {
-      const float2 v = ml[s];
-      const float x = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
-      L += x * v.y;
-      A += x * a.ws_acc[(bh * S + s) * D + t];
-    };
-    for (int s = 0; s < a.Sp; ++s)
-      if (r.prefix_part(s, a.Lp)) add(s);
-    for (int s = 0; s < own; ++s) add(a.Sp + s);
-    // M is -infinity where no key was seen; NaN comes through
-    Row<T>::store(out + bh * D + t, L == 0.f ? 0.f : A / L);
+  const float* acc = a.ws_acc + bh * S * D + lane * E;
+  float M = -INFINITY, L = 0.f, A[E] = {};
+  for (int u0 = 0; u0 < used; u0 += kBatch) {  // (the sums keep the parts' order)
+    float2 v[kBatch];
+    float y[kBatch][E];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i, part = u < np ? s0 + u : a.Sp + u - np;
+      v[i] = u < used ? ml[part] : make_float2(-INFINITY, 0.f);
+      const float* p = acc + (int64_t)part * D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[i][e] = 0.f;
+      if (u >= used) continue;
+      if (E >= 4) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(y[i] + e) = *reinterpret_cast<const float4*>(p + e);
+      } else if (E == 2) {
+        *reinterpret_cast<float2*>(y[i]) = *reinterpret_cast<const float2*>(p);
+      } else if (lane < D) {
+        y[i][0] = p[0];
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) m = fmaxf(m, v[i].x);
+    const float old = M == -INFINITY ? 0.f : fast_exp2(M - m);
+    L *= old;
+#pragma unroll
+    for (int e = 0; e < E; ++e) A[e] *= old;
+    M = m;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float x = v[i].x == -INFINITY ? 0.f : fast_exp2(v[i].x - m);
+      L = fmaf(x, v[i].y, L);                  // (NaN comes through, also where no maximum is)
+#pragma unroll
+      for (int e = 0; e < E; ++e) A[e] = fmaf(x, y[i][e], A[e]);
+    }
   }
+  if (lane * E < D)
+#pragma unroll
+    for (int e = 0; e < E; ++e) Row<T>::store(out + bh * D + lane * E + e, L == 0.f ? 0.f : A[e] / L);
 }
+
+int round16(int64_t x) { return (int)((x + 15) / 16 * 16); }
 
 PrefixPlan plan_prefix(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t* d) {
   PrefixPlan r;
-  r.Lp = r.Ls = 512;
-  r.Sp = (p->max_prefix_len + r.Lp - 1) / r.Lp;
+  const int rep = p->num_q_heads / d->num_heads, D = d->head_dim, P = p->max_prefix_len;
+  const int64_t rows = (int64_t)p->max_group * rep, heads = (int64_t)p->num_groups * d->num_heads;
+  const int sms = num_sms();
+  const bool mma = prefix_mma_supported(d->dtype, D);
+  r.tc = mma && D == 128 && rep <= 128 && d->scale > 0.f && rows > 64;
+  if (r.tc) {
+    // one CTA an SM; a key tile of 128 takes it some 1.46 us, setup and drain 6 us
+    const int64_t tr = 2 * prefix_tc_tile_rows(rep), units = std::max<int64_t>(1, heads * ((rows + tr - 1) / tr));
+    const int tiles = std::max(1, (P + 127) / 128);
+    double best = 1e30;
+    r.Lp = 128;
+    for (int n = 1; n <= std::min(tiles, 64); ++n) {
+      const int64_t per = (tiles + n - 1) / n, used = (tiles + per - 1) / per, waves = (units * used + sms - 1) / sms;
+      const double t = waves * (1.46 * per + 6.0);
+      if (t < best) {
+        best = t;
+        r.Lp = (int)per * 128;
+      }
+    }
+  } else if (mma) {
+    const int64_t nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, units = std::max<int64_t>(1, heads * ((rows + 16 * nt - 1) / (16 * nt)));
+    const int64_t slots = (int64_t)sms * (D == 256 ? 1 : 3);
+    r.Lp = round16(std::min<int64_t>(1536, std::max<int64_t>(nt == 1 ? 512 : 256, P * units / slots)));
+  } else {
+    r.Lp = 512;
+  }
+  r.Ls = mma ? 256 : 512;
+  r.Sp = (P + r.Lp - 1) / r.Lp;
   int own = p->max_suffix_len;
   if (d->window > 0) own = std::min(own, d->window);
   r.Ss = own > 0 ? (own + kBlockSize - 1 + r.Ls - 1) / r.Ls : 0;
-  r.ws_bytes = (size_t)B * p->num_q_heads * (r.Sp + r.Ss) * ((size_t)d->head_dim * 4 + 8);
+  r.ws_bytes = (size_t)B * p->num_q_heads * (r.Sp + r.Ss) * ((size_t)D * 4 + 8);
   return r;
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(void* out, const void* q, const void* kc, const void* vc, const PrefixArgs& a,
-                         cudaStream_t s) {
+                         bool tc, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if constexpr (sizeof(T) == 2 && (D == 64 || D == 128 || D == 256)) {
-    e = launch_prefix_mma(D, q, kc, vc, a, true, s);
+    e = launch_prefix_mma(D, q, kc, vc, a, !tc, s);
+    if (e == cudaSuccess && tc) e = launch_prefix_tc(q, kc, vc, a, s);
     if (e != cudaSuccess) return e;
   } else if (a.Sp + a.Ss > 0) {
     e = launch_pdl(prefix_part_kernel<T, D>, dim3(a.Sp + a.Ss, a.B, a.Hq), dim3(128), 0, s, (const T*)q,
@@ -187,15 +245,16 @@ cudaError_t launch_typed(void* out, const void* q, const void* kc, const void* v
     count_launch();
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(prefix_join_kernel<T, D>, dim3(a.B, a.Hq), dim3(128), 0, s, (T*)out, a);
+  e = launch_pdl(prefix_join_kernel<T, D>, dim3(a.B, (a.Hq + kJoinWarps - 1) / kJoinWarps),
+                 dim3(kJoinWarps * 32), 0, s, (T*)out, a);
   count_launch();
   return e;
 }
 
 cudaError_t launch_prefix(int dtype, int D, void* out, const void* q, const void* kc, const void* vc,
-                          const PrefixArgs& a, cudaStream_t s) {
+                          const PrefixArgs& a, bool tc, cudaStream_t s) {
 #define HYB_PRE(T, DD) \
-  if (D == DD) return launch_typed<T, DD>(out, q, kc, vc, a, s);
+  if (D == DD) return launch_typed<T, DD>(out, q, kc, vc, a, tc, s);
   if (dtype == HYB_BF16) {
     HYB_PRE(__nv_bfloat16, 16)
     HYB_PRE(__nv_bfloat16, 32)
@@ -278,7 +337,8 @@ hyb_status_t hyb_paged_attn_decode_shared_prefix(
   a.max_group = p->max_group;
   a.max_prefix = p->max_prefix_len;
   a.max_suffix = p->max_suffix_len;
-  a.scale_log2 = d->scale * 1.4426950408889634f;
+  a.scale_log2 = std::max(std::fabs(d->scale) * 1.4426950408889634f, 1e-37f);
+  a.q_sign = d->scale < 0.f ? 0x80008000u : 0u;
   a.Lp = plan.Lp;
   a.Sp = plan.Sp;
   a.Ls = plan.Ls;
@@ -287,7 +347,8 @@ hyb_status_t hyb_paged_attn_decode_shared_prefix(
   a.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
                                       (size_t)B * a.Hq * (plan.Sp + plan.Ss) * d->head_dim * 4);
   a.status = sw;
-  return cuda_status(launch_prefix(d->dtype, d->head_dim, out, q, k_cache, v_cache, a, (cudaStream_t)stream));
+  return cuda_status(launch_prefix(d->dtype, d->head_dim, out, q, k_cache, v_cache, a, plan.tc,
+                                   (cudaStream_t)stream));
 }
 
 }  // extern "C"

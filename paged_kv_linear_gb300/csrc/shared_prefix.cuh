@@ -9,6 +9,7 @@
 namespace hyb {
 
 struct PrefixPlan {
+  bool tc;             // the prefixes on the tensor cores
   int Lp, Sp;          // keys of a prefix part; parts of the longest prefix
   int Ls, Ss;          // keys of a part of a row's own tokens; parts of the longest
   size_t ws_bytes;
@@ -19,7 +20,8 @@ struct PrefixArgs {
   const int32_t *bt, *lens, *cu, *pre;
   int B, G, Hq, Hk, NB, MB, rsh, window;   // rsh: log2(block size / 16)
   int max_group, max_prefix, max_suffix;
-  float scale_log2;
+  float scale_log2;                        // log2(e) |scale|, not 0 (which is the same as a tiny one)
+  uint32_t q_sign;                         // a pair's bf16 sign bits where the scale is negative
   int Lp, Sp, Ls, Ss;
   float* ws_acc;                           // [B][Hq][Sp + Ss][D]
   float2* ws_ml;                           // [B][Hq][Sp + Ss]
@@ -30,6 +32,10 @@ bool prefix_mma_supported(int dtype, int D);
 // prefix: the prefixes' parts too, not only those of the rows' own tokens
 cudaError_t launch_prefix_mma(int D, const void* q, const void* kc, const void* vc, const PrefixArgs& a,
                               bool prefix, cudaStream_t s);
+
+// the prefixes' parts on the tensor cores (bf16, D = 128, scale > 0, at most 128 query heads a key head)
+int prefix_tc_tile_rows(int rep);          // rows of one of its row tiles; a CTA takes two
+cudaError_t launch_prefix_tc(const void* q, const void* kc, const void* vc, const PrefixArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
 // Rows [b0, b1) and prefix of a group; false where the call has to leave the group out.
@@ -54,11 +60,10 @@ struct RowSpan {
     return n > own_lo() ? (n - own_base() + Ls - 1) / Ls : 0;
   }
 };
-__device__ __forceinline__ RowSpan row_span(const PrefixArgs& a, int b, int first, int P) {
+__device__ __forceinline__ RowSpan row_span(const PrefixArgs& a, int n, int first, int P) {
   RowSpan r;
   r.first = first;
   r.P = P;
-  const int n = a.lens[b];
   r.n = max(n, 0);
   r.lo = (a.window > 0 && n > a.window) ? n - a.window : 0;
   // (n and P are at most 2^31 - 1 and 2^24: the difference cannot overflow)
@@ -66,26 +71,31 @@ __device__ __forceinline__ RowSpan row_span(const PrefixArgs& a, int b, int firs
   return r;
 }
 
-// Whole warp: the group of row b (-1: none).
-__device__ __forceinline__ int group_of(const PrefixArgs& a, int b) {
-  const int lane = threadIdx.x & 31;
-  for (int g0 = 0; g0 < a.G; g0 += 32) {
-    const int g = g0 + lane;
-    const bool mine = g < a.G && a.cu[g] <= b && b < a.cu[g + 1];
-    const unsigned m = __ballot_sync(0xffffffffu, mine);
-    if (m) return g0 + __ffs(m) - 1;
-  }
-  return -1;
-}
-// Whole warp: row b's keys (n < 0: left out)
-__device__ __forceinline__ RowSpan find_row(const PrefixArgs& a, int b) {
-  const int g = group_of(a, b);
+// Whole warp: row b's keys (n < 0: left out); bad: whether that is for its length. Group bounds, prefixes
+// and the row's length are loaded side by side, so that a CTA with nothing to do leaves after one round trip.
+__device__ __forceinline__ RowSpan find_row(const PrefixArgs& a, int b, bool* bad = nullptr) {
+  const int lane = threadIdx.x & 31, n = a.lens[b];
   RowSpan r;
   r.first = r.P = r.lo = 0;
   r.n = -1;
-  int b0, b1, P;
-  if (g < 0 || !group_ok(a, g, b0, b1, P)) return r;
-  return row_span(a, b, b0, P);
+  if (bad) *bad = false;
+  for (int g0 = 0; g0 < a.G; g0 += 32) {
+    const int g = g0 + lane;
+    int b0 = 0, b1 = 0, P = 0;
+    const bool ok = g < a.G && group_ok(a, g, b0, b1, P);
+    const unsigned m = __ballot_sync(0xffffffffu, g < a.G && b0 <= b && b < b1);
+    if (!m) continue;
+    const int src = __ffs(m) - 1;
+    const bool good = __shfl_sync(0xffffffffu, ok, src);
+    b0 = __shfl_sync(0xffffffffu, b0, src);
+    P = __shfl_sync(0xffffffffu, P, src);
+    if (good) {
+      r = row_span(a, n, b0, P);
+      if (bad) *bad = r.n < 0;
+    }
+    break;
+  }
+  return r;
 }
 #endif
 

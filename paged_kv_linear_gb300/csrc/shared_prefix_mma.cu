@@ -7,286 +7,428 @@
 // all in registers: S's accumulators are the A fragment of P V.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "shared_prefix.cuh"
 #include "tc.cuh"
 
 namespace hyb {
 namespace {
 
-constexpr int kWarps = 4;                      // computing warps; one more fetches
+constexpr int kWarps = 4;
 constexpr float kRescale = 8.f;                // log2: the largest p before the base moves
+constexpr float kNoBase = -3.3e38f;            // the base of a row that has seen no key
 
 template <int D, int NT>
 struct MmaShape {
-  static constexpr int KG = kWarps / NT;       // key groups: rings of pieces, each read by NT warps
+  static constexpr int KG = kWarps / NT;       // key groups: rings of stages, each read by NT warps
+  static constexpr int KP = NT == 1 ? 1 : NT == 4 && D == 64 ? 4 : 2;   // pieces of a stage
   static constexpr int TILE = 16 * D * 2;      // K or V of a piece
-  static constexpr int NST = 65536 / (KG * 2 * TILE) > 2 ? 65536 / (KG * 2 * TILE) : 2;
-  static constexpr int RING = KG * NST * 2 * TILE;
+  static constexpr int FIT = 65536 / (KG * KP * 2 * TILE);
+  static constexpr int NST = FIT > 2 ? FIT : 2;
+  static constexpr int LAG = NT == 1 || NST < 4 ? 0 : 1;
+  static constexpr int RING = KG * NST * KP * 2 * TILE;
   static constexpr int PITCH = D + 8;          // floats of a row where key groups are joined
   static constexpr int JOIN = kWarps * 16 * PITCH * 4;
   static constexpr int BODY = KG > 1 && JOIN > RING ? JOIN : RING;
-  static constexpr int BARS = BODY;            // full, empty: u64 [KG][NST]; ok: int [KG][NST]
-  static constexpr int ROWS = BARS + KG * NST * 20 + 16;         // int lo[64], hi[64]; float2 ml[64]
-  static constexpr int SMEM = ROWS + 64 * 16 + 1024;             // 1 KiB of alignment slack
+  static constexpr int BARS = BODY;            // full, empty: u64 [KG][NST]; have: int [KG][NST]
+  static constexpr int ROWS = BARS + KG * NST * 20 + 16;         // float2 ml[64]
+  static constexpr int SMEM = ROWS + 64 * 8 + 1024;             // 1 KiB of alignment slack
 };
 
-// What a CTA works on: rows row0 .. row0 + rows - 1 of those of key head hk from request first on
+template <int D>
+struct OwnShape {
+  static constexpr int TILE = 16 * D * 2;
+  static constexpr int NST = 16384 / (2 * TILE) > 2 ? 16384 / (2 * TILE) : 2;
+  static constexpr int RING = kWarps * NST * 2 * TILE;
+  static constexpr int SMEM = RING + kWarps * NST * 8 + 1024;
+};
+
+// What a CTA (of a request's own tokens: a warp) works on: rows row0 .. row0 + rows - 1 of those of key head hk from request first on
 // (row i: request first + i / rep, query head hk rep + i % rep), keys [k0, k1) through `table`.
 struct Unit {
   const int32_t* table;
   int first, hk, row0, rows, part, k0, k1;
 };
 
+// four 8 x 8 matrices at addr + OFF (an immediate), as they are or transposed
+template <int OFF>
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr), "n"(OFF));
 }
+template <int OFF>
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr), "n"(OFF));
+}
+// f(0), f(1), ... with the number as a constant
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<N, I + 1>(f);
+  }
 }
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A warp's 16 query rows against pieces of 16 keys: rows lane / 4 and lane / 4 + 8, key or column pairs
+// lane % 4 of every 8.
+template <int D>
+struct WarpTile {
+  static constexpr int TILE = 16 * D * 2;
+  uint32_t qa[D / 16][4];
+  float o[D / 8][4], m[2], l[2];
+  int lo0, hi0, lo1, hi1;              // keys that the two rows see
+
+  // sign: turns q's sign bits where the scale is negative
+  __device__ __forceinline__ void start(const __nv_bfloat16* q0, const __nv_bfloat16* q1, uint32_t sign) {
+    const int quad = threadIdx.x & 3;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const int c = k * 16 + quad * 2;
+      qa[k][0] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + c) ^ sign : 0u;
+      qa[k][1] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + c) ^ sign : 0u;
+      qa[k][2] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + c + 8) ^ sign : 0u;
+      qa[k][3] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + c + 8) ^ sign : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+    m[0] = m[1] = kNoBase;
+    l[0] = l[1] = 0.f;
+    lo0 = hi0 = lo1 = hi1 = 0;
+  }
+
+  // KP pieces (16 KP tokens from tok on) at kt, each K, then V. Only keys [k0, k1) are there, and of the
+  // pieces only those of the mask `have`; keys in [max_lo, min_hi) are seen by every row.
+  template <int KP>
+  __device__ __forceinline__ void step(int tok, uint8_t* kt, unsigned have, int k0, int k1, int min_hi, int max_lo,
+                                       float scale_log2) {
+    const int lane = threadIdx.x & 31, quad = lane & 3;
+    // a lane's row and 16-byte chunk in the four 8 x 8 matrices of a load
+    const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
+    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
+    constexpr int kKeys = KP * kBlockSize, NC = KP == 1 ? 2 : 1;     // chains of sums per 8 keys
+    // Chunk 2 k + kch of row krow lies at ((2 k + kch) ^ (krow & 7)) * 16 of its 128 bytes. The stage lies on
+    // 1 KiB, so the k-th address is the first with bits 5 and 6 turned by k % 4, and the
+    // rest an immediate.
+    const uint32_t ks = smem_u32(kt) + sw128_off(krow, kch), vs = smem_u32(kt) + TILE + sw128_off(vrow, vch);
+    const uint32_t ka[4] = {ks, ks ^ 32u, ks ^ 64u, ks ^ 96u}, va[4] = {vs, vs ^ 32u, vs ^ 64u, vs ^ 96u};
+    float s[NC][2 * KP][4];
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[n][i][c] = 0.f;
+    each<D / 16 * KP>([&](auto n) {
+      constexpr int k = n / KP, j = n % KP;
+      uint32_t b[4];
+      ldsm4<j * 2 * TILE + (k / 4) * 2048>(ka[k % 4], b);
+      mma16816(s[k % NC][2 * j], qa[k], b[0], b[1]);
+      mma16816(s[k % NC][2 * j + 1], qa[k], b[2], b[3]);
+    });
+    float x[2 * KP][4];
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[i][c] = NC == 2 ? s[0][i][c] + s[NC - 1][i][c] : s[0][i][c];
+    const bool edge = tok < k0 || tok + kKeys > k1 || have != (1u << KP) - 1;
+    if (edge || tok < max_lo || tok + kKeys > min_hi) {
+#pragma unroll
+      for (int i = 0; i < 2 * KP; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int key = tok + i * 8 + quad * 2 + (c & 1);
+          const bool see = ((have >> (i / 2)) & 1) && key >= k0 && key < k1 &&
+                           (c < 2 ? key >= lo0 && key < hi0 : key >= lo1 && key < hi1);
+          if (!see) x[i][c] = -INFINITY;
+        }
+      if (edge) {
+        // rows that hold no key of the part may hold NaN, and 0 x NaN is NaN (every warp that
+        // reads the stage writes the same zeros first)
+        for (int e = lane; e < kKeys * D / 8; e += 32) {
+          const int r = e / (D / 8), ch = e % (D / 8);
+          if (tok + r < k0 || tok + r >= k1 || !((have >> (r / kBlockSize)) & 1))
+            *reinterpret_cast<uint4*>(kt + (r / kBlockSize) * 2 * TILE + TILE + (ch >> 3) * 2048 +
+                                      (r % kBlockSize) * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();                // the ring's next copy comes after these writes
+        __syncwarp();
+      }
+    }
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i) {
+      mx0 = fmaxf(mx0, fmaxf(x[i][0], x[i][1]));
+      mx1 = fmaxf(mx1, fmaxf(x[i][2], x[i][3]));
+    }
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
+    }
+    mx0 *= scale_log2;                     // (scale > 0 keeps the order)
+    mx1 *= scale_log2;
+    // the base moves only where a row's maximum outgrows it: p stays below 2^8
+    const bool g0 = mx0 > m[0] + kRescale, g1 = mx1 > m[1] + kRescale;
+    if (__any_sync(0xffffffffu, g0 || g1)) {
+      const float a0 = g0 ? fast_exp2(m[0] - mx0) : 1.f, a1 = g1 ? fast_exp2(m[1] - mx1) : 1.f;
+      if (g0) m[0] = mx0;
+      if (g1) m[1] = mx1;
+      l[0] *= a0;
+      l[1] *= a1;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= a0;
+        o[i][1] *= a0;
+        o[i][2] *= a1;
+        o[i][3] *= a1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * KP; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[i][c] = fast_exp2(fmaf(x[i][c], scale_log2, -m[c / 2]));
+      l[0] += x[i][0] + x[i][1];
+      l[1] += x[i][2] + x[i][3];
+    }
+#pragma unroll
+    for (int j = 0; j < KP; ++j) {
+      // P as bf16: half a step of each weight
+      const uint32_t pa[4] = {pack_bf16(x[2 * j][0], x[2 * j][1]), pack_bf16(x[2 * j][2], x[2 * j][3]),
+                              pack_bf16(x[2 * j + 1][0], x[2 * j + 1][1]), pack_bf16(x[2 * j + 1][2], x[2 * j + 1][3])};
+      each<D / 16>([&](auto kk) {
+        constexpr int k = kk;
+        uint32_t b[4];
+        ldsm4_t<(k / 4) * 2048>(va[k % 4] + j * 2 * TILE, b);
+        mma16816(o[2 * k], pa, b[0], b[1]);
+        mma16816(o[2 * k + 1], pa, b[2], b[3]);
+      });
+    }
+  }
+
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
+    }
+    if (m[0] == kNoBase) m[0] = -INFINITY;
+    if (m[1] == kNoBase) m[1] = -INFINITY;
+  }
+};
+
+// Fills a ring of NST stages of KP pieces with every step-th stage of a part, by a whole warp.
+template <int D, int NST, int KP>
+struct Fetch {
+  static constexpr int TILE = 16 * D * 2, AHEAD = 32 / KP;     // stages whose rows are looked up together
+  const int32_t* table;
+  uint8_t* ring;
+  uint64_t* full;
+  int hk, sub0, subs, first, step, count;    // pieces [sub0, sub0 + subs) of the sequence; stages first, first + step, ..
+  int y, next;                               // pool rows of AHEAD stages' pieces, one a lane; the stage to ask for next
+
+  // asks for the next stage; which of its pieces there are (a bad block's is left out) is returned, and
+  // written to have[stage] for other warps, before the arrival that they wait for
+  __device__ __forceinline__ unsigned issue(const PrefixArgs& a, const CUtensorMap* tk, const CUtensorMap* tv,
+                                            int* have = nullptr) {
+    const int lane = threadIdx.x & 31;
+    if (next % AHEAD == 0) {
+      y = -1;
+      const int sub = (first + (next + lane / KP) * step) * KP + lane % KP;
+      if (next + lane / KP < count && sub < subs) {
+        const int pb = table[(sub0 + sub) >> a.rsh];
+        if (pb < 0 || pb >= a.NB) flag(a.status, HYB_DEVERR_BAD_BLOCK);
+        else y = ((pb * a.Hk + hk) << (4 + a.rsh)) + (((sub0 + sub) & ((1 << a.rsh) - 1)) << 4);
+      }
+    }
+    const int st = next % NST;
+    const unsigned mask = (__ballot_sync(0xffffffffu, y >= 0) >> (next % AHEAD * KP)) & ((1u << KP) - 1);
+    if (lane == 0) {
+      if (have) have[st] = mask;
+      if (mask) mbar_expect_tx(&full[st], __popc(mask) * 2 * TILE);
+      else mbar_arrive(&full[st]);
+    }
+#pragma unroll
+    for (int j = 0; j < KP; ++j) {
+      const int row = __shfl_sync(0xffffffffu, y, next % AHEAD * KP + j);
+      if (row >= 0 && lane == 0) {
+        uint8_t* dst = ring + (st * KP + j) * 2 * TILE;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + c * 2048, tk, c * 64, row, &full[st]);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + TILE + c * 2048, tv, c * 64, row, &full[st]);
+      }
+    }
+    ++next;
+    return mask;
+  }
+};
+
+// One warp's part of a request's own tokens: its ring of pieces is its own, filled by its lane 0.
+template <int D>
+__device__ __forceinline__ void attend_own(const CUtensorMap* tk, const CUtensorMap* tv,
+                                           const __nv_bfloat16* __restrict__ q, const PrefixArgs& a, const Unit& u,
+                                           int own_lo, uint8_t* sm) {
+  constexpr int TILE = 16 * D * 2, NST = OwnShape<D>::NST;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rep = a.Hq / a.Hk;
+  uint8_t* ring = sm + warp * NST * 2 * TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + OwnShape<D>::RING) + warp * NST;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < NST; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const int k0 = max(u.k0, own_lo), k1 = u.k1, np = (k1 - u.k0 + kBlockSize - 1) / kBlockSize;
+  WarpTile<D> w;
+  const int r0 = lane >> 2, r1 = r0 + 8, quad = lane & 3;
+  const int64_t row = (int64_t)u.first * a.Hq + u.hk * rep + u.row0;
+  w.start(r0 < u.rows ? q + (row + r0) * D : nullptr, r1 < u.rows ? q + (row + r1) * D : nullptr, a.q_sign);
+  w.lo0 = w.lo1 = k0;
+  w.hi0 = w.hi1 = k1;
+  Fetch<D, NST, 1> f{u.table, ring, full, u.hk, u.k0 / kBlockSize, np, 0, 1, np, -1, 0};
+  unsigned have = 0;                     // of the pieces in the ring, by stage
+  auto issue = [&]() {
+    const int st = f.next % NST;
+    have = (have & ~(1u << st)) | f.issue(a, tk, tv) << st;
+  };
+  while (f.next < NST && f.next < np) issue();
+  for (int i = 0; i < np; ++i) {
+    const int st = i % NST;
+    if (!__all_sync(0xffffffffu, mbar_wait_cycles(&full[st], (i / NST) & 1))) {
+      if (lane == 0) {                   // report, and let the copies in flight land
+        flag(a.status, HYB_DEVERR_TIMEOUT);
+        for (int j = i; j < f.next; ++j) mbar_wait_cycles(&full[j % NST], (j / NST) & 1, 200000000u);
+      }
+      break;
+    }
+    if ((have >> st) & 1)
+      w.template step<1>(u.k0 + i * kBlockSize, ring + st * 2 * TILE, 1u, k0, k1, k1, k0, a.scale_log2);
+    __syncwarp();
+    if (f.next < np) issue();
+  }
+  w.finish();
+  const int parts = a.Sp + a.Ss;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = half ? r1 : r0;
+    if (r >= u.rows) continue;
+    const int64_t at = (row + r) * parts + u.part;
+    if (quad == 0) a.ws_ml[at] = make_float2(w.m[half], w.l[half]);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      *reinterpret_cast<float2*>(a.ws_acc + at * D + i * 8 + quad * 2) = make_float2(w.o[i][2 * half], w.o[i][2 * half + 1]);
+  }
+}
+
 template <int D, int NT>
 __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap* tv,
                                        const __nv_bfloat16* __restrict__ q, const PrefixArgs& a, const Unit& u,
-                                       int P, bool shared, uint8_t* sm) {
+                                       int P, uint8_t* sm) {
   using S = MmaShape<D, NT>;
-  constexpr int KG = S::KG, NST = S::NST, TILE = S::TILE, NB64 = D / 64;
+  constexpr int KG = S::KG, NST = S::NST, KP = S::KP, TILE = S::TILE;
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::BARS);
   uint64_t* empty = full + KG * NST;
-  int* okp = reinterpret_cast<int*>(empty + KG * NST);
-  int* row_lo = reinterpret_cast<int*>(sm + S::ROWS);
-  int* row_hi = row_lo + 64;
-  float2* red_ml = reinterpret_cast<float2*>(row_hi + 64);
+  int* have_s = reinterpret_cast<int*>(empty + KG * NST);
+  float2* red_ml = reinterpret_cast<float2*>(sm + S::ROWS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rep = a.Hq / a.Hk;
-
-  if (tid < 16 * NT) {                         // keys that a row sees; hi 0: a row that is not there
-    int lo = 0, hi = 0;
-    if (tid < u.rows) {
-      const RowSpan r = row_span(a, u.first + (u.row0 + tid) / rep, 0, P);
-      lo = shared ? r.lo : r.own_lo();
-      hi = shared ? min(P, r.n) : r.n;
-    }
-    row_lo[tid] = lo;
-    row_hi[tid] = hi;
-  }
-  if (tid == kWarps * 32) {
+  if (tid == 96) {
     for (int i = 0; i < KG * NST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], NT);
     }
     fence_mbar_init();
   }
-  __syncthreads();
-  // the tile's bounds over its rows (rows that see nothing do not count for the lower ones)
-  int max_hi = 0, min_lo = INT32_MAX, min_hi = INT32_MAX, max_lo = 0;
-#pragma unroll
-  for (int i = 0; i < (16 * NT + 31) / 32; ++i) {
-    const int r = i * 32 + lane;
-    if (r < 16 * NT && row_hi[r] > row_lo[r]) {
-      max_hi = max(max_hi, row_hi[r]);
-      min_lo = min(min_lo, row_lo[r]);
+  int k0 = u.k0, k1 = u.k1;
+  if (a.window > 0) {                          // only keys that one of the rows sees (otherwise: all but always all)
+    int max_hi = 0, min_lo = INT32_MAX;
+    for (int r = lane; r < u.rows; r += 32) {
+      const RowSpan x = row_span(a, a.lens[u.first + (u.row0 + r) / rep], 0, P);
+      if (min(P, x.n) > x.lo) {
+        max_hi = max(max_hi, min(P, x.n));
+        min_lo = min(min_lo, x.lo);
+      }
     }
-    if (r < u.rows) {
-      min_hi = min(min_hi, row_hi[r]);
-      max_lo = max(max_lo, row_lo[r]);
-    }
+    k0 = max(k0, __reduce_min_sync(0xffffffffu, min_lo));
+    k1 = min(k1, __reduce_max_sync(0xffffffffu, max_hi));
+    if (k0 >= k1) return;                      // (the same in every warp)
   }
-  max_hi = __reduce_max_sync(0xffffffffu, max_hi);
-  min_lo = __reduce_min_sync(0xffffffffu, min_lo);
-  min_hi = __reduce_min_sync(0xffffffffu, min_hi);
-  max_lo = __reduce_max_sync(0xffffffffu, max_lo);
-  const int k0 = max(u.k0, min_lo), k1 = min(u.k1, max_hi);
-  if (k0 >= k1) return;                        // nothing that a row sees (min_lo may be INT32_MAX)
+  __syncthreads();
   const int kb = k0 & ~(kBlockSize - 1), np = (k1 - kb + kBlockSize - 1) / kBlockSize;
 
-  bool ok = true;
-  if (warp == kWarps) {
-    // ------------------------------------------------------------------ fetching
-    int issued = 0;
-    for (int i0 = 0; i0 < np && ok; i0 += 32) {
-      int y = -1;                              // pool row of piece i0 + lane
-      if (i0 + lane < np) {
-        const int sub = kb / kBlockSize + i0 + lane;
-        const int pb = u.table[sub >> a.rsh];
-        if (pb < 0 || pb >= a.NB) flag(a.status, HYB_DEVERR_BAD_BLOCK);
-        else y = ((pb * a.Hk + u.hk) << (4 + a.rsh)) + ((sub & ((1 << a.rsh) - 1)) << 4);
-      }
-      const int cnt = min(32, np - i0);
-      for (int j = 0; j < cnt; ++j) {
-        const int i = i0 + j, n = i / KG, st = (i % KG) * NST + n % NST;
-        const int row = __shfl_sync(0xffffffffu, y, j);
-        if (n >= NST) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (n / NST - 1) & 1));
-          if (!ok) break;
-        }
-        if (lane == 0) {
-          okp[st] = row >= 0;
-          if (row >= 0) {
-            uint8_t* dst = sm + st * 2 * TILE;
-            mbar_expect_tx(&full[st], 2 * TILE);
-#pragma unroll
-            for (int c = 0; c < NB64; ++c) tma_load_2d(dst + c * 2048, tk, c * 64, row, &full[st]);
-#pragma unroll
-            for (int c = 0; c < NB64; ++c) tma_load_2d(dst + TILE + c * 2048, tv, c * 64, row, &full[st]);
-          } else {
-            mbar_arrive(&full[st]);
-          }
-        }
-        __syncwarp();
-        issued = i + 1;
-      }
-    }
-    if (!ok && lane == 0) {                    // report, and let the copies in flight land
-      flag(a.status, HYB_DEVERR_TIMEOUT);
-      for (int i = max(0, issued - KG * NST); i < issued; ++i)
-        mbar_wait(&full[(i % KG) * NST + (i / KG) % NST], (i / KG / NST) & 1, 100000000ull);
-    }
-  }
-
-  // -------------------------------------------------------------------- computing
+  // warp t = 0 of a key group fills its ring: stage n + NST - LAG once all have done with stage n - LAG
   const int t = warp % NT, kg = warp / NT;     // row tile, key group
+  const int ns = (np + KP - 1) / KP, mine = ns > kg ? (ns - kg + KG - 1) / KG : 0;   // stages, this ring's
+  uint8_t* ring = sm + kg * NST * KP * 2 * TILE;
+  full += kg * NST;
+  empty += kg * NST;
+  have_s += kg * NST;
   const int r0 = t * 16 + (lane >> 2), r1 = r0 + 8, quad = lane & 3;
-  float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  if (warp < kWarps) {
-    uint32_t qa[D / 16][4];
-    const __nv_bfloat16 *q0 = nullptr, *q1 = nullptr;
-    if (r0 < u.rows) {
-      const int i = u.row0 + r0;
-      q0 = q + ((int64_t)(u.first + i / rep) * a.Hq + u.hk * rep + i % rep) * D;
+  const __nv_bfloat16 *q0 = nullptr, *q1 = nullptr;
+  if (r0 < u.rows) {
+    const int i = u.row0 + r0;
+    q0 = q + ((int64_t)(u.first + i / rep) * a.Hq + u.hk * rep + i % rep) * D;
+  }
+  if (r1 < u.rows) {
+    const int i = u.row0 + r1;
+    q1 = q + ((int64_t)(u.first + i / rep) * a.Hq + u.hk * rep + i % rep) * D;
+  }
+  // The rows' lengths, the queries and (in issue) the block ids: one round trip, so all are asked for first.
+  const int len0 = q0 ? a.lens[u.first + (u.row0 + r0) / rep] : 0, len1 = q1 ? a.lens[u.first + (u.row0 + r1) / rep] : 0;
+  WarpTile<D> w;
+  w.start(q0, q1, a.q_sign);
+  Fetch<D, NST, KP> f{u.table, ring, full, u.hk, kb / kBlockSize, np, kg, KG, mine, -1, 0};
+  if (t == 0)
+    while (f.next < NST && f.next < mine) f.issue(a, tk, tv, have_s);
+  // keys that the lane's rows see, and those that all of the warp's rows do
+  if (q0) {
+    const RowSpan x = row_span(a, len0, 0, P);
+    w.lo0 = x.lo;
+    w.hi0 = min(P, x.n);
+  }
+  if (q1) {
+    const RowSpan x = row_span(a, len1, 0, P);
+    w.lo1 = x.lo;
+    w.hi1 = min(P, x.n);
+  }
+  const int min_hi = __reduce_min_sync(0xffffffffu, min(q0 ? w.hi0 : INT32_MAX, q1 ? w.hi1 : INT32_MAX));
+  const int max_lo = __reduce_max_sync(0xffffffffu, max(w.lo0, w.lo1));
+  for (int n = 0; n < mine; ++n) {
+    const int st = n % NST;
+    bool ok = __all_sync(0xffffffffu, mbar_wait_cycles(&full[st], (n / NST) & 1));
+    const unsigned have = ok ? have_s[st] : 0;
+    if (have && t * 16 < u.rows)
+      w.template step<KP>(kb + (kg + n * KG) * KP * kBlockSize, ring + st * KP * 2 * TILE, have, k0, k1, min_hi, max_lo,
+                          a.scale_log2);
+    __syncwarp();
+    if (NT > 1 && lane == 0) mbar_arrive(&empty[st]);
+    if (ok && t == 0 && n >= S::LAG && f.next < mine) {
+      const int m = n - S::LAG;                // f.next = m + NST
+      if (NT > 1) ok = __all_sync(0xffffffffu, mbar_wait_cycles(&empty[m % NST], (m / NST) & 1));
+      if (ok) f.issue(a, tk, tv, have_s);
     }
-    if (r1 < u.rows) {
-      const int i = u.row0 + r1;
-      q1 = q + ((int64_t)(u.first + i / rep) * a.Hq + u.hk * rep + i % rep) * D;
-    }
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const int c = k * 16 + quad * 2;
-      qa[k][0] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + c) : 0u;
-      qa[k][1] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + c) : 0u;
-      qa[k][2] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + c + 8) : 0u;
-      qa[k][3] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + c + 8) : 0u;
-    }
-    const int lo0 = row_lo[r0], hi0 = row_hi[r0], lo1 = row_lo[r1], hi1 = row_hi[r1];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-    // a lane's row and 16-byte chunk in the four 8 x 8 matrices of a load
-    const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
-    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
-
-    for (int n = 0; kg + n * KG < np; ++n) {
-      const int st = kg * NST + n % NST;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (n / NST) & 1));
-      if (!ok) {
-        if (lane == 0) flag(a.status, HYB_DEVERR_TIMEOUT);
-        break;
+    if (!ok) {                                 // report, and let the copies in flight land
+      if (lane == 0) {
+        flag(a.status, HYB_DEVERR_TIMEOUT);
+        if (t == 0)
+          for (int j = max(0, f.next - NST); j < f.next; ++j) mbar_wait_cycles(&full[j % NST], (j / NST) & 1, 200000000u);
       }
-      if (okp[st]) {
-        const int tok = kb + (kg + n * KG) * kBlockSize;
-        uint8_t* kt = sm + st * 2 * TILE;
-        const uint32_t ks = smem_u32(kt), vs = ks + TILE;
-        float s[2][2][4];                      // [half of the head][8 keys][.]: two chains each
-#pragma unroll
-        for (int i = 0; i < 16; ++i) (&s[0][0][0])[i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          const int ch = k * 2 + kch;
-          ldsm4(ks + (ch >> 3) * 2048 + sw128_off(krow, ch & 7), b);
-          mma16816(s[k & 1][0], qa[k], b[0], b[1]);
-          mma16816(s[k & 1][1], qa[k], b[2], b[3]);
-        }
-        float x[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[i][c] = (s[0][i][c] + s[1][i][c]) * a.scale_log2;
-        if (tok < max_lo || tok + kBlockSize > min_hi || tok < k0 || tok + kBlockSize > k1) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int key = tok + i * 8 + quad * 2 + (c & 1);
-              const bool see = key >= k0 && key < k1 && (c < 2 ? key >= lo0 && key < hi0 : key >= lo1 && key < hi1);
-              if (!see) x[i][c] = -INFINITY;
-            }
-          if (tok < k0 || tok + kBlockSize > k1) {
-            // rows that hold no key of the part may hold NaN, and 0 x NaN is NaN (every warp that
-            // reads the piece writes the same zeros first)
-            for (int e = lane; e < kBlockSize * D / 8; e += 32) {
-              const int r = e / (D / 8), ch = e % (D / 8);
-              if (tok + r < k0 || tok + r >= k1)
-                *reinterpret_cast<uint4*>(kt + TILE + (ch >> 3) * 2048 + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();                // the ring's next copy comes after these writes
-            __syncwarp();
-          }
-        }
-        float mx0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-        float mx1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
-#pragma unroll
-        for (int d = 1; d <= 2; d <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-        }
-        // the base moves only where a row's maximum outgrows it: p stays below 2^8
-        const bool g0 = mx0 > m[0] + kRescale || (m[0] == -INFINITY && mx0 != -INFINITY);
-        const bool g1 = mx1 > m[1] + kRescale || (m[1] == -INFINITY && mx1 != -INFINITY);
-        if (__any_sync(0xffffffffu, g0 || g1)) {
-          const float a0 = g0 ? (m[0] == -INFINITY ? 0.f : fast_exp2(m[0] - mx0)) : 1.f;
-          const float a1 = g1 ? (m[1] == -INFINITY ? 0.f : fast_exp2(m[1] - mx1)) : 1.f;
-          if (g0) m[0] = mx0;
-          if (g1) m[1] = mx1;
-          l[0] *= a0;
-          l[1] *= a1;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= a0;
-            o[i][1] *= a0;
-            o[i][2] *= a1;
-            o[i][3] *= a1;
-          }
-        }
-        const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
-        float p[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) p[i][c] = fast_exp2(x[i][c] - (c < 2 ? b0 : b1));
-        l[0] += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
-        l[1] += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
-        // P as bf16: half a step of a weight, 2^-9 of it on average less, of bf16 outputs
-        const uint32_t pa[4] = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]),
-                                pack_bf16(p[1][0], p[1][1]), pack_bf16(p[1][2], p[1][3])};
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          const int ch = k * 2 + vch;
-          ldsm4_t(vs + (ch >> 3) * 2048 + sw128_off(vrow, ch & 7), b);
-          mma16816(o[2 * k], pa, b[0], b[1]);
-          mma16816(o[2 * k + 1], pa, b[2], b[3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-    }
-#pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
-      l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
+      break;
     }
   }
+  w.finish();
 
   // -------------------------------------------------------------------- the part's state
   const int parts = a.Sp + a.Ss;
@@ -295,44 +437,43 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
     return ((int64_t)(u.first + i / rep) * a.Hq + u.hk * rep + i % rep) * parts + u.part;
   };
   if (KG == 1) {
-    if (warp < kWarps)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = half ? r1 : r0;
-        if (r >= u.rows) continue;
-        const int64_t at = slot(r);
-        if (quad == 0) a.ws_ml[at] = make_float2(m[half], l[half]);
+    for (int half = 0; half < 2; ++half) {
+      const int r = half ? r1 : r0;
+      if (r >= u.rows) continue;
+      const int64_t at = slot(r);
+      if (quad == 0) a.ws_ml[at] = make_float2(w.m[half], w.l[half]);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<float2*>(a.ws_acc + at * D + i * 8 + quad * 2) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
-      }
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2*>(a.ws_acc + at * D + i * 8 + quad * 2) = make_float2(w.o[i][2 * half], w.o[i][2 * half + 1]);
+    }
     return;
   }
   __syncthreads();                             // all pieces are read: the rings hold the sums now
   float* red = reinterpret_cast<float*>(sm);
-  if (warp < kWarps) {
+  {
     const int base = (kg * NT + t) * 16 + (lane >> 2);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-      *reinterpret_cast<float2*>(red + base * S::PITCH + i * 8 + quad * 2) = make_float2(o[i][0], o[i][1]);
-      *reinterpret_cast<float2*>(red + (base + 8) * S::PITCH + i * 8 + quad * 2) = make_float2(o[i][2], o[i][3]);
+      *reinterpret_cast<float2*>(red + base * S::PITCH + i * 8 + quad * 2) = make_float2(w.o[i][0], w.o[i][1]);
+      *reinterpret_cast<float2*>(red + (base + 8) * S::PITCH + i * 8 + quad * 2) = make_float2(w.o[i][2], w.o[i][3]);
     }
     if (quad == 0) {
-      red_ml[base] = make_float2(m[0], l[0]);
-      red_ml[base + 8] = make_float2(m[1], l[1]);
+      red_ml[base] = make_float2(w.m[0], w.l[0]);
+      red_ml[base + 8] = make_float2(w.m[1], w.l[1]);
     }
   }
   __syncthreads();
-  if (warp < kWarps) {
+  {
     for (int r = warp; r < u.rows; r += kWarps) {
-      float M = -INFINITY, L = 0.f, w[KG];
+      float M = -INFINITY, L = 0.f, x[KG];
 #pragma unroll
       for (int k = 0; k < KG; ++k) M = fmaxf(M, red_ml[k * NT * 16 + r].x);
 #pragma unroll
       for (int k = 0; k < KG; ++k) {
         const float2 v = red_ml[k * NT * 16 + r];
-        w[k] = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
-        L += w[k] * v.y;
+        x[k] = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);
+        L += x[k] * v.y;
       }
       const int64_t at = slot(r);
       if (lane == 0) a.ws_ml[at] = make_float2(M, L);
@@ -341,8 +482,8 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
           const float2 v = *reinterpret_cast<const float2*>(red + (k * NT * 16 + r) * S::PITCH + e);
-          A.x = fmaf(w[k], v.x, A.x);
-          A.y = fmaf(w[k], v.y, A.y);
+          A.x = fmaf(x[k], v.x, A.x);
+          A.y = fmaf(x[k], v.y, A.y);
         }
         *reinterpret_cast<float2*>(a.ws_acc + at * D + e) = A;
       }
@@ -351,15 +492,19 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
 }
 
 // CTAs [0, pre_ctas): ((group Hk + key head) tiles + row tile) Sp + part of the prefixes; the others:
-// ((request Hk + key head) tiles + row tile) Ss + part of the requests' own tokens.
+// request own_ctas + four of its (part, key head, row tile), one a warp.
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32 + 32)
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3)
 prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __nv_bfloat16* __restrict__ q, const PrefixArgs a, int pre_ctas, int pre_tiles,
-                  int own_tiles) {
+                  int own_ctas, int own_tiles) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
   pdl_wait();
   pdl_trigger();
   const int rep = a.Hq / a.Hk;
@@ -379,24 +524,26 @@ prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     u.k1 = min(P, u.k0 + a.Lp);
     u.table = a.bt + (int64_t)u.first * a.MB;
     if (u.rows <= 0 || u.k0 >= u.k1) return;
-    attend<D, NT>(&tk, &tv, q, a, u, P, true, sm);
+    attend<D, NT>(&tk, &tv, q, a, u, P, sm);
   } else {
+    // every warp takes one of the request's (part, key head, row tile)
     i -= pre_ctas;
-    u.part = i % a.Ss;
-    i /= a.Ss;
+    u.first = i / own_ctas;
+    const RowSpan r = find_row(a, u.first);
+    if (r.n < 0) return;
+    i = (i % own_ctas) * kWarps + (threadIdx.x >> 5);
     const int tile = i % own_tiles;
     i /= own_tiles;
     u.hk = i % a.Hk;
-    u.first = i / a.Hk;
-    const RowSpan r = find_row(a, u.first);
-    if (r.n < 0 || u.part >= r.own_parts(a.Ls)) return;
+    u.part = i / a.Hk;
+    if (u.part >= r.own_parts(a.Ls)) return;
     u.row0 = tile * 16;
     u.rows = min(16, rep - u.row0);
     u.k0 = r.own_base() + u.part * a.Ls;
     u.k1 = min(r.n, u.k0 + a.Ls);
     u.part += a.Sp;
     u.table = a.bt + (int64_t)u.first * a.MB;
-    attend<D, 1>(&tk, &tv, q, a, u, r.P, false, sm);
+    attend_own<D>(&tk, &tv, q, a, u, r.own_lo(), sm);
   }
 }
 
@@ -406,14 +553,14 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const __n
   const int rep = a.Hq / a.Hk;
   const int64_t pre_tiles = ((int64_t)a.max_group * rep + 16 * NT - 1) / (16 * NT), own_tiles = (rep + 15) / 16;
   const int64_t pre = prefix ? (int64_t)a.G * a.Hk * pre_tiles * a.Sp : 0;
-  const int64_t own = (int64_t)a.B * a.Hk * own_tiles * a.Ss;
+  const int64_t own_ctas = ((int64_t)a.Ss * a.Hk * own_tiles + kWarps - 1) / kWarps, own = a.B * own_ctas;
   if (pre + own == 0) return cudaSuccess;
   if (pre + own > INT32_MAX) return cudaErrorInvalidConfiguration;   // its workspace would be above 1 TB
-  constexpr int smem = MmaShape<D, NT>::SMEM > MmaShape<D, 1>::SMEM ? MmaShape<D, NT>::SMEM : MmaShape<D, 1>::SMEM;
+  constexpr int smem = MmaShape<D, NT>::SMEM > OwnShape<D>::SMEM ? MmaShape<D, NT>::SMEM : OwnShape<D>::SMEM;
   cudaError_t e = set_smem((const void*)prefix_mma_kernel<D, NT>, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(prefix_mma_kernel<D, NT>, dim3((unsigned)(pre + own)), dim3(kWarps * 32 + 32), smem, s, tk, tv, q, a,
-                 (int)pre, (int)pre_tiles, (int)own_tiles);
+  e = launch_pdl(prefix_mma_kernel<D, NT>, dim3((unsigned)(pre + own)), dim3(kWarps * 32), smem, s, tk, tv, q, a,
+                 (int)pre, (int)pre_tiles, (int)own_ctas, (int)own_tiles);
   count_launch();
   return e;
 }
@@ -433,7 +580,7 @@ cudaError_t launch_prefix_mma(int D, const void* q, const void* kc, const void* 
   if (!encode_tmap_bf16(&tk, kc, 2, dims, str, box) || !encode_tmap_bf16(&tv, vc, 2, dims, str, box))
     return cudaErrorInvalidValue;
   const int64_t rows = (int64_t)a.max_group * (a.Hq / a.Hk);
-  const int nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const int nt = !prefix || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 #define HYB_MMA(DD, N) \
   if (D == DD && nt == N) return launch_typed<DD, N>(tk, tv, (const __nv_bfloat16*)q, a, prefix, s);
   HYB_MMA(64, 1)
