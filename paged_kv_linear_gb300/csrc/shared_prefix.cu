@@ -121,13 +121,13 @@ prefix_part_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
   }
 }
 
-constexpr int kJoinWarps = 4, kBatch = 8;   // parts whose loads are in flight together
+constexpr int kJoinWarps = 4;
 
 // Joins the parts of a (row, query head), one a warp, D / 32 columns a lane. What says which parts a row has was there before the
 // parts' kernel began, so it is read before that kernel ends. The first CTA also reports bad groups.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(T* __restrict__ out, const PrefixArgs a) {
-  constexpr int E = D / 32 > 0 ? D / 32 : 1;
+  constexpr int E = D / 32 > 0 ? D / 32 : 1, kBatch = E <= 4 ? 12 : 6;   // parts whose loads are in flight together
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x, h = blockIdx.y * kJoinWarps + warp;
   pdl_trigger();
@@ -202,14 +202,16 @@ PrefixPlan plan_prefix(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t*
   const bool mma = prefix_mma_supported(d->dtype, D);
   r.tc = mma && D == 128 && rep <= 128 && d->scale > 0.f && rows > 64;
   if (r.tc) {
-    // one CTA an SM; a key tile of 128 takes it some 1.46 us, setup and drain 6 us
+    // one CTA an SM; a key tile of 128 takes it some 1.6 us, setup and drain 8 us; a part's state
+    // is written and read once, at some 6 TB/s
     const int64_t tr = 2 * prefix_tc_tile_rows(rep), units = std::max<int64_t>(1, heads * ((rows + tr - 1) / tr));
     const int tiles = std::max(1, (P + 127) / 128);
+    const double state_us = (double)B * p->num_q_heads * (D * 4 + 8) * 2 / 6e6;
     double best = 1e30;
     r.Lp = 128;
     for (int n = 1; n <= std::min(tiles, 64); ++n) {
       const int64_t per = (tiles + n - 1) / n, used = (tiles + per - 1) / per, waves = (units * used + sms - 1) / sms;
-      const double t = waves * (1.46 * per + 6.0);
+      const double t = waves * (1.6 * per + 8.0) + used * state_us;
       if (t < best) {
         best = t;
         r.Lp = (int)per * 128;
@@ -236,8 +238,9 @@ cudaError_t launch_typed(void* out, const void* q, const void* kc, const void* v
                          bool tc, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if constexpr (sizeof(T) == 2 && (D == 64 || D == 128 || D == 256)) {
-    e = launch_prefix_mma(D, q, kc, vc, a, !tc, s);
-    if (e == cudaSuccess && tc) e = launch_prefix_tc(q, kc, vc, a, s);
+    const bool behind = tc && a.Sp > 0;
+    if (behind) e = launch_prefix_tc(q, kc, vc, a, s);
+    if (e == cudaSuccess) e = launch_prefix_mma(D, q, kc, vc, a, !tc, behind, s);
     if (e != cudaSuccess) return e;
   } else if (a.Sp + a.Ss > 0) {
     e = launch_pdl(prefix_part_kernel<T, D>, dim3(a.Sp + a.Ss, a.B, a.Hq), dim3(128), 0, s, (const T*)q,

@@ -29,9 +29,10 @@ struct PrefixArgs {
 };
 
 bool prefix_mma_supported(int dtype, int D);
-// prefix: the prefixes' parts too, not only those of the rows' own tokens
+// prefix: the prefixes' parts too, not only those of the rows' own tokens; early: behind launch_prefix_tc of
+// the same call
 cudaError_t launch_prefix_mma(int D, const void* q, const void* kc, const void* vc, const PrefixArgs& a,
-                              bool prefix, cudaStream_t s);
+                              bool prefix, bool early, cudaStream_t s);
 
 // the prefixes' parts on the tensor cores (bf16, D = 128, scale > 0, at most 128 query heads a key head)
 int prefix_tc_tile_rows(int rep);          // rows of one of its row tiles; a CTA takes two

@@ -497,7 +497,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3)
 prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __nv_bfloat16* __restrict__ q, const PrefixArgs a, int pre_ctas, int pre_tiles,
-                  int own_ctas, int own_tiles) {
+                  int own_ctas, int own_tiles, int early) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -505,7 +505,10 @@ prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  pdl_wait();
+  // early: launched behind the tensor-core kernel of the same call, which began when everything before it had
+  // ended and writes nothing that this one reads or writes. So this one runs beside it, and waits for it
+  // only at its end (the joining kernel waits for this one alone).
+  if (!early) pdl_wait();
   pdl_trigger();
   const int rep = a.Hq / a.Hk;
   Unit u;
@@ -530,26 +533,27 @@ prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     i -= pre_ctas;
     u.first = i / own_ctas;
     const RowSpan r = find_row(a, u.first);
-    if (r.n < 0) return;
     i = (i % own_ctas) * kWarps + (threadIdx.x >> 5);
     const int tile = i % own_tiles;
     i /= own_tiles;
     u.hk = i % a.Hk;
     u.part = i / a.Hk;
-    if (u.part >= r.own_parts(a.Ls)) return;
-    u.row0 = tile * 16;
-    u.rows = min(16, rep - u.row0);
-    u.k0 = r.own_base() + u.part * a.Ls;
-    u.k1 = min(r.n, u.k0 + a.Ls);
-    u.part += a.Sp;
-    u.table = a.bt + (int64_t)u.first * a.MB;
-    attend_own<D>(&tk, &tv, q, a, u, r.own_lo(), sm);
+    if (r.n >= 0 && u.part < r.own_parts(a.Ls)) {
+      u.row0 = tile * 16;
+      u.rows = min(16, rep - u.row0);
+      u.k0 = r.own_base() + u.part * a.Ls;
+      u.k1 = min(r.n, u.k0 + a.Ls);
+      u.part += a.Sp;
+      u.table = a.bt + (int64_t)u.first * a.MB;
+      attend_own<D>(&tk, &tv, q, a, u, r.own_lo(), sm);
+    }
+    if (early) pdl_wait();
   }
 }
 
 template <int D, int NT>
 cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const __nv_bfloat16* q, const PrefixArgs& a,
-                         bool prefix, cudaStream_t s) {
+                         bool prefix, bool early, cudaStream_t s) {
   const int rep = a.Hq / a.Hk;
   const int64_t pre_tiles = ((int64_t)a.max_group * rep + 16 * NT - 1) / (16 * NT), own_tiles = (rep + 15) / 16;
   const int64_t pre = prefix ? (int64_t)a.G * a.Hk * pre_tiles * a.Sp : 0;
@@ -560,7 +564,7 @@ cudaError_t launch_typed(const CUtensorMap& tk, const CUtensorMap& tv, const __n
   cudaError_t e = set_smem((const void*)prefix_mma_kernel<D, NT>, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(prefix_mma_kernel<D, NT>, dim3((unsigned)(pre + own)), dim3(kWarps * 32), smem, s, tk, tv, q, a,
-                 (int)pre, (int)pre_tiles, (int)own_ctas, (int)own_tiles);
+                 (int)pre, (int)pre_tiles, (int)own_ctas, (int)own_tiles, early ? 1 : 0);
   count_launch();
   return e;
 }
@@ -572,7 +576,7 @@ bool prefix_mma_supported(int dtype, int D) {
 }
 
 cudaError_t launch_prefix_mma(int D, const void* q, const void* kc, const void* vc, const PrefixArgs& a, bool prefix,
-                              cudaStream_t s) {
+                              bool early, cudaStream_t s) {
   CUtensorMap tk, tv;
   const uint64_t dims[2] = {(uint64_t)D, (uint64_t)a.NB * a.Hk * (kBlockSize << a.rsh)};
   const uint64_t str[1] = {(uint64_t)D * 2};
@@ -582,7 +586,7 @@ cudaError_t launch_prefix_mma(int D, const void* q, const void* kc, const void* 
   const int64_t rows = (int64_t)a.max_group * (a.Hq / a.Hk);
   const int nt = !prefix || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 #define HYB_MMA(DD, N) \
-  if (D == DD && nt == N) return launch_typed<DD, N>(tk, tv, (const __nv_bfloat16*)q, a, prefix, s);
+  if (D == DD && nt == N) return launch_typed<DD, N>(tk, tv, (const __nv_bfloat16*)q, a, prefix, early, s);
   HYB_MMA(64, 1)
   HYB_MMA(64, 2)
   HYB_MMA(64, 4)

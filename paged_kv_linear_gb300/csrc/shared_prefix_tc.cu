@@ -44,6 +44,14 @@ struct Bars {
   uint64_t sfull[2], pfull[2], odone[2], drain;    // per row tile
 };
 
+// asks L2 for a box of a tensor map
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -81,6 +89,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   const int cnt = (b1 - b0) * rep, row0 = duo * 2 * tile_rows;   // rows of the group; the pair's first
   int k0 = part * a.Lp, k1 = min(P, k0 + a.Lp);
   if (row0 >= cnt || k0 >= k1) return;
+  const int duos = (cnt + 2 * tile_rows - 1) / (2 * tile_rows);   // CTAs that read the same keys
   const bool two = row0 + tile_rows < cnt;             // second row tile present
   if (a.window > 0) {                                  // only keys that one of the rows sees
     int max_hi = 0, min_lo = INT32_MAX;
@@ -109,6 +118,19 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
                                            ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(sm + kOffBar);
   __shared__ uint32_t tmem_base;
+  // what the softmax threads need rarely waits here: their registers are all spoken for
+  __shared__ struct {
+    const int32_t* btrow;
+    int b0, row0, cnt, part, head0;                  // head0: the first query head of hk
+  } info;
+  if (tid == 0) {
+    info.btrow = btrow;
+    info.b0 = b0;
+    info.row0 = row0;
+    info.cnt = cnt;
+    info.part = part;
+    info.head0 = hk * rep;
+  }
 
   if (warp == kWarpMma) {
     if (lane == 0) {
@@ -152,13 +174,23 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           tma_load_3d(q_s + t * kTile + kSubQ, &tq, 64, hk * rep, b0 + (duo * 2 + t) * per, &bars->qfull);
         }
       }
-      int ids = -1;                                      // pool rows of 4 tiles' pieces, one per lane
+      // pool rows of 4 tiles' pieces, one per lane, looked up 4 tiles ahead; L2 is asked for the pieces then, each
+      // by one of the CTAs that read the same keys: the rings are too short for memory's latency
+      auto rows_of = [&](int j) {
+        const int s = kb / kBlockSize + j * 8 + lane;
+        const int pb = block_of(s);
+        if (isk && pb < 0 && s * kBlockSize < k1) flag(a.status, HYB_DEVERR_BAD_BLOCK);
+        return pb < 0 ? -1 : ((pb * a.Hk + hk) << (4 + a.rsh)) + ((s & ((1 << a.rsh) - 1)) << 4);
+      };
+      int ids = -1, ahead = rows_of(0);
       for (int jj = 0; jj < nloc; ++jj) {
         if ((jj & 3) == 0) {
-          const int s = kb / kBlockSize + jj * 8 + lane;
-          const int pb = block_of(s);
-          ids = pb < 0 ? -1 : ((pb * a.Hk + hk) << (4 + a.rsh)) + ((s & ((1 << a.rsh) - 1)) << 4);
-          if (isk && pb < 0 && s * kBlockSize < k1) flag(a.status, HYB_DEVERR_BAD_BLOCK);
+          ids = ahead;
+          ahead = rows_of(jj + 4);
+          if (ahead >= 0 && lane % duos == duo % 32) {
+            tma_prefetch_2d(map, 0, ahead);
+            tma_prefetch_2d(map, 64, ahead);
+          }
         }
         int blk[8];
         int nbox = 0;
@@ -290,99 +322,109 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     const int r = quarter * 32 + lane;                 // row of the tile = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_col = tl + t * 128, o_col = tl + kColO + t * 128;
-    const int f = row0 + t * tile_rows + r;            // row of the group
-    const bool there = (t == 0 || two) && r < tile_rows && f < cnt;
-    const int b = b0 + f / rep, h = hk * rep + f % rep;
-    int lo = 0, hi = 0;                                // keys that the row sees
-    if (there) {
-      const RowSpan x = row_span(a, a.lens[b], 0, P);
-      lo = x.lo;
-      hi = min(P, x.n);
+    // keys that the row sees, of the part's; a row that is not there: none, and it does not count below
+    int lo = 0, hi = 0, max_lo = 0, min_hi = INT32_MAX;
+    {
+      const int f = row0 + t * tile_rows + r;          // row of the group
+      if ((t == 0 || two) && r < tile_rows && f < cnt) {
+        const RowSpan x = row_span(a, a.lens[b0 + f / rep], 0, P);
+        lo = max_lo = max(x.lo, k0);
+        hi = min_hi = min(min(P, x.n), k1);
+      }
     }
-    const int max_lo = __reduce_max_sync(0xffffffffu, lo), min_hi = __reduce_min_sync(0xffffffffu, there ? hi : INT32_MAX);
-    const bool any = __any_sync(0xffffffffu, there);   // a warp without rows only keeps the pace
+    const bool any = __any_sync(0xffffffffu, min_hi != INT32_MAX);   // a warp without rows only keeps the pace
+    bool good = true;                                  // no bad block in the part
+    for (int s = kb / kBlockSize + lane; s * kBlockSize < k1; s += 32) good = good && block_of(s) >= 0;
+    if (!good) min_hi = 0;                             // one: every tile takes the masking path
+    max_lo = __reduce_max_sync(0xffffffffu, max_lo);
+    min_hi = __reduce_min_sync(0xffffffffu, min_hi);
     const float scale_log2 = a.scale_log2;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     const int steps = (t == 0 || two) ? nloc : 0;
-    int pb = lane < 8 ? block_of(kb / kBlockSize + lane) : -1;
-    for (int it = 0; it < steps && ok; ++it) {
-      const unsigned have = __ballot_sync(0xffffffffu, pb >= 0);
-      if (lane < 8 && it + 1 < steps) pb = block_of(kb / kBlockSize + (it + 1) * 8 + lane);
+    for (int it = 0; !any && it < steps && ok; ++it) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[t], it & 1));
+      tc_fence_before();
+      if (ok) mbar_arrive(&bars->pfull[t]);
+    }
+    for (int it = 0; any && it < steps && ok; ++it) {
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[t], it & 1));
       if (!ok) break;
       tc_fence_after();
-      if (any) {
-        float x[128];
+      float x[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, x + c * 32);
-        tmem_ld_wait();
-        const int kbase = kb + it * kBN;
-        if (kbase < max_lo || kbase + kBN > min_hi || kbase < k0 || have != 0xffu) {
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_col + c * 32, x + c * 32);
+      tmem_ld_wait();
+      const int kbase = kb + it * kBN;
+      if (kbase < max_lo || kbase + kBN > min_hi) {
+        int pb = -1;                                 // pieces that are there
+        if (lane < 8 && kbase + lane * kBlockSize < a.max_prefix) pb = info.btrow[(kbase / kBlockSize + lane) >> a.rsh];
+        const unsigned have = __ballot_sync(0xffffffffu, pb >= 0 && pb < a.NB);
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const int kp = kbase + c;
-            x[c] = (kp >= lo && kp < hi && kp >= k0 && kp < k1 && ((have >> (c / 16)) & 1)) ? x[c] : -INFINITY;
-          }
+        for (int c = 0; c < 128; ++c) {
+          const int kp = kbase + c;
+          x[c] = (kp >= lo && kp < hi && ((have >> (c / 16)) & 1)) ? x[c] : -INFINITY;
         }
-        // row max of the raw scores (scale > 0 keeps the order)
-        float mp[8];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) mp[n] = x[n];
-#pragma unroll
-        for (int c = 8; c + 16 <= 128; c += 16)
-#pragma unroll
-          for (int n = 0; n < 8; ++n) mp[n] = max3f(mp[n], x[c + n], x[c + 8 + n]);
-#pragma unroll
-        for (int n = 0; n < 8; ++n) mp[n] = fmaxf(mp[n], x[120 + n]);
-        const float mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]),
-                               fmaxf(mp[6], mp[7])) * scale_log2;
-        const float m_new = fmaxf(m_used, mx);
-        const bool grow = m_new > m_used + kRescaleLog2 || (m_used == -INFINITY && m_new != -INFINITY);
-        const float m_tgt = grow ? m_new : m_used;
-        const float m_sub = m_tgt == -INFINITY ? 0.f : m_tgt;   // no key seen yet: P = 0
-        uint32_t w[64];
-        f32x2 sp[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) sp[n] = pair(0.f, 0.f);
-        const f32x2 sc2 = pair(scale_log2, scale_log2), nm2 = pair(-m_sub, -m_sub);
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          float y0, y1;
-          unpair(fma2(pair(x[2 * c], x[2 * c + 1]), sc2, nm2), y0, y1);
-          const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-          sp[c & 3] = add2(sp[c & 3], pair(p0, p1));
-          w[c] = pack_bf16(p0, p1);                    // P as bf16: half a step of each weight
-        }
-        float s0, s1;
-        unpair(add2(add2(sp[0], sp[1]), add2(sp[2], sp[3])), s0, s1);
-        const float ls = s0 + s1;
-        if (it >= 1 && __any_sync(0xffffffffu, grow)) {
-          const float alpha = (grow && m_used != -INFINITY) ? fast_exp2(m_used - m_new) : 1.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {                // warp-wide TMEM access, per-row factor
-            float o[32];
-            tmem_ld32(o_col + c * 32, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            tmem_st32(o_col + c * 32, o);
-          }
-          if (grow) l *= alpha;
-        }
-        m_used = m_tgt;
-        l += ls;
-        tmem_st32u(s_col, w);                          // P_t: keys 0..127 as bf16 pairs
-        tmem_st32u(s_col + 32, w + 32);
-        tmem_st_wait();
       }
+      // row max of the raw scores (scale > 0 keeps the order)
+      float mp[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) mp[n] = x[n];
+#pragma unroll
+      for (int c = 8; c + 16 <= 128; c += 16)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) mp[n] = max3f(mp[n], x[c + n], x[c + 8 + n]);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) mp[n] = fmaxf(mp[n], x[120 + n]);
+      const float mx = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]),
+                             fmaxf(mp[6], mp[7])) * scale_log2;
+      const float m_new = fmaxf(m_used, mx);
+      const bool grow = m_new > m_used + kRescaleLog2 || (m_used == -INFINITY && m_new != -INFINITY);
+      const float m_tgt = grow ? m_new : m_used;
+      const float m_sub = m_tgt == -INFINITY ? 0.f : m_tgt;   // no key seen yet: P = 0
+      uint32_t w[64];
+      f32x2 sp[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) sp[n] = pair(0.f, 0.f);
+      const f32x2 sc2 = pair(scale_log2, scale_log2), nm2 = pair(-m_sub, -m_sub);
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        float y0, y1;
+        unpair(fma2(pair(x[2 * c], x[2 * c + 1]), sc2, nm2), y0, y1);
+        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+        sp[c & 3] = add2(sp[c & 3], pair(p0, p1));
+        w[c] = pack_bf16(p0, p1);                    // P as bf16: half a step of each weight
+      }
+      float s0, s1;
+      unpair(add2(add2(sp[0], sp[1]), add2(sp[2], sp[3])), s0, s1);
+      const float ls = s0 + s1;
+      if (it >= 1 && __any_sync(0xffffffffu, grow)) {
+        const float alpha = (grow && m_used != -INFINITY) ? fast_exp2(m_used - m_new) : 1.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {                // warp-wide TMEM access, per-row factor
+          float o[32];
+          tmem_ld32(o_col + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= alpha;
+          tmem_st32(o_col + c * 32, o);
+        }
+        if (grow) l *= alpha;
+      }
+      m_used = m_tgt;
+      l += ls;
+      tmem_st32u(s_col, w);                          // P_t: keys 0..127 as bf16 pairs
+      tmem_st32u(s_col + 32, w + 32);
+      tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->pfull[t]);
     }
     if (ok && steps) ok = __all_sync(0xffffffffu, mbar_wait(&bars->odone[t], 0));
     if (ok && steps && any) {
       tc_fence_after();
-      const int64_t at = ((int64_t)b * a.Hq + h) * (a.Sp + a.Ss) + part;
+      const int f = info.row0 + t * tile_rows + r, of = a.Hq / a.Hk;
+      const bool there = r < tile_rows && f < info.cnt;
+      const int64_t at = ((int64_t)(info.b0 + f / of) * a.Hq + info.head0 + f % of) * (a.Sp + a.Ss) + info.part;
       if (there) a.ws_ml[at] = make_float2(m_used, l);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
