@@ -584,9 +584,9 @@ hyb_status_t hyb_layer_dispatch(const int32_t* layer_types, int32_t L, int32_t m
  *   d           num_heads (key heads), head_dim, block_size, num_blocks, max_blocks_per_seq and
  *               dtype of the caches; the rest has to be valid as in the other calls
  * Bad block ids set HYB_DEVERR_BAD_BLOCK, bad slots HYB_DEVERR_BAD_STATE, and what they name is
- * not copied. `workspace`: device memory, 4-byte aligned, hyb_beam_reorder_workspace_size()
- * bytes, no initialisation, nothing kept between calls. R = 0 or L = 0 moves no data (L = 0: tables
- * and slots move all the same). Limits: W <= 128, R x W <= 65535, L <= 65535.
+ * not copied. `workspace`: hyb_beam_reorder_workspace_size() bytes, which is 0 (the call keeps what it needs on
+ * chip; NULL is fine). R = 0 is a no-op; with L = 0 tables, lengths and slots move all the same.
+ * Limits: W <= 128, R x W <= 65535, L <= 65535.
  * ------------------------------------------------------------------------- */
 size_t hyb_beam_reorder_workspace_size(int32_t R, int32_t W);
 hyb_status_t hyb_beam_reorder(const int32_t* parents, int32_t* block_tables, int32_t* seq_lens,

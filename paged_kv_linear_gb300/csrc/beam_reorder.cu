@@ -1,5 +1,10 @@
 // Reordering of beams (hyb_beam_reorder): tables, lengths and state slots move by permutation,
 // cached tokens and states are copied only for a beam's second and later children.
+//
+// Two kernels, the copies first: they go by the old tables and slots, and each CTA works out for itself from
+// its request's W parents what its row gets from where (a load and some votes). The permutation follows in
+// place; it reads and sorts while the copies run, and writes once they have ended. Nothing is bound by anything but the
+// bytes that are copied, each read once and written once.
 #include <set>
 
 #include "hyb_internal.cuh"
@@ -10,79 +15,85 @@ namespace {
 constexpr int kMaxBeams = 128, kMaxLayers = 96;
 constexpr int kCols = 32;                // table columns of a CTA
 
-// Rows of request r's next beams, by all threads: seat[i] (the old row, 0 .. W - 1, whose table
-// and slot beam i gets) and from[i] (the beam whose row holds the data to copy there, -1: none).
-__device__ __forceinline__ void seats(const int32_t* __restrict__ parents, int W, int* par, int* seat, int* from,
+// What the request's next beam i gets: the row of old beam `seat`, and a copy of old beam `from`'s data there
+// (-1: none, the row's own data go on or there is no parent).
+struct Move {
+  int seat, from;
+};
+
+// Whole CTA (a multiple of 32 threads, W <= kMaxBeams): beam i's move, the same in all threads, or with i < 0
+// that of beam threadIdx.x (of those below W). Bits over the beams: `first`, the first children of their
+// parents; `child`, the beams that have some. The k-th beam that is not a first child gets the k-th
+// beam's row that has none.
+__device__ __forceinline__ Move moves(const int32_t* __restrict__ parents, int W, int i, int* par, unsigned* bits,
                                       unsigned* status) {
   const int tid = threadIdx.x;
-  for (int i = tid; i < W; i += blockDim.x) {
-    int p = parents[i];
+  unsigned *rest = bits, *child = bits + kMaxBeams / 32;
+  if (tid < 2 * kMaxBeams / 32) bits[tid] = 0;
+  for (int j = tid; j < W; j += blockDim.x) {
+    int p = parents[j];
     if (p < -1 || p >= W) {
       flag(status, HYB_DEVERR_BAD_VALUE);
       p = -1;
     }
-    par[i] = p;
+    par[j] = p;
   }
   __syncthreads();
-  for (int i = tid; i < W; i += blockDim.x) {
-    // first child of its parent? and how many before it are not
-    int heir = -1, later = 0;
-    const int p = par[i];
-    for (int j = 0; j < i; ++j) {
-      if (par[j] == p && heir < 0) heir = j;
-      bool first = par[j] >= 0;
-      for (int k = 0; k < j && first; ++k) first = par[k] != par[j];
-      later += !first;
-    }
-    if (p >= 0 && heir < 0) {
-      seat[i] = p;
-      from[i] = -1;
-    } else {
-      int c = -1, left = later;          // the beam without children of that number
-      for (int w = 0; w < W && c < 0; ++w) {
-        bool child = false;
-        for (int k = 0; k < W && !child; ++k) child = par[k] == w;
-        if (!child && left-- == 0) c = w;
-      }
-      seat[i] = c;
-      from[i] = p >= 0 ? heir : -1;
-    }
+  for (int j = tid; j < W; j += blockDim.x) {
+    const int p = par[j];
+    bool first = p >= 0;
+    for (int k = 0; k < j && first; ++k) first = par[k] != p;
+    if (!first) atomicOr(&rest[j / 32], 1u << (j % 32));
+    if (p >= 0) atomicOr(&child[p / 32], 1u << (p % 32));
   }
   __syncthreads();
+  const int me = i < 0 ? min(tid, W - 1) : i;
+  Move mv{par[me], -1};
+  if ((rest[me / 32] >> (me % 32)) & 1) {
+    int k = __popc(rest[me / 32] & ((1u << (me % 32)) - 1));
+    for (int w = 0; w < me / 32; ++w) k += __popc(rest[w]);
+    int w = 0;                             // the k-th beam without children (there are as many as in `rest`)
+    unsigned none = ~child[0];
+    while (k >= __popc(none)) {
+      k -= __popc(none);
+      none = ~child[++w];
+    }
+    for (; k > 0; --k) none &= none - 1;
+    mv.from = mv.seat;
+    mv.seat = w * 32 + __ffs(none) - 1;
+  }
+  return mv;
 }
 
-// grid (table columns / 32, at least 1; R)
-__global__ void __launch_bounds__(128)
+// grid (table columns / 32, at least 1; R). early: behind this call's copies, which write nothing that is read here
+__global__ void __launch_bounds__(kMaxBeams)
 beam_seat_kernel(const int32_t* __restrict__ parents, int32_t* __restrict__ bt, int32_t* __restrict__ lens,
-                 const int32_t* __restrict__ pre, int32_t* __restrict__ slots, int32_t* __restrict__ copy, int W,
-                 int MB, int bs, unsigned* status) {
-  __shared__ int par[kMaxBeams], seat[kMaxBeams], from[kMaxBeams];
+                 const int32_t* __restrict__ pre, int32_t* __restrict__ slots, int W, int MB, int bs, int early,
+                 unsigned* status) {
+  __shared__ int par[kMaxBeams], seat[kMaxBeams];
+  __shared__ unsigned bits[2 * kMaxBeams / 32];
   __shared__ int32_t strip[kMaxBeams][kCols];
-  pdl_wait();
-  pdl_trigger();
+  if (!early) pdl_wait();
   const int r = blockIdx.y, tid = threadIdx.x, row0 = r * W;
-  seats(parents + row0, W, par, seat, from, blockIdx.x == 0 ? status : nullptr);
-  if (blockIdx.x == 0) {
-    int n = 0, sl = 0;
-    if (tid < W) {
-      if (lens) n = lens[row0 + (par[tid] >= 0 ? par[tid] : seat[tid])];
-      if (slots) sl = slots[row0 + seat[tid]];
-    }
-    __syncthreads();
-    if (tid < W) {
-      if (lens) lens[row0 + tid] = n;
-      if (slots) slots[row0 + tid] = sl;
-      copy[row0 + tid] = from[tid] < 0 ? -1 : row0 + from[tid];
-    }
+  const Move mv = moves(parents + row0, W, -1, par, bits, blockIdx.x == 0 ? status : nullptr);
+  seat[tid] = mv.seat;
+  int n = 0, sl = 0;
+  if (blockIdx.x == 0 && tid < W) {
+    if (lens) n = lens[row0 + (par[tid] >= 0 ? par[tid] : mv.seat)];
+    if (slots) sl = slots[row0 + mv.seat];
   }
-  if (!bt) return;
-  const int c0 = max((int)blockIdx.x * kCols, pre ? max(pre[r], 0) / bs : 0), c1 = min(MB, (int)(blockIdx.x + 1) * kCols);
-  if (c0 >= c1) return;
-  const int col = c0 + (tid & 31);
-  for (int w = tid >> 5; w < W; w += 4)
+  const int c0 = max((int)blockIdx.x * kCols, pre ? max(pre[r], 0) / bs : 0);
+  const int c1 = bt ? min(MB, (int)(blockIdx.x + 1) * kCols) : 0, col = c0 + (tid & 31);
+  for (int w = tid >> 5; w < W; w += kMaxBeams / 32)
     if (col < c1) strip[w][tid & 31] = bt[(int64_t)(row0 + w) * MB + col];
   __syncthreads();
-  for (int w = tid >> 5; w < W; w += 4)
+  if (early) pdl_wait();                   // the copies go by the old tables, lengths and slots
+  pdl_trigger();
+  if (blockIdx.x == 0 && tid < W) {
+    if (lens) lens[row0 + tid] = n;
+    if (slots) slots[row0 + tid] = sl;
+  }
+  for (int w = tid >> 5; w < W; w += kMaxBeams / 32)
     if (col < c1) bt[(int64_t)(row0 + w) * MB + col] = strip[seat[w]][tid & 31];
 }
 
@@ -94,50 +105,71 @@ struct Layers {
   Layer l[kMaxLayers];
 };
 
-// grid (pieces, rows, layers): row blockIdx.y's copy of its parent's state (pieces of 1024 vectors) or
-// tokens (a piece is 16 tokens of all heads)
-__global__ void __launch_bounds__(256)
-beam_copy_kernel(const __grid_constant__ Layers layers, const int32_t* __restrict__ copy,
+constexpr int kCopyThreads = 256, kU = 8;   // vectors of a thread in flight
+
+// grid (pieces, rows, layers): what row blockIdx.y's beam gets of its parent's state or tokens. A CTA takes every
+// gridDim.x-th piece: of the tokens 16 of all heads, of a state 32 KiB.
+__global__ void __launch_bounds__(kCopyThreads)
+beam_copy_kernel(const __grid_constant__ Layers layers, const int32_t* __restrict__ parents,
                  const int32_t* __restrict__ bt, const int32_t* __restrict__ lens, const int32_t* __restrict__ pre,
                  const int32_t* __restrict__ slots, int W, int64_t state_vecs, int max_suffix, int H, int vpr, int NB,
                  int MB, int bs, unsigned* status) {
+  __shared__ int par[kMaxBeams];
+  __shared__ unsigned bits[2 * kMaxBeams / 32];
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.y, src = copy[row];
-  if (src < 0) return;
+  const int r = blockIdx.y / W, tid = threadIdx.x;
+  const Move mv = moves(parents + (int64_t)r * W, W, blockIdx.y - r * W, par, bits, nullptr);
+  if (mv.from < 0) return;
+  const int src = r * W + mv.from, dst = r * W + mv.seat;
   const Layer ly = layers.l[blockIdx.z];
-  const int tid = threadIdx.x;
+  const bool says = blockIdx.x == 0 && tid == 0;
   if (!ly.b) {
-    const int s0 = slots[src], s1 = slots[row];
+    const int s0 = slots[src], s1 = slots[dst];
     if (s0 < 0 || s0 >= ly.slots || s1 < 0 || s1 >= ly.slots) {
-      if (blockIdx.x == 0 && tid == 0) flag(status, HYB_DEVERR_BAD_STATE);
+      if (says) flag(status, HYB_DEVERR_BAD_STATE);
       return;
     }
     const uint4* x = static_cast<const uint4*>(ly.a) + s0 * state_vecs;
     uint4* y = static_cast<uint4*>(ly.a) + s1 * state_vecs;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < state_vecs; i += (int64_t)gridDim.x * 256) y[i] = x[i];
+    constexpr int kPiece = kCopyThreads * kU;
+    for (int64_t i0 = (int64_t)blockIdx.x * kPiece + tid; i0 < state_vecs; i0 += (int64_t)gridDim.x * kPiece) {
+      uint4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (i0 + u * kCopyThreads < state_vecs) v[u] = __ldcs(x + i0 + u * kCopyThreads);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (i0 + u * kCopyThreads < state_vecs) __stcs(y + i0 + u * kCopyThreads, v[u]);
+    }
     return;
   }
-  const int P = pre ? max(pre[row / W], 0) : 0, n = lens[src];
+  const int P = pre ? max(pre[r], 0) : 0, n = lens[src];
   if (n - P > max_suffix || n > (int64_t)MB * bs) {
-    if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) flag(status, HYB_DEVERR_BAD_LENGTH);
+    if (says && blockIdx.z == 0) flag(status, HYB_DEVERR_BAD_LENGTH);
     return;
   }
   // the next token is number n: a window of W ending there starts at n + 1 - W
   const int lo = ly.window > 0 ? max(P, n + 1 - ly.window) : P;
+  const int64_t head = (int64_t)bs * vpr;
   for (int t = (lo & ~15) + blockIdx.x * 16; t < n; t += gridDim.x * 16) {
-    const int p0 = bt[(int64_t)src * MB + t / bs], p1 = bt[(int64_t)row * MB + t / bs];
+    const int p0 = bt[(int64_t)src * MB + t / bs], p1 = bt[(int64_t)dst * MB + t / bs];
     if (p0 < 0 || p0 >= NB || p1 < 0 || p1 >= NB) {
       if (tid == 0) flag(status, HYB_DEVERR_BAD_BLOCK);
       continue;
     }
-    const int a = max(lo, t), rows = min(n, t + 16) - a, vecs = rows * vpr;
-    for (int i = tid; i < 2 * H * vecs; i += 256) {
-      const int kv = i / (H * vecs), h = (i - kv * H * vecs) / vecs, e = i % vecs;
-      uint4* c = static_cast<uint4*>(kv ? ly.b : ly.a);
-      const int64_t off = (int64_t)(a % bs) * vpr + e;
-      c[((int64_t)p1 * H + h) * bs * vpr + off] = c[((int64_t)p0 * H + h) * bs * vpr + off];
-    }
+    const int a = max(lo, t), vecs = (min(n, t + 16) - a) * vpr;
+    const int64_t x0 = p0 * H * head + (int64_t)(a % bs) * vpr, y0 = p1 * H * head + (int64_t)(a % bs) * vpr;
+    for (int e = tid; e < vecs; e += kCopyThreads)
+      for (int h0 = 0; h0 < H; h0 += kU / 2) {
+        uint4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (h0 + u / 2 < H) v[u] = __ldcs(static_cast<const uint4*>(u & 1 ? ly.b : ly.a) + x0 + (h0 + u / 2) * head + e);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (h0 + u / 2 < H) __stcs(static_cast<uint4*>(u & 1 ? ly.b : ly.a) + y0 + (h0 + u / 2) * head + e, v[u]);
+      }
   }
 }
 
@@ -150,10 +182,7 @@ using namespace hyb;
 
 extern "C" {
 
-size_t hyb_beam_reorder_workspace_size(int32_t R, int32_t W) {
-  if (R <= 0 || W <= 0 || W > kMaxBeams || (int64_t)R * W > 65535) return 0;
-  return (size_t)R * W * 4;
-}
+size_t hyb_beam_reorder_workspace_size(int32_t, int32_t) { return 0; }
 
 hyb_status_t hyb_beam_reorder(const int32_t* parents, int32_t* block_tables, int32_t* seq_lens,
                               const int32_t* prefix_lens, int32_t* state_slots,
@@ -193,18 +222,16 @@ hyb_status_t hyb_beam_reorder(const int32_t* parents, int32_t* block_tables, int
       !al(state_slots, 4))
     return HYB_ERR_INVALID_ARG;
   if ((full && (!block_tables || !seq_lens)) || (linear && !state_slots)) return HYB_ERR_INVALID_ARG;
-  if (!workspace || !al(workspace, 4) || ws_bytes < hyb_beam_reorder_workspace_size(R, W))
-    return HYB_ERR_INVALID_ARG;
-  if (R > 65535) return HYB_ERR_UNSUPPORTED;
+  (void)workspace;
+  (void)ws_bytes;
   unsigned* sw = status_word();
   if (!sw) return HYB_ERR_CUDA;
   const cudaStream_t s = (cudaStream_t)stream;
-  int32_t* copy = static_cast<int32_t*>(workspace);
-  const int MB = d->max_blocks_per_seq, bs = d->block_size;
-  cudaError_t e = launch_pdl(beam_seat_kernel, dim3(block_tables ? (MB + kCols - 1) / kCols : 1, R), dim3(128), 0, s,
-                             parents, block_tables, seq_lens, prefix_lens, state_slots, copy, W, MB, bs, sw);
-  count_launch();
-  const int esize = d->dtype == HYB_BF16 ? 2 : 4;
+  const int MB = d->max_blocks_per_seq, bs = d->block_size, esize = d->dtype == HYB_BF16 ? 2 : 4;
+  // Pieces of a row and layer, each a CTA's: 16 of them fill the GPU from a handful of copies on, and a long
+  // state or answer has more work for each.
+  const int pieces = 16;
+  cudaError_t e = cudaSuccess;
   for (int l0 = 0; l0 < L && e == cudaSuccess; l0 += kMaxLayers) {
     Layers ls = {};
     const int n = std::min(kMaxLayers, L - l0);
@@ -213,11 +240,15 @@ hyb_status_t hyb_beam_reorder(const int32_t* parents, int32_t* block_tables, int
       ls.l[l] = layer_types[l0 + l] == HYB_LINEAR ? Layer{io.state_pool, nullptr, io.num_state_slots, 0}
                                                   : Layer{io.k_cache, io.v_cache, 0, io.window};
     }
-    e = launch_pdl(beam_copy_kernel, dim3(16, R * W, n), dim3(256), 0, s, ls, (const int32_t*)copy,
+    e = launch_pdl(beam_copy_kernel, dim3(pieces, R * W, n), dim3(kCopyThreads), 0, s, ls, parents,
                    (const int32_t*)block_tables, (const int32_t*)seq_lens, prefix_lens, (const int32_t*)state_slots, W,
                    state_size / 4, max_suffix_len, d->num_heads, d->head_dim * esize / 16, d->num_blocks, MB, bs, sw);
     count_launch();
   }
+  if (e != cudaSuccess) return cuda_status(e);
+  e = launch_pdl(beam_seat_kernel, dim3(block_tables ? (MB + kCols - 1) / kCols : 1, R), dim3(kMaxBeams), 0, s, parents,
+                 block_tables, seq_lens, prefix_lens, state_slots, W, MB, bs, L > 0 ? 1 : 0, sw);
+  count_launch();
   return cuda_status(e);
 }
 

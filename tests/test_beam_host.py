@@ -117,9 +117,7 @@ def test_reorder_refused(hyb):
     assert call(io=(full, hyb.layer_io(state_pool=3 * F + 8, num_state_slots=9))) == inv
     assert call(size=0) == inv and call(size=126) == inv and call(size=1 << 40) == uns
     assert call(window=4) == inv and call(block_size=24) == uns and call(num_heads=0) == inv
-    n = hyb.hyb_beam_reorder_workspace_size(2, 4)
-    assert n > 0 and hyb.hyb_beam_reorder_workspace_size(0, 4) == 0 and hyb.hyb_beam_reorder_workspace_size(2, 129) == 0
-    assert call(ws=None) == inv and call(ws=F + 2) == inv and call(nb=n - 1) == inv
+    assert hyb.hyb_beam_reorder_workspace_size(2, 4) == 0
     assert hyb.hyb_beam_reorder(F, F, F, F, F, (0, 1), 2, (full, lin), 2, 4, 64, 128, None, F, 1 << 20, 0) == inv
 
 
