@@ -426,8 +426,9 @@ def hyb_beam_reorder(parents, block_tables, seq_lens, prefix_lens, state_slots, 
                      layers, R, W, max_suffix_len, state_size, d, workspace, ws_bytes, stream=None):
     """Tables, lengths, slots, states and cached tokens of the next beams, in place. layer_types
     and layers: host sequences, as for hyb_layer_dispatch."""
-    lt = (C.c_int32 * max(L, 1))(*[int(x) for x in layer_types[:max(L, 0)]])
-    io = (hyb_layer_io_t * max(L, 1))(*layers[:max(L, 0)])
+    n = max(L, 0)
+    lt = (C.c_int32 * max(n, 1))(*map(int, layer_types[:n]))
+    io = (hyb_layer_io_t * max(n, 1))(*layers[:n])
     return _lib.hyb_beam_reorder(_p(parents), _p(block_tables), _p(seq_lens), _p(prefix_lens),
                                  _p(state_slots), lt, L, io, R, W, max_suffix_len, state_size,
                                  _d(d), _p(workspace), ws_bytes, _s(stream))

@@ -5,7 +5,7 @@
 // its request's W parents what its row gets from where (a load and some votes). The permutation follows in
 // place; it reads and sorts while the copies run, and writes once they have ended. Nothing is bound by anything but the
 // bytes that are copied, each read once and written once.
-#include <set>
+#include <vector>
 
 #include "hyb_internal.cuh"
 
@@ -197,26 +197,30 @@ hyb_status_t hyb_beam_reorder(const int32_t* parents, int32_t* block_tables, int
   if (d->window != 0) return HYB_ERR_INVALID_ARG;          // windows come from the layer types
   if (W > kMaxBeams || (int64_t)R * W > 65535 || L > 65535) return HYB_ERR_UNSUPPORTED;
   bool full = false, linear = false;
-  std::set<const void*> seen;                              // each layer owns its pools
+  std::vector<const void*> pools;                          // each layer owns its own
+  pools.reserve(2 * (size_t)L);
   for (int l = 0; l < L; ++l) {
     const hyb_layer_io_t& io = layers[l];
     const int lt = layer_types[l];
     if (lt == HYB_SLIDING ? io.window <= 0 : io.window != 0) return HYB_ERR_INVALID_ARG;
     if (lt == HYB_FULL || lt == HYB_SLIDING) {
-      if (!io.k_cache || !io.v_cache || !al(io.k_cache, 16) || !al(io.v_cache, 16) ||
-          !seen.insert(io.k_cache).second || !seen.insert(io.v_cache).second)
-        return HYB_ERR_INVALID_ARG;
+      if (!io.k_cache || !io.v_cache || !al(io.k_cache, 16) || !al(io.v_cache, 16)) return HYB_ERR_INVALID_ARG;
+      pools.push_back(io.k_cache);
+      pools.push_back(io.v_cache);
       full = true;
     } else if (lt == HYB_LINEAR) {
-      if (!io.state_pool || !al(io.state_pool, 16) || !seen.insert(io.state_pool).second ||
+      if (!io.state_pool || !al(io.state_pool, 16) ||
           io.num_state_slots <= 0 || state_size <= 0 || state_size % 4 != 0)
         return HYB_ERR_INVALID_ARG;
       if (state_size > ((int64_t)1 << 40) / io.num_state_slots) return HYB_ERR_UNSUPPORTED;
+      pools.push_back(io.state_pool);
       linear = true;
     } else {
       return HYB_ERR_INVALID_ARG;
     }
   }
+  std::sort(pools.begin(), pools.end());
+  if (std::adjacent_find(pools.begin(), pools.end()) != pools.end()) return HYB_ERR_INVALID_ARG;
   if (R == 0) return HYB_OK;
   if (!parents || !al(parents, 4) || !al(block_tables, 4) || !al(seq_lens, 4) || !al(prefix_lens, 4) ||
       !al(state_slots, 4))

@@ -63,11 +63,11 @@ struct RowSpan {
 };
 __device__ __forceinline__ RowSpan row_span(const PrefixArgs& a, int n, int first, int P) {
   RowSpan r;
+  n = max(n, 0);
   r.first = first;
   r.P = P;
-  r.n = max(n, 0);
+  r.n = n;
   r.lo = (a.window > 0 && n > a.window) ? n - a.window : 0;
-  // (n and P are at most 2^31 - 1 and 2^24: the difference cannot overflow)
   if (n - P > a.max_suffix || n > (a.MB << a.rsh) * kBlockSize) r.n = -1;
   return r;
 }

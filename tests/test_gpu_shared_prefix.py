@@ -106,11 +106,43 @@ def test_prefix_ends(hyb, devstatus, P, dt, D, bs):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 33, 63, 65, 127, 128, 129, 257, 300])
-@pytest.mark.parametrize("Hq,Hk,D", [(2, 2, 128), (8, 2, 128), (3, 1, 64), (5, 5, 64)])
-def test_group_sizes(hyb, devstatus, rows, Hq, Hk, D):
+@pytest.mark.parametrize("Hq,Hk,D,dt", [(2, 2, 128, torch.bfloat16), (8, 2, 128, torch.bfloat16), (3, 1, 64, torch.bfloat16), (5, 5, 64, torch.bfloat16), (3, 1, 128, torch.bfloat16),
+                                        (2, 1, 256, torch.bfloat16), (4, 2, 32, torch.bfloat16), (4, 2, 128, torch.float32), (3, 3, 16, torch.float32)])
+def test_group_sizes(hyb, devstatus, rows, Hq, Hk, D, dt):
+    """From one row to more than a CTA takes, on both sides of every tile and of the choice of the kernel."""
     tails = [1 + (i * 7) % 50 for i in range(rows)]
-    Case(hyb, [(700, tails), (130, tails[:rows // 2 + 1])], Hq, Hk, D, seed=rows).check()
+    Case(hyb, [(700, tails), (130, tails[:rows // 2 + 1])], Hq, Hk, D, dt, seed=rows).check()
     assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(17, 1, 64), (24, 1, 128), (40, 2, 128), (96, 1, 128), (130, 1, 128), (20, 1, 256)])
+def test_many_query_heads(hyb, devstatus, Hq, Hk, D):
+    """More query heads to a key head than a row tile has rows, and than the tensor-core kernel takes."""
+    Case(hyb, [(300, [1, 40, 3, 0]), (513, [9] * 5), (20, [-4, 300])], Hq, Hk, D, seed=Hq).check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 3.0, 1e-30])
+@pytest.mark.parametrize("dt,D,rows", [(torch.bfloat16, 128, 3), (torch.bfloat16, 128, 70), (torch.bfloat16, 32, 9), (torch.float32, 64, 3), (torch.float32, 64, 12)])
+def test_scales(hyb, devstatus, scale, dt, D, rows):
+    c = Case(hyb, [(200, [1 + i % 9 for i in range(rows)]), (40, [5, 30])], 2, 2, D, dt, seed=rows, amp=0.3)
+    c.d.scale = scale
+    c.check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt,D", [(torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 64)])
+def test_no_keys_at_all(hyb, devstatus, dt, D):
+    """Bounds of zero, requests without tokens, and a bound on a group of none."""
+    c = Case(hyb, [(0, [0, 0]), (0, [0])], 2, 2, D, dt)
+    out = c.check()
+    assert (out == 0).all()
+    c.p = hyb.prefix_dims(2, 2, 0, 5, 0)           # groups of rows, none allowed
+    c.n = hyb.hyb_paged_attn_decode_shared_prefix_workspace_size(c.B, c.p, c.d)
+    c.ws = torch.empty(c.n // 4 + 4, device="cuda")
+    c.out.fill_(7)
+    hyb.check(c.call())
+    assert (c.out == 7).all() and devstatus() == (hyb.HYB_ERR_DEVICE_CHECK, hyb.HYB_DEVERR_BAD_LENGTH)
 
 
 @pytest.mark.parametrize("dt,D,Hq,Hk", [(torch.bfloat16, 128, 8, 2), (torch.bfloat16, 128, 32, 32), (torch.bfloat16, 256, 2, 1), (torch.float32, 64, 3, 3)])
@@ -181,14 +213,9 @@ def test_equal_to_the_plain_decode(hyb):
 def test_many_groups(hyb, devstatus, dt, D):
     """More groups than a warp has lanes, some empty, and rows of none between them."""
     groups = [(10 + 13 * g, [1 + g % 5] * (g % 4)) for g in range(150)]
-    c = Case(hyb, groups, 2, 2, D, dt, seed=1)
-    c.check()
-    # every second group goes: its rows are nobody's
-    keep = range(0, 150, 2)
-    cu = [c.cu[g] for g in keep] + [c.cu[149]]
-    lens = [c.cu[g + 1] - c.cu[g] for g in keep]
+    Case(hyb, groups, 2, 2, D, dt, seed=1).check()
+    Case(hyb, groups, 2, 2, D, dt, seed=1, empty_groups=True, extra_rows=3).check()
     assert devstatus() == (0, 0)
-    assert len(cu) == len(lens) + 1
 
 
 def test_bad_groups_and_lengths_are_flagged_and_left(hyb, devstatus):
@@ -222,10 +249,16 @@ def test_bad_groups_and_lengths_are_flagged_and_left(hyb, devstatus):
     R.check_attention(c.out, ref, c.dt)
     assert (c.out[4] == 7).all()
     # a negative length is no key
-    c = Case(hyb, groups, 4, 2, 128, seed=5)
-    c.dev[0][1] = -3
-    hyb.check(c.call())
-    assert (c.out[1] == 0).all() and devstatus() == (0, 0)
+    for n in (-3, -2 ** 31):
+        c = Case(hyb, groups, 4, 2, 128, seed=5)
+        c.dev[0][1] = n
+        hyb.check(c.call())
+        assert (c.out[1] == 0).all() and devstatus() == (0, 0)
+    for n in (2 ** 31 - 1, 1 << 20):
+        c.dev[0][1] = n
+        c.out.fill_(7)
+        hyb.check(c.call())
+        assert (c.out[1] == 7).all() and devstatus() == (hyb.HYB_ERR_DEVICE_CHECK, hyb.HYB_DEVERR_BAD_LENGTH)
 
 
 @pytest.mark.parametrize("dt,D", [(torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 64)])
