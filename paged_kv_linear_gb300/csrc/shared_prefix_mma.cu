@@ -22,7 +22,7 @@ constexpr float kNoBase = -3.3e38f;            // the base of a row that has see
 template <int D, int NT>
 struct MmaShape {
   static constexpr int KG = kWarps / NT;       // key groups: rings of stages, each read by NT warps
-  static constexpr int KP = NT == 1 ? 1 : NT == 4 && D == 64 ? 4 : 2;   // pieces of a stage
+  static constexpr int KP = NT == 1 ? 1 : NT == 4 && D <= 128 ? 4 : 2;   // pieces of a stage
   static constexpr int TILE = 16 * D * 2;      // K or V of a piece
   static constexpr int FIT = 65536 / (KG * KP * 2 * TILE);
   static constexpr int NST = FIT > 2 ? FIT : 2;
@@ -265,10 +265,8 @@ struct Fetch {
       const int row = __shfl_sync(0xffffffffu, y, next % AHEAD * KP + j);
       if (row >= 0 && lane == 0) {
         uint8_t* dst = ring + (st * KP + j) * 2 * TILE;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + c * 2048, tk, c * 64, row, &full[st]);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + TILE + c * 2048, tv, c * 64, row, &full[st]);
+        tma_load_3d(dst, tk, 0, row, 0, &full[st]);
+        tma_load_3d(dst + TILE, tv, 0, row, 0, &full[st]);
       }
     }
     ++next;
@@ -578,10 +576,11 @@ bool prefix_mma_supported(int dtype, int D) {
 cudaError_t launch_prefix_mma(int D, const void* q, const void* kc, const void* vc, const PrefixArgs& a, bool prefix,
                               bool early, cudaStream_t s) {
   CUtensorMap tk, tv;
-  const uint64_t dims[2] = {(uint64_t)D, (uint64_t)a.NB * a.Hk * (kBlockSize << a.rsh)};
-  const uint64_t str[1] = {(uint64_t)D * 2};
-  const uint32_t box[2] = {64, kBlockSize};
-  if (!encode_tmap_bf16(&tk, kc, 2, dims, str, box) || !encode_tmap_bf16(&tv, vc, 2, dims, str, box))
+  // {64 columns, rows, column blocks}: one box is a piece of all columns, [D / 64][16 rows][64], swizzled
+  const uint64_t dims[3] = {64, (uint64_t)a.NB * a.Hk * (kBlockSize << a.rsh), (uint64_t)D / 64};
+  const uint64_t str[2] = {(uint64_t)D * 2, 128};
+  const uint32_t box[3] = {64, kBlockSize, (uint32_t)D / 64};
+  if (!encode_tmap_bf16(&tk, kc, 3, dims, str, box) || !encode_tmap_bf16(&tv, vc, 3, dims, str, box))
     return cudaErrorInvalidValue;
   const int64_t rows = (int64_t)a.max_group * (a.Hq / a.Hk);
   const int nt = !prefix || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
