@@ -434,7 +434,10 @@ hyb_status_t hyb_qk_norm_rope_append(void* q_out, void* k_out, const void* q, co
  * A group whose rows are not within [0, B), decrease, or are more than max_group, or whose
  * prefix is negative or above max_prefix_len, sets HYB_DEVERR_BAD_LENGTH; its out rows are left as they were, and
  * so is a request's with n > P + max_suffix_len or n above the block table's capacity. A bad
- * block id sets HYB_DEVERR_BAD_BLOCK and its tokens are left out.
+ * block id sets HYB_DEVERR_BAD_BLOCK and its tokens are left out. A NaN or infinity in a request's
+ * q or own tokens stays within it; one among the common tokens may reach all of the group's requests.
+ * bf16 with heads of 64, 128 or 256 runs on matrix instructions, which take the softmax's weights rounded to
+ * bf16; other types and heads compute in fp32 throughout.
  * `workspace`: device memory, 16-byte aligned, hyb_paged_attn_decode_shared_prefix_workspace_size()
  * bytes (the parts' partial results); no initialisation, nothing kept between calls. Calls that
  * may run at the same time need workspaces of their own. The bounds, B and the heads choose how

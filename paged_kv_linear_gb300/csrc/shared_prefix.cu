@@ -439,9 +439,11 @@ PrefixPlan plan_prefix(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t*
     const int64_t slots = (int64_t)sms * (D == 256 ? 1 : 3);
     r.Lp = round16(std::min<int64_t>(1536, std::max<int64_t>(nt == 1 ? 512 : 256, P * units / slots)));
   } else if (use_tiles(rows)) {
-    // three CTAs an SM
+    // one wave of the CTAs that shared memory holds, if that leaves parts of 128 to 512 keys
+    const int es = d->dtype == HYB_BF16 ? 2 : 4, smem = kTileKeys * (4 * D * es + 32) + kTileRows * (D + kTileKeys) * 4 + 256;
     const int64_t units = std::max<int64_t>(1, heads * ((rows + kTileRows - 1) / kTileRows));
-    r.Lp = round16(std::min<int64_t>(512, std::max<int64_t>(128, P * units / (3 * sms))));
+    const int64_t n = std::max<int64_t>(1, std::min(227 * 1024 / (smem + 1024), 5) * sms / units);
+    r.Lp = (int)std::min<int64_t>(512, std::max<int64_t>(128, (P / n + 32) / 32 * 32));
   } else {
     r.Lp = round16(std::min<int64_t>(256, std::max<int64_t>(64, (int64_t)P * B * p->num_q_heads / (8 * sms))));
   }

@@ -504,8 +504,9 @@ prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     tma_prefetch_desc(&tv);
   }
   // early: launched behind the tensor-core kernel of the same call, which began when everything before it had
-  // ended and writes nothing that this one reads or writes. So this one runs beside it, and waits for it
-  // only at its end (the joining kernel waits for this one alone).
+  // ended and writes nothing that this one reads or writes. So this one runs beside it, on the SMs that it leaves, and
+  // its last CTA alone waits for it: the joining kernel waits for this one, which then ends after both. (With every
+  // CTA waiting, the first ones kept the others off those SMs: 256 requests on 32768 tokens 137 us against 118.)
   if (!early) pdl_wait();
   pdl_trigger();
   const int rep = a.Hq / a.Hk;
@@ -545,7 +546,7 @@ prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       u.table = a.bt + (int64_t)u.first * a.MB;
       attend_own<D>(&tk, &tv, q, a, u, r.own_lo(), sm);
     }
-    if (early) pdl_wait();
+    if (early && blockIdx.x == gridDim.x - 1) pdl_wait();
   }
 }
 

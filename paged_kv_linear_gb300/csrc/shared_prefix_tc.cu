@@ -121,7 +121,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   // what the softmax threads need rarely waits here: their registers are all spoken for
   __shared__ struct {
     const int32_t* btrow;
-    int b0, row0, cnt, part, head0;                  // head0: the first query head of hk
+    int b0, row0, cnt, part, head0, two;             // head0: the first query head of hk
   } info;
   if (tid == 0) {
     info.btrow = btrow;
@@ -130,6 +130,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     info.cnt = cnt;
     info.part = part;
     info.head0 = hk * rep;
+    info.two = two;
   }
 
   if (warp == kWarpMma) {
@@ -334,7 +335,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     }
     const bool any = __any_sync(0xffffffffu, min_hi != INT32_MAX);   // a warp without rows only keeps the pace
     bool good = true;                                  // no bad block in the part
-    for (int s = kb / kBlockSize + lane; s * kBlockSize < k1; s += 32) good = good && block_of(s) >= 0;
+#pragma unroll 8
+    for (int s = kb / kBlockSize + lane; s < (k1 + kBlockSize - 1) / kBlockSize; s += 32) {
+      const int pb = btrow[s >> a.rsh];                // (all asked for at once)
+      good = good & (pb >= 0) & (pb < a.NB);
+    }
     if (!good) min_hi = 0;                             // one: every tile takes the masking path
     max_lo = __reduce_max_sync(0xffffffffu, max_lo);
     min_hi = __reduce_min_sync(0xffffffffu, min_hi);
@@ -420,21 +425,39 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       mbar_arrive(&bars->pfull[t]);
     }
     if (ok && steps) ok = __all_sync(0xffffffffu, mbar_wait(&bars->odone[t], 0));
+    // The state of the warp's 32 rows through shared memory (the rings', once no product reads them any more), so
+    // that a row is written by 32 lanes side by side (a row a thread: 5.3 us at the end of each CTA).
+    if (ok && info.two) ok = __all_sync(0xffffffffu, mbar_wait(&bars->odone[t ^ 1], 0));
     if (ok && steps && any) {
       tc_fence_after();
-      const int f = info.row0 + t * tile_rows + r, of = a.Hq / a.Hk;
-      const bool there = r < tile_rows && f < info.cnt;
-      const int64_t at = ((int64_t)(info.b0 + f / of) * a.Hq + info.head0 + f % of) * (a.Sp + a.Ss) + info.part;
-      if (there) a.ws_ml[at] = make_float2(m_used, l);
+      constexpr int kPitch = kD + 4;
+      static_assert(kNSW * 32 * kPitch * 4 <= (kNK + kNV) * kTile, "the rings hold all rows' sums");
+      float* const stage = reinterpret_cast<float*>(sm + kOffK) + (size_t)warp * 32 * kPitch;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float o[32];
         tmem_ld32(o_col + c * 32, o);
         tmem_ld_wait();
-        if (there)
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(a.ws_acc + at * kD + c * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(stage + lane * kPitch + c * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+      __syncwarp();
+      const int of = a.Hq / a.Hk;
+      auto slot = [&](int row) {                       // of a row of the tile; -1: none there
+        const int f = info.row0 + t * tile_rows + row;
+        return row < tile_rows && f < info.cnt
+                   ? ((int64_t)(info.b0 + f / of) * a.Hq + info.head0 + f % of) * (a.Sp + a.Ss) + info.part
+                   : (int64_t)-1;
+      };
+      const int64_t mine = slot(quarter * 32 + lane);
+      if (mine >= 0) a.ws_ml[mine] = make_float2(m_used, l);
+#pragma unroll 8
+      for (int n = 0; n < 32; ++n) {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, n);
+        if (at >= 0)
+          *reinterpret_cast<float4*>(a.ws_acc + at * kD + lane * 4) =
+              *reinterpret_cast<const float4*>(stage + n * kPitch + lane * 4);
       }
     } else if (!ok && lane == 0) {
       flag(a.status, HYB_DEVERR_TIMEOUT);
