@@ -450,7 +450,7 @@ beam_pick_kernel(float* __restrict__ scores_out, int32_t* __restrict__ parents, 
                  uint8_t* __restrict__ finished_out, const SelectArgs a) {
   // total = (x - top) + base with base = score - log sum e^(x - top) (NaN: no candidates of logits);
   // a logit of any size then keeps its distance from the largest
-  __shared__ double base[128];
+  __shared__ double base[128], terms[kThreads];
   __shared__ float top[128];
   __shared__ float score[128];
   __shared__ uint8_t done[128];
@@ -468,39 +468,53 @@ beam_pick_kernel(float* __restrict__ scores_out, int32_t* __restrict__ parents, 
 #pragma unroll
   for (int k = 0; k < 2; ++k) early[k] = tid + k * kThreads < C ? best[tid + k * kThreads] : make_float2(0.f, 0.f);
   if (tid == 0) count = 0;
+  // Each row's maximum (and whether it has one), a row a warp
   for (int w = warp; w < a.W; w += kThreads / 32) {
     const int row = r * a.W + w;
     const float2* ml = a.ml + (int64_t)row * a.S;
     const float2 v0 = lane < a.S ? ml[lane] : make_float2(0.f, 0.f);      // (not used where the row is not live)
     const float s = a.scores[row];
-    const bool fin = a.finished && a.finished[row];
-    double b = NAN;
+    const bool fin = a.finished && a.finished[row], live = fabsf(s) < INFINITY && !fin;
     float M = -INFINITY;
-    if (fabsf(s) < INFINITY && !fin) {
+    if (live)
       for (int i = lane; i < a.S; i += 32) {
         const float2 v = i == lane ? v0 : ml[i];
         if (v.y > 0.f) M = fmaxf(M, v.x);
       }
-      for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      double l = 0.0;
-      for (int i = lane; i < a.S; i += 32) {
-        const float2 v = i == lane ? v0 : ml[i];
-        if (v.y != 0.f) l += v.x == M ? (double)v.y : (double)v.y * exp((double)v.x - (double)M);
-      }
-      for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (l > 0.0) b = (double)s - log(l);
-      else if (l != l && lane == 0) flag(a.status, HYB_DEVERR_BAD_VALUE);
-    } else if (!(s < INFINITY) && lane == 0) {
-      flag(a.status, HYB_DEVERR_BAD_VALUE);
-    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane == 0) {
-      base[w] = b;
+      base[w] = live ? 0.0 : (double)NAN;
       top[w] = M;
       score[w] = s;
       done[w] = fin;
+      if (!(s < INFINITY)) flag(a.status, HYB_DEVERR_BAD_VALUE);
     }
   }
   __syncthreads();
+  // and its sum in 64 bits, a (row, slice) a thread and then a row a thread: the 64-bit unit is narrow, so what
+  // fits into one warp goes through it once (a row a warp: 4 us more for 8 beams).
+  const int group = max(1, kThreads / a.S);      // rows at a time
+  for (int w0 = 0; w0 < a.W; w0 += group) {
+    const int rows = min(group, a.W - w0);
+    double part = 0.0;
+    for (int i = tid; i < rows * a.S; i += kThreads) {           // (more than one a thread only for one row)
+      const int w = w0 + i / a.S;
+      if (base[w] != base[w]) continue;
+      const float2 v = a.ml[((int64_t)r * a.W + w) * a.S + i % a.S];
+      if (v.y != 0.f) part += v.x == top[w] ? (double)v.y : (double)v.y * exp((double)v.x - (double)top[w]);
+    }
+    terms[tid] = part;
+    __syncthreads();
+    if (tid < rows && base[w0 + tid] == base[w0 + tid]) {
+      const int n = min(a.S, kThreads);
+      double l = 0.0;
+      for (int i = 0; i < n; ++i) l += terms[tid * n + i];
+      if (l != l) flag(a.status, HYB_DEVERR_BAD_VALUE);
+      base[w0 + tid] = l > 0.0 ? (double)score[w0 + tid] - log(l) : (double)NAN;
+    }
+    __syncthreads();
+  }
   // Candidates 256 at a time, behind those kept; more than kKeep of them are thinned to 256 at most.
   for (int i0 = 0; i0 < C + a.W; i0 += kThreads) {
     const int i = i0 + tid;
