@@ -3,8 +3,12 @@
 //
 // Two kernels, the copies first: they go by the old tables and slots, and each CTA works out for itself from
 // its request's W parents what its row gets from where (a load and some votes). The permutation follows in
-// place; it reads and sorts while the copies run, and writes once they have ended. Nothing is bound by anything but the
-// bytes that are copied, each read once and written once.
+// place; it reads and sorts while the copies run, and writes once they have ended (the other way round, with a list of
+// the copies in memory: 16.5 us against 7.2 for one request of 4 beams in 4 layers).
+//
+// Bound by the bytes that are copied, each read once and written once: 16 x 4 beams in 8 layers, up to 1024 tokens, 828
+// MB 127 us, 0.96 of the copy rate; 32 x 8 beams in two Linear layers, 755 MB 107 us, 1.04. Eight vectors of 16 bytes a
+// thread in flight (one: 150 us for the former). Streaming loads and stores: the next step reads other layers first.
 #include <vector>
 
 #include "hyb_internal.cuh"

@@ -9,6 +9,12 @@
 // part but for rows that end inside it and windows, so both row tiles walk the same key tiles; rows come
 // through a tensor map {D, query heads, requests} whose box of rep x (128 / rep) rows is a tile (rep: query
 // heads of a key head; 126 rows where it is 3); and a CTA leaves its softmax's state instead of dividing.
+//
+// 256 requests of 4 query heads a key head on 32768 tokens, 8 key heads: 128 CTAs of 64 key tiles, 108 us, 1.28 PFLOP/s,
+// 0.67 of the bf16 rate (tensor pipe 53 % busy over 152 SMs): a key tile takes 1.43 us, as in the causal prefill, the
+// start 4 us and the end 3, and 24 SMs have no CTA (they run the requests' own tokens). Parts of half the length
+// fill them but start and end twice (128 us). Not kept: the two softmax warpgroups on every other key tile of one row
+// tile (no change at 64 to 128 rows, and its registers cost the large case 13 us).
 #include <cuda_bf16.h>
 
 #include "shared_prefix.cuh"
