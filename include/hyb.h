@@ -430,7 +430,8 @@ hyb_status_t hyb_qk_norm_rope_append(void* q_out, void* k_out, const void* q, co
  * request of the group (of the prefix) or not the request (of its own part) sees are not read.
  *   q, out      [B][num_q_heads][D] of d->dtype; caches as for hyb_paged_attn_decode
  *   cu_groups   int32 [G+1], prefix_lens int32 [G]. Rows that belong to no group are left as
- *               they were. Groups of one request, empty groups and P = 0 are fine.
+ *               they were. Groups of one request, empty groups and P = 0 are fine; cu_groups does
+ *               not decrease, so that no row belongs to two.
  * A group whose rows are not within [0, B), decrease, or are more than max_group, or whose
  * prefix is negative or above max_prefix_len, sets HYB_DEVERR_BAD_LENGTH; its out rows are left as they were, and
  * so is a request's with n > P + max_suffix_len or n above the block table's capacity. A bad
@@ -484,7 +485,7 @@ hyb_status_t hyb_paged_attn_decode_shared_prefix(
  * outputs overlap nothing. R = 0 is a no-op. `workspace`: device memory, 16-byte aligned, of
  * hyb_beam_select_workspace_size() bytes; no initialisation, nothing kept between calls;
  * calls that may run at the same time need workspaces of their own. Equal calls give equal
- * bits. Limits: num_beams <= 128, num_out <= 128 and <= W V, W V <= 2^31 - 1, R x W <= 2^20.
+ * bits. Limits: num_beams <= 128, num_out <= 128 and <= W V, V <= 2^30, W V <= 2^31 - 1, R x W <= 2^20.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t num_beams;           /* W                                                       */
@@ -583,7 +584,7 @@ hyb_status_t hyb_layer_dispatch(const int32_t* layer_types, int32_t L, int32_t m
  *               share a pool
  *   state_size  fp32 elements of one slot of a state pool (num_v_heads D D), a multiple of 4; not used without a Linear layer
  *   max_suffix_len  a bound on n - P; a longer parent sets HYB_DEVERR_BAD_LENGTH and its tokens
- *               are not copied, nor where n is above the table's capacity
+ *               are not copied, nor where n is above the table's capacity (or 2^30)
  *   d           num_heads (key heads), head_dim, block_size, num_blocks, max_blocks_per_seq and
  *               dtype of the caches; the rest has to be valid as in the other calls
  * Bad block ids set HYB_DEVERR_BAD_BLOCK, bad slots HYB_DEVERR_BAD_STATE, and what they name is

@@ -594,7 +594,7 @@ hyb_status_t check_beam_dims(int R, const hyb_beam_dims_t* d) {
   if (d->row_stride != 0 && d->row_stride < d->vocab) return HYB_ERR_INVALID_ARG;
   const int64_t all = (int64_t)d->num_beams * d->vocab;
   if (d->num_out > all) return HYB_ERR_INVALID_ARG;
-  if (d->num_beams > 128 || d->num_out > 128 || all > INT32_MAX || d->row_stride > ((int64_t)1 << 40) ||
+  if (d->num_beams > 128 || d->num_out > 128 || d->vocab > (1 << 30) || all > INT32_MAX || d->row_stride > ((int64_t)1 << 40) ||
       (int64_t)R * d->num_beams > (1 << 20))
     return HYB_ERR_UNSUPPORTED;
   return HYB_OK;

@@ -600,6 +600,7 @@ hyb_status_t hyb_paged_attn_decode_shared_prefix(
   a.max_group = p->max_group;
   a.max_prefix = p->max_prefix_len;
   a.max_suffix = p->max_suffix_len;
+  a.cap = (int)std::min<int64_t>(INT32_MAX, (int64_t)d->max_blocks_per_seq * d->block_size);
   a.scale_log2 = std::max(std::fabs(d->scale) * 1.4426950408889634f, 1e-37f);
   a.q_sign = d->scale < 0.f ? 0x80008000u : 0u;
   a.Lp = plan.Lp;

@@ -20,6 +20,7 @@ struct PrefixArgs {
   const int32_t *bt, *lens, *cu, *pre;
   int B, G, Hq, Hk, NB, MB, rsh, window;   // rsh: log2(block size / 16)
   int max_group, max_prefix, max_suffix;
+  int cap;                                 // tokens that a table row holds (2^31 - 1 at most)
   float scale_log2;                        // log2(e) |scale|, not 0 (which is the same as a tiny one)
   uint32_t q_sign;                         // a pair's bf16 sign bits where the scale is negative
   int Lp, Sp, Ls, Ss;
@@ -45,7 +46,7 @@ __device__ __forceinline__ bool group_ok(const PrefixArgs& a, int g, int& b0, in
   b1 = a.cu[g + 1];
   P = a.pre[g];
   return b0 >= 0 && b1 >= b0 && b1 <= a.B && b1 - b0 <= a.max_group && P >= 0 &&
-         P <= a.max_prefix && P <= (a.MB << a.rsh) * kBlockSize;
+         P <= a.max_prefix && P <= a.cap;
 }
 
 // Keys of row b: [lo, min(P, n)) of the prefix, [max(P, lo), n) of its own. n < 0: left out.
@@ -68,7 +69,7 @@ __device__ __forceinline__ RowSpan row_span(const PrefixArgs& a, int n, int firs
   r.P = P;
   r.n = n;
   r.lo = (a.window > 0 && n > a.window) ? n - a.window : 0;
-  if (n - P > a.max_suffix || n > (a.MB << a.rsh) * kBlockSize) r.n = -1;
+  if (n - P > a.max_suffix || n > a.cap) r.n = -1;
   return r;
 }
 
@@ -80,12 +81,21 @@ __device__ __forceinline__ RowSpan find_row(const PrefixArgs& a, int b, bool* ba
   r.first = r.P = r.lo = 0;
   r.n = -1;
   if (bad) *bad = false;
-  for (int g0 = 0; g0 < a.G; g0 += 32) {
+  // the last group that begins at b or before, 32 probes a step (cu does not decrease), down to 32 of them
+  int g0 = 0, g1 = a.G;
+  while (g1 - g0 > 32) {
+    const int step = (g1 - g0 + 31) / 32, g = g0 + lane * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, g < g1 && a.cu[g] <= b));
+    if (k == 0) return r;
+    g0 += (k - 1) * step;
+    g1 = min(g1, g0 + step);
+  }
+  {
     const int g = g0 + lane;
     int b0 = 0, b1 = 0, P = 0;
-    const bool ok = g < a.G && group_ok(a, g, b0, b1, P);
-    const unsigned m = __ballot_sync(0xffffffffu, g < a.G && b0 <= b && b < b1);
-    if (!m) continue;
+    const bool ok = g < g1 && group_ok(a, g, b0, b1, P);
+    const unsigned m = __ballot_sync(0xffffffffu, g < g1 && b0 <= b && b < b1);
+    if (!m) return r;
     const int src = __ffs(m) - 1;
     const bool good = __shfl_sync(0xffffffffu, ok, src);
     b0 = __shfl_sync(0xffffffffu, b0, src);
@@ -94,7 +104,6 @@ __device__ __forceinline__ RowSpan find_row(const PrefixArgs& a, int b, bool* ba
       r = row_span(a, n, b0, P);
       if (bad) *bad = r.n < 0;
     }
-    break;
   }
   return r;
 }

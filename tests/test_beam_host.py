@@ -75,6 +75,7 @@ def test_select_refused(hyb):
         assert call(**{name: 0}) == inv and call(**{name: -3}) == inv
     assert call(num_out=5, vocab=1) == inv                       # more than there are candidates
     assert call(num_beams=129) == uns and call(num_out=129) == uns
+    assert call(num_beams=1, vocab=(1 << 30) + 1) == uns
     assert call(num_beams=100, vocab=1 << 25) == uns and call(R=1 << 19) == uns
     assert call(dtype=hyb.HYB_F16) == inv and call(eos_token=1000) == inv and call(eos_token=-2) == inv
     assert call(row_stride=999) == inv and call(row_stride=-1) == inv and call(row_stride=1 << 41) == uns

@@ -345,6 +345,17 @@ def test_reorder_bad_values_are_flagged_and_left_out(hyb, devstatus):
     assert all(torch.equal(a, b) for a, b in zip(before, s.pools[0])) and (s.lens_d[:3] == lens[0]).all()
 
 
+def test_reorder_of_odd_lengths_copies_nothing(hyb, devstatus):
+    """A parent without tokens behind the prefix, shorter than it, or of a length below zero."""
+    for n in (20, 7, 0, -1, -2 ** 31):
+        s = Stack(hyb, [FULL, SLIDING], 1, 3, 20, 30, seed=4)
+        s.lens_d[0] = n
+        before = [x.clone() for p in s.pools for x in p]
+        hyb.check(s.call(on_gpu([[0, 0, 0]]), slots=None))
+        assert s.lens_d.tolist() == [n] * 3 and all(torch.equal(a, b) for a, b in zip(before, [x for p in s.pools for x in p]))
+    assert devstatus() == (0, 0)
+
+
 def test_reorder_in_a_graph(hyb, devstatus):
     s = Stack(hyb, [FULL, LINEAR], 3, 4, 18, 60, seed=6)
     p = on_gpu(parents_of(3, 4, 0, "keep"))

@@ -218,6 +218,31 @@ def test_many_groups(hyb, devstatus, dt, D):
     assert devstatus() == (0, 0)
 
 
+def test_groups_of_one_in_thousands(hyb, devstatus):
+    """A search among more than 32 x 32 groups, rows before, between and behind them."""
+    g = torch.Generator().manual_seed(3)
+    groups = [(int(p), [int(t)] if keep else []) for p, t, keep in zip(torch.randint(0, 40, (2500,), generator=g), torch.randint(1, 20, (2500,), generator=g), torch.rand(2500, generator=g) < 0.7)]
+    c = Case(hyb, groups, 1, 1, 64, seed=4, extra_rows=5)
+    c.check()
+    # the first rows are nobody's either
+    for i in range(3):
+        c.cu[i] = c.cu[3]
+    c.dev[1].copy_(torch.tensor(c.cu, dtype=torch.int32))
+    c.out.fill_(7)
+    c.check()
+    assert devstatus() == (0, 0) and c.cu[0] > 0
+
+
+def test_a_table_of_more_tokens_than_an_integer_counts(hyb, devstatus):
+    c = Case(hyb, [(300, [70])], 2, 1, 128, bs=256, seed=2)
+    wide = torch.full((1, 1 << 23), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.bt.shape[1]] = c.bt
+    c.bt = wide
+    c.d.max_blocks_per_seq = 1 << 23
+    c.check()
+    assert devstatus() == (0, 0)
+
+
 def test_bad_groups_and_lengths_are_flagged_and_left(hyb, devstatus):
     groups = [(40, [3, 4]), (50, [1, 2, 9]), (30, [5]), (64, [2, 8])]
     for what, edit in {
