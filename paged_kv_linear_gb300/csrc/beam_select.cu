@@ -17,9 +17,11 @@
 // Bytes would bound it, each logit read once; instructions do. 64 x 8 beams over 131072 tokens, bf16 (134 MB): 43 us a
 // call, 20 at the copy rate; the first kernel 38 us, 3.5 TB/s, 27 million warp instructions, issue slots 57 % busy: some
 // 140 of a warp's 400 a batch are the exponentials and their sum, 110 the loads, maxima and loop, the rest the
-// candidates. Four CTAs an SM with the next batch's loads in flight (five without: 52 us). A slice is 8 batches where
-// there are rows enough (4: 50 us, 2: 61, 1: 75, since each starts its bound anew). One request of 4 beams over 32768
-// tokens, fp32: 9.6 us, two kernels of some 4 us.
+// candidates. Four CTAs an SM with the next batch's loads in flight, and a slice of 8 batches where there are rows enough
+// (while the whole took 48 us: five CTAs without loads ahead 54; slices of 4 batches 50, 2 61, 1 75, since each starts
+// its bound anew). Warps that put down their own best without a barrier a batch: 47 us, and rising rows 0.8 ms or more.
+// The same shape with 8 choices and every row constant takes 57 us, falling 44, rising, where each batch raises the
+// bound, 168. One request of 4 beams over 32768 tokens, fp32: 9.6 us, two kernels of some 4 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
