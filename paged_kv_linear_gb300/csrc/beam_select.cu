@@ -524,9 +524,12 @@ beam_pick_kernel(float* __restrict__ scores_out, int32_t* __restrict__ parents, 
     }
     __syncthreads();
   }
-  // Candidates 256 at a time, behind those kept; more than kKeep of them are thinned to 256 at most.
+  // Candidates 256 at a time, behind those kept; more than kKeep of them are thinned to 256 at most. Whether there are
+  // more is what the barrier says of the places that were given out: the counter itself may already be on its way to the
+  // next 256 when a late warp looks at it.
   for (int i0 = 0; i0 < C + a.W; i0 += kThreads) {
     const int i = i0 + tid;
+    int at = -1;                         // this thread's place
     if (i < C) {
       const int w = i / per;
       const float2 c = i0 == 0 ? early[0] : i0 == kThreads ? early[1] : best[i];
@@ -534,7 +537,7 @@ beam_pick_kernel(float* __restrict__ scores_out, int32_t* __restrict__ parents, 
         Key y;
         y.hi = ordered(base[w] + ((double)c.x - (double)top[w]));
         y.lo = kNone - ((uint32_t)w * (uint32_t)a.V + __float_as_uint(c.y));
-        list[atomicAdd(&count, 1)] = y;
+        list[at = atomicAdd(&count, 1)] = y;
       }
     } else if (i < C + a.W) {
       const int w = i - C;
@@ -542,13 +545,11 @@ beam_pick_kernel(float* __restrict__ scores_out, int32_t* __restrict__ parents, 
         Key y;
         y.hi = ordered((double)score[w]);
         y.lo = kNone - ((uint32_t)w * (uint32_t)a.V + (uint32_t)a.eos);
-        list[atomicAdd(&count, 1)] = y;
+        list[at = atomicAdd(&count, 1)] = y;
       }
     }
-    __syncthreads();
-    const int n = count;
-    if (n > kKeep) {
-      const int kept = thin_out(list, n, a.N, scratch, low, &left);
+    if (__syncthreads_or(at >= kKeep)) {
+      const int kept = thin_out(list, count, a.N, scratch, low, &left);
       __syncthreads();
       if (tid == 0) count = kept;
       __syncthreads();
