@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const T* __rest
   __shared__ K list[kKeep + kBatch];
   __shared__ K scratch[kThreads];
   __shared__ int count, left;
+  __shared__ volatile int full;          // the last batch that filled the list beyond kKeep
   __shared__ float red[kThreads / 32];
   __shared__ uint32_t low[kLow];
   pdl_wait();
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const T* __rest
   const int off = (int)(reinterpret_cast<uintptr_t>(x) & 15);
   const int lo = s * a.slice, hi = min(a.V, lo + a.slice);   // this slice's tokens
   const int64_t o = (int64_t)row * a.S + s;
-  if (tid == 0) count = 0;
+  if (tid == 0) count = full = 0;
   float bound_x = -INFINITY;             // logits that do not reach it are not among the N best
   float lm = -INFINITY;                  // the thread's maximum
   float m = -INFINITY, l = 0.f;          // the warp's maximum, and the thread's sum of e^(x - m)
@@ -409,11 +410,14 @@ __global__ void __launch_bounds__(kThreads, 4) beam_slice_kernel(const T* __rest
             const int e = __ffs(mask) - 1;
             list[at++] = X::key(X::at(cur[v], e), base - lo + (v * kThreads + tid) * VEC + e);
           }
+          if (at > kKeep) full = batch;
         }
     __syncthreads();
-    const int n = count;
-    if (n > kKeep) {                     // (the same in all threads)
-      const int kept = thin_out(list, n, a.N, scratch, low, &left);
+    // Whether this batch filled the list beyond kKeep, the same in all threads: a fast warp may be at the next batch
+    // already when a late one looks here, and what it writes (to count, or the next batch's number to full) then says
+    // "not this one" as well; where it is this one, no warp leaves before all have looked.
+    if (full == batch) {
+      const int kept = thin_out(list, count, a.N, scratch, low, &left);
       __syncthreads();
       // what is left are N at least, and they bound those to come
       const uint32_t mine = tid < kept ? ordered(X::logit(list[tid])) : ~0u;

@@ -25,7 +25,8 @@ def want_of(x, scores, N):
         found = []
         for w in range(W):
             y = x[r, w].double()
-            y = y - torch.logsumexp(y, 0)
+            y = y - y.max()
+            y = y - y.exp().sum().log()
             v, at = torch.sort(y, descending=True, stable=True)
             found += [(-(float(scores[r, w]) + a), w, b) for a, b in zip(v[:N0].tolist(), at[:N0].tolist()) if a > -INF]
         found = sorted(found)[:N]
@@ -72,4 +73,122 @@ def test_candidates_in_many_rounds(hyb, devstatus, Rn, W, N, V, dt):
     c.s.fill_(-1.5)
     x[:] = x[:, :1].clone()                      # equal beams: every total is there W times
     c.check(again=50)
+    assert devstatus() == (0, 0)
+
+
+# -------------------------------------------------------------- several batches of a slice
+def ranked(x, scores, N):
+    """Per request the candidates in the exact order, N and those whose totals lie next to the N-th: (total, beam, token).
+    Each row's sum is a reduction of its own: within one over all rows the order of the terms, and so the last bit, goes
+    by where a row lies, and equal rows would not tie. The maximum is taken off first: beside logits of 1e30 the log of
+    a sum is lost in 64 bits too."""
+    res = []
+    for r in range(x.shape[0]):
+        y = x[r].double()
+        y = y - y.amax(-1, keepdim=True)
+        y = y - torch.stack([row.clone().exp().sum().log() for row in y])[:, None]
+        v, at = torch.sort(y, dim=-1, descending=True, stable=True)
+        v, at, found = v[:, :N + 8].tolist(), at[:, :N + 8].tolist(), []
+        for w, s in enumerate(scores[r].tolist()):
+            found += [(-(s + a), w, b) for a, b in zip(v[w], at[w]) if a > -INF]
+        res.append([(-t, w, b) for t, w, b in sorted(found)[:N + 8 * len(v)]])
+    return res
+
+
+def check_order(got, ref, N, what=""):
+    """The sums over the vocabulary are of 32-bit terms, each total off by 2^-18 at most (beam_ref), the same in all of a
+    beam's. So two beams' candidates may change places where their exact totals are nearer than twice that, but not where
+    they are equal (equal rows have equal sums), and a beam's own never."""
+    lim = 2.0 ** -18
+    for scores, parents, tokens, exact in zip(*(t.tolist() for t in got[:3]), ref):
+        assert len(exact) >= N
+        total = {(w, v): t for t, w, v in exact}
+        mine = list(zip(parents, tokens))
+        assert len(set(mine)) == N, what
+        for i, (pair, s) in enumerate(zip(mine, scores)):
+            assert pair in total, (what, i, pair)
+            t = total[pair]
+            assert abs(s - t) <= lim + R.U * abs(t), (what, i, s, t)
+            if pair != exact[i][1:]:
+                assert 0 < abs(t - exact[i][0]) <= 2 * lim, (what, i, pair, exact[i])
+        for w in set(parents):
+            seq = [v for p, v in mine if p == w]
+            assert seq == [v for _, p, v in exact if p == w][:len(seq)], (what, w)
+    assert (got[3] == 0).all(), what
+
+
+KINDS = ["random", "constant", "few values", "rising", "falling", "one block", "zeros of both signs", "equal beams", "large", "far apart", "late best"]
+
+
+def logits_of(kind, Rn, W, V, dt):
+    x = rnd(5, Rn, W, V)
+    s = -rnd(6, Rn, W).abs()
+    at = torch.arange(V, device="cuda")
+    if kind == "constant":
+        x = torch.full_like(x, -2.5)
+    elif kind == "few values":
+        x = (x * 1.5).round()
+    elif kind == "rising":
+        x = (at / V * 9).expand(Rn, W, V)
+    elif kind == "falling":
+        x = (-at / V * 9).expand(Rn, W, V)
+    elif kind == "one block":
+        x = torch.where((at >= V // 2) & (at < V // 2 + 200), 8 + x, x)
+    elif kind == "zeros of both signs":
+        x = torch.where(x > 0, 0.0, -0.0)
+    elif kind == "equal beams":
+        x, s = x[:, :1].expand(Rn, W, V), s[:, :1].expand(Rn, W).contiguous()
+    elif kind == "large":
+        x = x * 1e30
+    elif kind == "far apart":
+        x = x * 100
+    elif kind == "late best":                        # rising steps, each tied over most of a batch
+        x = (at // 3000).float().expand(Rn, W, V)
+    return x.to(dt).contiguous(), s
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Rn,W,batches", [(19, 4, 2), (38, 3, 3), (76, 4, 8)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_slices_of_several_batches(hyb, devstatus, kind, Rn, W, batches, dt):
+    """Slices of 2, 3 and 8 batches (fp32: twice as many): what one batch leaves bounds the next, lists are carried
+    over and thinned out, ties cross batches."""
+    V = 130001
+    x, s = logits_of(kind, Rn, W, V, dt)
+    ref = ranked(x, s, 128)
+    for N in (8, 25, 128):
+        c = Select(hyb, x, s, N)
+        if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+            assert c.slices == -(-16 // batches)
+        got = c.call()
+        check_order(got, ref, N, f"{kind}, {N} kept")
+        for _ in range(5):
+            assert all(torch.equal(a, b) for a, b in zip(got, c.call())), (kind, N)
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt,V", [(torch.float32, 1100001), (torch.bfloat16, 2200003)])
+@pytest.mark.parametrize("kind", ["random", "constant", "rising", "equal beams"])
+def test_more_than_256_slices(hyb, devstatus, kind, dt, V):
+    x, s = logits_of(kind, 1, 2, V, dt)
+    ref = ranked(x, s, 128)
+    for N in (4, 128):
+        c = Select(hyb, x, s, N)
+        assert c.slices > 256
+        check_order(c.call(), ref, N, f"{kind}, {N} kept")
+    assert devstatus() == (0, 0)
+
+
+def test_the_largest_vocabulary(hyb, devstatus):
+    """Two beams of 2^30 - 1 tokens, the second row off the 16-byte boundary: all equal but a few."""
+    V, N = (1 << 30) - 1, 6
+    x = torch.zeros(2, V, device="cuda", dtype=torch.bfloat16)
+    x[0, 12345], x[0, V - 1], x[1, V - 1], x[1, V - 2] = 5.0, 4.0, 4.5, 4.5
+    c = Select(hyb, x.view(1, 2, V), torch.tensor([[-1.0, -1.25]], device="cuda"), N)
+    got = c.call()
+    base = [-1 - math.log(V - 2 + math.exp(5) + math.exp(4)), -1.25 - math.log(V - 2 + 2 * math.exp(4.5))]
+    want = [(0, 12345, 5.0), (1, V - 2, 4.5), (1, V - 1, 4.5), (0, V - 1, 4.0), (0, 0, 0.0), (0, 1, 0.0)]
+    assert got[1][0].tolist() == [p for p, _, _ in want] and got[2][0].tolist() == [v for _, v, _ in want]
+    for g, (p, _, y) in zip(got[0][0].tolist(), want):
+        assert abs(g - (base[p] + y)) <= 2.0 ** -18 + R.U * abs(base[p] + y)
     assert devstatus() == (0, 0)
