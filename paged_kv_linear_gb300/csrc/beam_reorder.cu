@@ -150,7 +150,7 @@ beam_copy_kernel(const __grid_constant__ Layers layers, const int32_t* __restric
   }
   const int P = pre ? max(pre[r], 0) : 0, n = lens[src];
   if ((int64_t)n - P > max_suffix || n > min((int64_t)MB * bs, (int64_t)1 << 30)) {
-    if (says && blockIdx.z == 0) flag(status, HYB_DEVERR_BAD_LENGTH);
+    if (says) flag(status, HYB_DEVERR_BAD_LENGTH);
     return;
   }
   // the next token is number n: a window of W ending there starts at n + 1 - W

@@ -345,6 +345,22 @@ def test_reorder_bad_values_are_flagged_and_left_out(hyb, devstatus):
     assert all(torch.equal(a, b) for a, b in zip(before, s.pools[0])) and (s.lens_d[:3] == lens[0]).all()
 
 
+@pytest.mark.parametrize("types", [[LINEAR, FULL], [LINEAR, LINEAR, SLIDING], [FULL, LINEAR], ([LINEAR] + [FULL] * 95) * 2])
+def test_reorder_flags_a_long_parent_in_any_layer(hyb, devstatus, types):
+    """A parent longer than the bound, or than its table, is flagged wherever a launch's Full layers stand."""
+    for most, n in ((29, 50), (30, 16 * 40)):
+        s = Stack(hyb, types, 2, 3, 20, 30, 1, 16, state=64, seed=4)
+        s.lens_d[0] = n
+        p = [[0, 0, 0], [0, 1, 2]]
+        lens = s.lens_d.clone()
+        before = [[x.clone() for x in pool] for pool, t in zip(s.pools, types) if t != LINEAR]
+        hyb.check(s.call(on_gpu(p), most=most))
+        assert devstatus() == (hyb.HYB_ERR_DEVICE_CHECK, hyb.HYB_DEVERR_BAD_LENGTH)
+        after = [pool for pool, t in zip(s.pools, types) if t != LINEAR]
+        assert all(torch.equal(a, b) for x, y in zip(before, after) for a, b in zip(x, y))
+        assert (s.lens_d[:3] == n).all() and torch.equal(s.lens_d[3:], lens[3:])
+
+
 def test_reorder_of_odd_lengths_copies_nothing(hyb, devstatus):
     """A parent without tokens behind the prefix, shorter than it, or of a length below zero."""
     for n in (20, 7, 0, -1, -2 ** 31):
