@@ -426,8 +426,9 @@ hyb_status_t hyb_qk_norm_rope_append(void* q_out, void* k_out, const void* q, co
  * hold the prefix even where that request is shorter; those of p >= P through row b's own. A
  * prefix may end inside a block: the tokens behind it are then the row's own, in the row's own
  * block. A request with n < P sees its first n tokens of the prefix, one with n <= 0 gets
- * zeros. d->window = W > 0 restricts p to n - W <= p < n; table entries of blocks that no
- * request of the group (of the prefix) or not the request (of its own part) sees are not read.
+ * zeros. d->window = W > 0 restricts p to n - W <= p < n. Table entries of blocks that no
+ * request of the group (of the prefix) or not the request (of its own part) sees, behind the
+ * longest request, before all windows or between them, may hold anything.
  *   q, out      [B][num_q_heads][D] of d->dtype; caches as for hyb_paged_attn_decode
  *   cu_groups   int32 [G+1], prefix_lens int32 [G]. Rows that belong to no group are left as
  *               they were. Groups of one request, empty groups and P = 0 are fine; cu_groups does

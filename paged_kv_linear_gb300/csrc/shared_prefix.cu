@@ -200,17 +200,14 @@ prefix_tile_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
   const int rows = min(kTileRows, (b1 - b0) * rep - row0);
   int k0 = part * a.Lp, k1 = min(P, k0 + a.Lp);
   if (rows <= 0 || k0 >= k1) return;
-  // keys that the warp's rows see, and of the tile's rows the first and the last
-  int lo[RW], hi[RW], min_lo = INT32_MAX, max_hi = 0;
-  for (int r = lane; r < rows; r += 32) {
-    const RowSpan x = row_span(a, a.lens[b0 + (row0 + r) / rep], 0, P);
-    if (min(P, x.n) > x.lo) {
-      min_lo = min(min_lo, x.lo);
-      max_hi = max(max_hi, min(P, x.n));
-    }
-  }
-  k0 = max(k0, __reduce_min_sync(0xffffffffu, min_lo));
-  k1 = min(k1, __reduce_max_sync(0xffffffffu, max_hi));
+  // keys that the warp's rows see, and those of the tile's requests
+  int lo[RW], hi[RW];
+  const int q0 = b0 + row0 / rep, q1 = b0 + (row0 + rows - 1) / rep + 1;
+  Hull seen;
+  for (int b = q0 + lane; b < q1; b += 32) seen.add(a, a.lens[b], P);
+  seen.join();
+  k0 = max(k0, seen.lo);
+  k1 = min(k1, seen.hi);
   if (k0 >= k1) return;                        // (the same in every warp)
 #pragma unroll
   for (int r = 0; r < RW; ++r) {
@@ -247,8 +244,9 @@ prefix_tile_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* _
     for (int n = 0; n < N; ++n) {
       const int e = tid + n * 128, k = e / S::VPR, c = e % S::VPR, p = k0 + t * kTileKeys + k;
       if (e >= kTileKeys * S::VPR) break;
-      const bool ok = pb[n] >= 0 && pb[n] < a.NB;
-      if (p < k1 && !ok && c == 0) flag(a.status, HYB_DEVERR_BAD_BLOCK);
+      const bool want = p < k1 && (!seen.gaps || any_sees(a, q0, q1, P, p, p + 1));
+      const bool ok = want && pb[n] >= 0 && pb[n] < a.NB;
+      if (want && !ok && c == 0) flag(a.status, HYB_DEVERR_BAD_BLOCK);
       const int64_t at = ok ? (((int64_t)pb[n] * a.Hk + hk) * bs + p % bs) * D + c * VEC : 0;
       cp16(ks + k * S::KP + c * VEC, kc + at, ok);
       cp16(vs + k * D + c * VEC, vc + at, ok);
@@ -450,7 +448,7 @@ PrefixPlan plan_prefix(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t*
   } else if (mma) {
     const int64_t nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, units = std::max<int64_t>(1, heads * ((rows + 16 * nt - 1) / (16 * nt)));
     const int64_t slots = (int64_t)sms * (D == 256 ? 1 : 3);
-    r.Lp = round16(std::min<int64_t>(1536, std::max<int64_t>(nt == 1 ? 512 : 256, P * units / slots)));
+    r.Lp = round16(std::min<int64_t>(kMmaMaxPart, std::max<int64_t>(nt == 1 ? 512 : 256, P * units / slots)));
   } else if (use_tiles(rows)) {
     // one wave of the CTAs that shared memory holds, if that leaves parts of 128 to 512 keys
     const int es = d->dtype == HYB_BF16 ? 2 : 4, smem = kTileKeys * (4 * D * es + 32) + kTileRows * (D + kTileKeys) * 4 + 256;

@@ -29,6 +29,7 @@ struct PrefixArgs {
   unsigned* status;
 };
 
+constexpr int kMmaMaxPart = 1536;          // keys of a prefix part on warp matrix instructions, at most
 bool prefix_mma_supported(int dtype, int D);
 // prefix: the prefixes' parts too, not only those of the rows' own tokens; early: behind launch_prefix_tc of
 // the same call
@@ -71,6 +72,35 @@ __device__ __forceinline__ RowSpan row_span(const PrefixArgs& a, int n, int firs
   r.lo = (a.window > 0 && n > a.window) ? n - a.window : 0;
   if (n - P > a.max_suffix || n > a.cap) r.n = -1;
   return r;
+}
+
+// The keys of a prefix that some requests see: [lo, hi) from the first to the last of them. With a window, one request
+// that ends early in the prefix and one that goes on behind it leave keys between that neither sees (gaps): then
+// any_sees tells. What none sees is neither fetched nor looked at, whatever its table entries hold.
+struct Hull {
+  int lo = INT32_MAX, hi = 0;
+  bool gaps = false;
+  __device__ __forceinline__ void add(const PrefixArgs& a, int len, int P) {
+    const RowSpan x = row_span(a, len, 0, P);
+    const int end = min(P, x.n);
+    if (end <= x.lo) return;
+    lo = min(lo, x.lo);
+    hi = max(hi, end);
+    gaps |= end < P && a.window > 0;
+  }
+  __device__ __forceinline__ void join() {                     // the whole warp's
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    gaps = __any_sync(0xffffffffu, gaps);
+  }
+};
+// Whether one of requests [b0, b1) sees one of the prefix's keys [k0, k1)
+__device__ __forceinline__ bool any_sees(const PrefixArgs& a, int b0, int b1, int P, int k0, int k1) {
+  for (int b = b0; b < b1; ++b) {
+    const RowSpan x = row_span(a, a.lens[b], 0, P);
+    if (max(x.lo, k0) < min(min(P, x.n), k1)) return true;
+  }
+  return false;
 }
 
 // Whole warp: row b's keys (n < 0: left out); bad: whether that is for its length. Group bounds, prefixes

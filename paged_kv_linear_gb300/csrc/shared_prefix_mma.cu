@@ -33,6 +33,9 @@ constexpr int kWarps = 4;
 constexpr float kRescale = 8.f;                // log2: the largest p before the base moves
 constexpr float kNoBase = -3.3e38f;            // the base of a row that has seen no key
 
+constexpr int kPieces = kMmaMaxPart / kBlockSize;
+static_assert(kPieces % 32 == 0, "a part's pieces are looked up by whole warps, in stages of up to four");
+
 template <int D, int NT>
 struct MmaShape {
   static constexpr int KG = kWarps / NT;       // key groups: rings of stages, each read by NT warps
@@ -46,8 +49,10 @@ struct MmaShape {
   static constexpr int JOIN = kWarps * 16 * PITCH * 4;
   static constexpr int BODY = KG > 1 && JOIN > RING ? JOIN : RING;
   static constexpr int BARS = BODY;            // full, empty: u64 [KG][NST]; have: int [KG][NST]
-  static constexpr int ROWS = BARS + KG * NST * 20 + 16;         // float2 ml[64]
-  static constexpr int SMEM = ROWS + 64 * 8 + 1024;             // 1 KiB of alignment slack
+  static constexpr int ROWS = (BARS + KG * NST * 20 + 15) / 16 * 16;   // float2 ml[64]
+  static constexpr int PIECES = ROWS + 64 * 8; // int [kPieces]
+  static constexpr int UNIT = PIECES + kPieces * 4;              // Unit
+  static constexpr int SMEM = UNIT + 64 + 1024;                 // 1 KiB of alignment slack
 };
 
 template <int D>
@@ -64,6 +69,7 @@ struct Unit {
   const int32_t* table;
   int first, hk, row0, rows, part, k0, k1;
 };
+static_assert(sizeof(Unit) <= 64, "what MmaShape sets aside");
 
 // four 8 x 8 matrices at addr + OFF (an immediate), as they are or transposed
 template <int OFF>
@@ -243,48 +249,44 @@ struct WarpTile {
   }
 };
 
-// Fills a ring of NST stages of KP pieces with every step-th stage of a part, by a whole warp.
-template <int D, int NST, int KP>
+// The pool row of 16-token piece `sub` of a sequence, block id pb; -1, and flagged, for a bad block
+__device__ __forceinline__ int pool_row(const PrefixArgs& a, int pb, int hk, int sub) {
+  if (pb < 0 || pb >= a.NB) {
+    flag(a.status, HYB_DEVERR_BAD_BLOCK);
+    return -1;
+  }
+  return ((pb * a.Hk + hk) << (4 + a.rsh)) + ((sub & ((1 << a.rsh) - 1)) << 4);
+}
+
+// Fills a ring of NST pieces with pieces [sub0, sub0 + subs) of a sequence, by a whole warp.
+template <int D, int NST>
 struct Fetch {
-  static constexpr int TILE = 16 * D * 2, AHEAD = 32 / KP;     // stages whose rows are looked up together
+  static constexpr int TILE = 16 * D * 2;
   const int32_t* table;
   uint8_t* ring;
   uint64_t* full;
-  int hk, sub0, subs, first, step, count;    // pieces [sub0, sub0 + subs) of the sequence; stages first, first + step, ..
-  int y, next;                               // pool rows of AHEAD stages' pieces, one a lane; the stage to ask for next
+  int hk, sub0, subs;
+  int y, next;                               // pool rows of 32 pieces, one a lane; the piece to ask for next
 
-  // asks for the next stage; which of its pieces there are (a bad block's is left out) is returned, and
-  // written to have[stage] for other warps, before the arrival that they wait for
-  __device__ __forceinline__ unsigned issue(const PrefixArgs& a, const CUtensorMap* tk, const CUtensorMap* tv,
-                                            int* have = nullptr) {
+  // asks for the next piece; returned: whether there is one (a bad block's is left out)
+  __device__ __forceinline__ bool issue(const PrefixArgs& a, const CUtensorMap* tk, const CUtensorMap* tv) {
     const int lane = threadIdx.x & 31;
-    if (next % AHEAD == 0) {
+    if (next % 32 == 0) {
       y = -1;
-      const int sub = (first + (next + lane / KP) * step) * KP + lane % KP;
-      if (next + lane / KP < count && sub < subs) {
-        const int pb = table[(sub0 + sub) >> a.rsh];
-        if (pb < 0 || pb >= a.NB) flag(a.status, HYB_DEVERR_BAD_BLOCK);
-        else y = ((pb * a.Hk + hk) << (4 + a.rsh)) + (((sub0 + sub) & ((1 << a.rsh) - 1)) << 4);
-      }
+      const int sub = sub0 + next + lane;
+      if (next + lane < subs) y = pool_row(a, table[sub >> a.rsh], hk, sub);
     }
-    const int st = next % NST;
-    const unsigned mask = (__ballot_sync(0xffffffffu, y >= 0) >> (next % AHEAD * KP)) & ((1u << KP) - 1);
-    if (lane == 0) {
-      if (have) have[st] = mask;
-      if (mask) mbar_expect_tx(&full[st], __popc(mask) * 2 * TILE);
-      else mbar_arrive(&full[st]);
-    }
-#pragma unroll
-    for (int j = 0; j < KP; ++j) {
-      const int row = __shfl_sync(0xffffffffu, y, next % AHEAD * KP + j);
-      if (row >= 0 && lane == 0) {
-        uint8_t* dst = ring + (st * KP + j) * 2 * TILE;
-        tma_load_3d(dst, tk, 0, row, 0, &full[st]);
-        tma_load_3d(dst + TILE, tv, 0, row, 0, &full[st]);
-      }
+    const int st = next % NST, row = __shfl_sync(0xffffffffu, y, next % 32);
+    if (row >= 0 && lane == 0) {
+      uint8_t* dst = ring + st * 2 * TILE;
+      mbar_expect_tx(&full[st], 2 * TILE);
+      tma_load_3d(dst, tk, 0, row, 0, &full[st]);
+      tma_load_3d(dst + TILE, tv, 0, row, 0, &full[st]);
+    } else if (lane == 0) {
+      mbar_arrive(&full[st]);
     }
     ++next;
-    return mask;
+    return row >= 0;
   }
 };
 
@@ -312,11 +314,11 @@ __device__ __forceinline__ void attend_own(const CUtensorMap* tk, const CUtensor
   w.start(r0 < u.rows ? q + (row + r0) * D : nullptr, r1 < u.rows ? q + (row + r1) * D : nullptr, a.q_sign);
   w.lo0 = w.lo1 = k0;
   w.hi0 = w.hi1 = k1;
-  Fetch<D, NST, 1> f{u.table, ring, full, u.hk, u.k0 / kBlockSize, np, 0, 1, np, -1, 0};
+  Fetch<D, NST> f{u.table, ring, full, u.hk, u.k0 / kBlockSize, np, -1, 0};
   unsigned have = 0;                     // of the pieces in the ring, by stage
   auto issue = [&]() {
     const int st = f.next % NST;
-    have = (have & ~(1u << st)) | f.issue(a, tk, tv) << st;
+    have = (have & ~(1u << st)) | (unsigned)f.issue(a, tk, tv) << st;
   };
   while (f.next < NST && f.next < np) issue();
   for (int i = 0; i < np; ++i) {
@@ -357,8 +359,13 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
   uint64_t* empty = full + KG * NST;
   int* have_s = reinterpret_cast<int*>(empty + KG * NST);
   float2* red_ml = reinterpret_cast<float2*>(sm + S::ROWS);
+  int* pieces = reinterpret_cast<int*>(sm + S::PIECES);         // pool rows of the part's pieces; -1: left out
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rep = a.Hq / a.Hk;
+  // with four row tiles registers are short in the loop: the end reads the unit here (64 requests 85.7 -> 85.0 us; with
+  // one row tile it costs 0.5 of 18)
+  Unit* const us = reinterpret_cast<Unit*>(sm + S::UNIT);
   if (tid == 96) {
+    if (NT == 4) *us = u;
     for (int i = 0; i < KG * NST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], NT);
@@ -366,25 +373,21 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
     fence_mbar_init();
   }
   int k0 = u.k0, k1 = u.k1;
-  if (a.window > 0) {                          // only keys that one of the rows sees (otherwise: all but always all)
-    int max_hi = 0, min_lo = INT32_MAX;
-    for (int r = lane; r < u.rows; r += 32) {
-      const RowSpan x = row_span(a, a.lens[u.first + (u.row0 + r) / rep], 0, P);
-      if (min(P, x.n) > x.lo) {
-        max_hi = max(max_hi, min(P, x.n));
-        min_lo = min(min_lo, x.lo);
-      }
-    }
-    k0 = max(k0, __reduce_min_sync(0xffffffffu, min_lo));
-    k1 = min(k1, __reduce_max_sync(0xffffffffu, max_hi));
-    if (k0 >= k1) return;                      // (the same in every warp)
-  }
+  const int b0 = u.first + u.row0 / rep, b1 = u.first + (u.row0 + u.rows - 1) / rep + 1;
+  Hull seen;                                   // only keys that one of the rows sees
+  auto see = [&]() {
+    for (int b = b0 + lane; b < b1; b += 32) seen.add(a, a.lens[b], P);
+    seen.join();
+    k0 = max(k0, seen.lo);
+    k1 = min(k1, seen.hi);
+    return k0 < k1;                            // (the same in every warp)
+  };
+  if (a.window > 0 && !see()) return;
   __syncthreads();
-  const int kb = k0 & ~(kBlockSize - 1), np = (k1 - kb + kBlockSize - 1) / kBlockSize;
+  const int kb = k0 & ~(kBlockSize - 1);
 
   // warp t = 0 of a key group fills its ring: stage n + NST - LAG once all have done with stage n - LAG
   const int t = warp % NT, kg = warp / NT;     // row tile, key group
-  const int ns = (np + KP - 1) / KP, mine = ns > kg ? (ns - kg + KG - 1) / KG : 0;   // stages, this ring's
   uint8_t* ring = sm + kg * NST * KP * 2 * TILE;
   full += kg * NST;
   empty += kg * NST;
@@ -399,13 +402,49 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
     const int i = u.row0 + r1;
     q1 = q + ((int64_t)(u.first + i / rep) * a.Hq + u.hk * rep + i % rep) * D;
   }
-  // The rows' lengths, the queries and (in issue) the block ids: one round trip, so all are asked for first.
+  // The requests' lengths and the block ids: one round trip, so both are asked for first; the queries come while the
+  // first keys do. (Without a window the rows see all keys, or all up to the longest one's last, which cuts the part
+  // short only then.)
+  int ids[kPieces / 32];
+#pragma unroll
+  for (int i = 0; i < kPieces / 32; ++i) {
+    const int p = kb + (i * 32 + lane) * kBlockSize;
+    ids[i] = t == 0 && p < k1 ? u.table[p / kBlockSize >> a.rsh] : -1;
+  }
+  if (a.window == 0 && !see()) return;
+  const int ns = (k1 - kb + KP * kBlockSize - 1) / (KP * kBlockSize), mine = ns > kg ? (ns - kg + KG - 1) / KG : 0;   // stages, this ring's
+  if (t == 0) {
+#pragma unroll
+    for (int i = 0; i < kPieces / 32; ++i) {                   // (the same of every ring)
+      const int p = kb + (i * 32 + lane) * kBlockSize;
+      const bool want = p < k1 && (!seen.gaps || any_sees(a, b0, b1, P, p, p + kBlockSize));
+      pieces[i * 32 + lane] = want ? pool_row(a, ids[i], u.hk, p / kBlockSize) : -1;
+    }
+    __syncwarp();
+  }
+  // lane 0 of the warp that fills the ring: asks for the ring's stage n; which of its pieces there are goes to
+  // have_s, before the arrival that the readers wait for
+  auto issue = [&](int n) {
+    const int st = n % NST, *p = pieces + (kg + n * KG) * KP;
+    unsigned have = 0;
+#pragma unroll
+    for (int j = 0; j < KP; ++j) have |= (unsigned)(p[j] >= 0) << j;
+    have_s[st] = have;
+    if (have) mbar_expect_tx(&full[st], __popc(have) * 2 * TILE);
+    else mbar_arrive(&full[st]);
+#pragma unroll
+    for (int j = 0; j < KP; ++j)
+      if (p[j] >= 0) {
+        uint8_t* dst = ring + (st * KP + j) * 2 * TILE;
+        tma_load_3d(dst, tk, 0, p[j], 0, &full[st]);
+        tma_load_3d(dst + TILE, tv, 0, p[j], 0, &full[st]);
+      }
+  };
+  if (t == 0 && lane == 0)
+    for (int n = 0; n < min(NST, mine); ++n) issue(n);
   const int len0 = q0 ? a.lens[u.first + (u.row0 + r0) / rep] : 0, len1 = q1 ? a.lens[u.first + (u.row0 + r1) / rep] : 0;
   WarpTile<D> w;
   w.start(q0, q1, a.q_sign);
-  Fetch<D, NST, KP> f{u.table, ring, full, u.hk, kb / kBlockSize, np, kg, KG, mine, -1, 0};
-  if (t == 0)
-    while (f.next < NST && f.next < mine) f.issue(a, tk, tv, have_s);
   // keys that the lane's rows see, and those that all of the warp's rows do
   if (q0) {
     const RowSpan x = row_span(a, len0, 0, P);
@@ -428,16 +467,19 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
                           a.scale_log2);
     __syncwarp();
     if (NT > 1 && lane == 0) mbar_arrive(&empty[st]);
-    if (ok && t == 0 && n >= S::LAG && f.next < mine) {
-      const int m = n - S::LAG;                // f.next = m + NST
+    if (ok && t == 0 && n >= S::LAG && n - S::LAG + NST < mine) {
+      const int m = n - S::LAG;
       if (NT > 1) ok = __all_sync(0xffffffffu, mbar_wait_cycles(&empty[m % NST], (m / NST) & 1));
-      if (ok) f.issue(a, tk, tv, have_s);
+      if (ok && lane == 0) issue(m + NST);
+      __syncwarp();
     }
     if (!ok) {                                 // report, and let the copies in flight land
       if (lane == 0) {
         flag(a.status, HYB_DEVERR_TIMEOUT);
         if (t == 0)
-          for (int j = max(0, f.next - NST); j < f.next; ++j) mbar_wait_cycles(&full[j % NST], (j / NST) & 1, 200000000u);
+          // asked for so far: up to the stage NST behind the last that was done with
+          for (int j = max(0, n - S::LAG); j < min(mine, max(0, n - S::LAG) + NST); ++j)
+            mbar_wait_cycles(&full[j % NST], (j / NST) & 1, 200000000u);
       }
       break;
     }
@@ -446,15 +488,16 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
 
   // -------------------------------------------------------------------- the part's state
   const int parts = a.Sp + a.Ss;
+  const Unit& end = NT == 4 ? *us : u;
   auto slot = [&](int r) {                     // of tile row r
-    const int i = u.row0 + r;
-    return ((int64_t)(u.first + i / rep) * a.Hq + u.hk * rep + i % rep) * parts + u.part;
+    const int i = end.row0 + r, n = a.Hq / a.Hk;
+    return ((int64_t)(end.first + i / n) * a.Hq + end.hk * n + i % n) * parts + end.part;
   };
   if (KG == 1) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = half ? r1 : r0;
-      if (r >= u.rows) continue;
+      if (r >= end.rows) continue;
       const int64_t at = slot(r);
       if (quad == 0) a.ws_ml[at] = make_float2(w.m[half], w.l[half]);
 #pragma unroll
@@ -479,7 +522,7 @@ __device__ __forceinline__ void attend(const CUtensorMap* tk, const CUtensorMap*
   }
   __syncthreads();
   {
-    for (int r = warp; r < u.rows; r += kWarps) {
+    for (int r = warp; r < end.rows; r += kWarps) {
       float M = -INFINITY, L = 0.f, x[KG];
 #pragma unroll
       for (int k = 0; k < KG; ++k) M = fmaxf(M, red_ml[k * NT * 16 + r].x);

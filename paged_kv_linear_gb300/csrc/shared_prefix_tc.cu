@@ -73,6 +73,9 @@ __device__ __forceinline__ void zero_v_rows(uint8_t* tile, int r0, int r1, int l
 }
 
 // grid: (((group Hk + key head) Sp + part) pairs + pair of row tiles); tile_rows: rep x (128 / rep)
+// kGaps: with a window, the requests may leave keys between theirs (Hull). Without one they cannot, and the code for it
+// stays out: it costs 256 requests on 32768 tokens 3 to 5 us of 120 though it never runs.
+template <bool kGaps>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const PrefixArgs a, int pairs, int tile_rows) {
@@ -112,12 +115,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   }
   const int kb = k0 & ~(kBlockSize - 1), nloc = (k1 - kb + kBN - 1) / kBN;   // key tiles [kb + 128 j, ..)
   const int32_t* btrow = a.bt + (int64_t)b0 * a.MB;
-  // block id of 16-token piece s of the prefix; -1: none that may be read
-  auto block_of = [&](int s) {
-    if (s * kBlockSize >= k1) return -1;
-    const int pb = btrow[s >> a.rsh];
-    return pb >= 0 && pb < a.NB ? pb : -1;
-  };
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -137,6 +134,15 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
     info.part = part;
     info.head0 = hk * rep;
     info.two = two;
+  }
+
+  // What none of the rows' requests [q0, q1) sees is not loaded, whatever the table holds there; looked up while the
+  // barriers and TMEM are set up.
+  const int q0 = b0 + row0 / rep, q1 = b0 + (min(row0 + 2 * tile_rows, cnt) - 1) / rep + 1;
+  Hull seen;
+  if (warp == kWarpTmaK || warp == kWarpTmaV) {
+    for (int b = q0 + lane; b < q1; b += 32) seen.add(a, a.lens[b], P);
+    seen.join();
   }
 
   if (warp == kWarpMma) {
@@ -183,11 +189,15 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       }
       // pool rows of 4 tiles' pieces, one per lane, looked up 4 tiles ahead; L2 is asked for the pieces then, each
       // by one of the CTAs that read the same keys: the rings are too short for memory's latency
+      const int kend = min(k1, seen.hi);
       auto rows_of = [&](int j) {
         const int s = kb / kBlockSize + j * 8 + lane;
-        const int pb = block_of(s);
-        if (isk && pb < 0 && s * kBlockSize < k1) flag(a.status, HYB_DEVERR_BAD_BLOCK);
-        return pb < 0 ? -1 : ((pb * a.Hk + hk) << (4 + a.rsh)) + ((s & ((1 << a.rsh) - 1)) << 4);
+        if (s * kBlockSize >= kend) return -1;
+        if (kGaps && seen.gaps && !any_sees(a, q0, q1, P, s * kBlockSize, (s + 1) * kBlockSize)) return -1;
+        const int pb = btrow[s >> a.rsh];
+        const bool there = pb >= 0 && pb < a.NB;
+        if (isk && !there) flag(a.status, HYB_DEVERR_BAD_BLOCK);
+        return there ? ((pb * a.Hk + hk) << (4 + a.rsh)) + ((s & ((1 << a.rsh) - 1)) << 4) : -1;
       };
       int ids = -1, ahead = rows_of(0);
       for (int jj = 0; jj < nloc; ++jj) {
@@ -495,9 +505,10 @@ cudaError_t launch_prefix_tc(const void* q, const void* kc, const void* vc, cons
   if (!encode_tmap_bf16(&mq, q, 3, qdims, qstr, qbox) || !encode_tmap_bf16(&mk, kc, 2, cdims, cstr, cbox) ||
       !encode_tmap_bf16(&mv, vc, 2, cdims, cstr, cbox))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem((const void*)prefix_tc_kernel, kSmem);
+  const auto kernel = a.window > 0 ? prefix_tc_kernel<true> : prefix_tc_kernel<false>;
+  cudaError_t e = set_smem((const void*)kernel, kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(prefix_tc_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmem, s, mq, mk, mv, a, (int)pairs, tile_rows);
+  e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), kSmem, s, mq, mk, mv, a, (int)pairs, tile_rows);
   count_launch();
   return e;
 }
