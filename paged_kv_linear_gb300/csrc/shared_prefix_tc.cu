@@ -73,9 +73,9 @@ __device__ __forceinline__ void zero_v_rows(uint8_t* tile, int r0, int r1, int l
 }
 
 // grid: (((group Hk + key head) Sp + part) pairs + pair of row tiles); tile_rows: rep x (128 / rep)
-// kGaps: with a window, the requests may leave keys between theirs (Hull). Without one they cannot, and the code for it
-// stays out: it costs 256 requests on 32768 tokens 3 to 5 us of 120 though it never runs.
-template <bool kGaps>
+// kWindow: with a window, the requests' keys may begin inside a piece and leave gaps (Hull). Without one they cannot, and
+// the code for it stays out: it costs 256 requests on 32768 tokens 3 to 5 us of 120 though it never runs.
+template <bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const PrefixArgs a, int pairs, int tile_rows) {
@@ -193,7 +193,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       auto rows_of = [&](int j) {
         const int s = kb / kBlockSize + j * 8 + lane;
         if (s * kBlockSize >= kend) return -1;
-        if (kGaps && seen.gaps && !any_sees(a, q0, q1, P, s * kBlockSize, (s + 1) * kBlockSize)) return -1;
+        if (kWindow && seen.gaps && !any_sees(a, q0, q1, P, s * kBlockSize, (s + 1) * kBlockSize)) return -1;
         const int pb = btrow[s >> a.rsh];
         const bool there = pb >= 0 && pb < a.NB;
         if (isk && !there) flag(a.status, HYB_DEVERR_BAD_BLOCK);
@@ -225,7 +225,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           if (!ok) break;
         }
         // V rows that hold no key of the part must be finite (P is 0 there, but 0 x NaN is NaN): pieces that
-        // are not loaded are zeroed here, rows past k1 inside the last one by the landing warp
+        // are not loaded are zeroed here, rows before k0 and past k1 inside the first and last one by the landing warp
         if (!isk && nbox < 16) {
 #pragma unroll
           for (int bi = 0; bi < 8; ++bi)
@@ -265,6 +265,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         const int vtail = k1 - (kb + jj * kBN);
         if (vtail < kBN && (vtail & 15) != 0) {          // rows past k1 in the last piece
           zero_v_rows(sm + kOffV + (jj % kNV) * kTile, vtail, (vtail + 15) & ~15, lane);
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (kWindow && jj == 0 && kb < k0) {             // and before k0 in the first
+          zero_v_rows(sm + kOffV, 0, k0 - kb, lane);
           fence_async_smem();
           __syncwarp();
         }

@@ -70,3 +70,15 @@ def test_no_request_of_a_group_sees_its_prefix(hyb, devstatus, dt, D, Hq, Hk, ro
         assert release(c, 0, how) == 44 and release(c, 1, how) == (40 if window else 0)
         c.check(how)
     assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+@pytest.mark.parametrize("n,window", [(1005, 300), (1001, 990), (1015, 140), (1005, 5)])
+def test_tokens_before_every_window(hyb, dt, D, Hq, Hk, rows, n, window):
+    """What stands in a block before the first token that some request sees reaches none of them, NaN or not."""
+    c = Case(hyb, [(1000, [n - 1000] * rows), (60, [3])], Hq, Hk, D, dt, window=window, seed=rows)
+    lo = n - window
+    assert lo % 16 and lo <= 1000
+    for x in (c.kc, c.vc):
+        x[c.bt[0, lo // 16].long(), :, :lo % 16] = math.nan
+    c.check()
