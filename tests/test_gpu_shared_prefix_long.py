@@ -22,7 +22,7 @@ def release(c, group, how):
     P, rows = c.pre[group], range(c.cu[group], c.cu[group + 1])
     spans = [(max(0, c.lens[b] - c.window) if c.window else 0, min(P, c.lens[b])) for b in rows]
     n = 0
-    for i in range(P // c.bs + (P % c.bs > 0 and min(c.lens[b] for b in rows) < P)):
+    for i in range(P // c.bs + (P % c.bs > 0 and c.lens[rows[0]] <= P)):       # (a last block with the first request's own tokens is its own)
         if not any(max(lo, i * c.bs) < min(hi, (i + 1) * c.bs) for lo, hi in spans):
             c.bt[c.cu[group], i] = {"none": -1, "outside": c.NB, "someone else's": int(c.spare)}[how]
             n += 1
@@ -82,3 +82,191 @@ def test_tokens_before_every_window(hyb, dt, D, Hq, Hk, rows, n, window):
     for x in (c.kc, c.vc):
         x[c.bt[0, lo // 16].long(), :, :lo % 16] = math.nan
     c.check()
+
+
+# ------------------------------------------------ windows, bad input, peaks and order on every kernel
+@pytest.mark.parametrize("window", [1, 100, 512, 1000])
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+def test_windows_on_every_kernel(hyb, devstatus, dt, D, Hq, Hk, rows, window):
+    tails = [1 + (i * 37) % 600 for i in range(rows)]
+    c = Case(hyb, [(1100, tails), (37, [5, -20, 600]), (0, [700, 2])], Hq, Hk, D, dt, bs=32, window=window, seed=window, slack=40)
+    spare_block(c)
+    for g in range(3):
+        release(c, g, "someone else's")
+    for b, n in enumerate(c.lens):                   # a request's own blocks before its window
+        P = c.pre[sum(b >= x for x in c.cu[1:])]
+        first = b in c.cu
+        c.bt[b, -(-P // c.bs) if first else P // c.bs:max(0, n - window) // c.bs] = -1
+    c.check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+def test_bad_blocks_on_every_kernel(hyb, devstatus, dt, D, Hq, Hk, rows):
+    c = Case(hyb, [(900, [1 + (i * 7) % 50 for i in range(rows)]), (0, [40])], Hq, Hk, D, dt, seed=6)
+    for i, bad in ((0, c.NB), (7, -1), (8, -7), (30, c.NB + 5), (55, -1)):
+        c.bt[0, i] = bad
+    c.bt[rows, :] = -7                     # all of a request
+    hyb.check(c.call())
+    assert devstatus() == (hyb.HYB_ERR_DEVICE_CHECK, hyb.HYB_DEVERR_BAD_BLOCK)
+    c.bt[c.bt >= c.NB] = -1
+    R.check_attention(c.out, c.ref(), dt)
+    assert (c.out[rows] == 0).all()
+
+
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+def test_non_finite_values_on_every_kernel(hyb, dt, D, Hq, Hk, rows):
+    """A request's NaN in q or among its own tokens stays within it."""
+    c = Case(hyb, [(650, [20 + i % 50 for i in range(rows)]), (150, [30])], Hq, Hk, D, dt, seed=7)
+    clean = c.check().clone()
+    c.q[1, Hq - 1, 5] = math.nan
+    c.q[rows, 0, 1] = math.inf
+    c.vc[c.bt[2, 650 // 16 + 1].long(), 0, 3, 7] = math.inf          # token 659 of request 2
+    hyb.check(c.call())
+    assert c.out[1, Hq - 1].isnan().all() and torch.equal(c.out[1, :Hq - 1], clean[1, :Hq - 1])
+    assert not c.out[rows, 0].isfinite().any() and torch.equal(c.out[rows, 1:], clean[rows, 1:])
+    rep = Hq // Hk
+    assert not c.out[2, :rep, 7].isfinite().any() and torch.equal(c.out[2, rep:], clean[2, rep:])
+    rest = [b for b in range(rows) if b not in (1, 2)]
+    assert torch.equal(c.out[rest], clean[rest])
+
+
+def peaks(c, P, profile, rows):
+    """Scores that rise, fall or spike by dozens along the keys, for queries that look along the first."""
+    c.q[:] = c.q.sign() * 0.5
+    D = c.q.shape[-1]
+    along = c.q[0, 0].sign().float() / D ** 0.5
+    for b in range(rows):
+        n = c.lens[b]
+        at = torch.arange(0 if b == 0 else P, n, device="cuda")
+        z = {"rising": at / n, "falling": 1 - at / n, "spike": (at % 777 == 5).float(), "waves": torch.sin(at / 90.0)}[profile] * 40
+        c.kc[c.bt[b, at // c.bs].long(), :, at % c.bs] = (z[:, None] * along).to(c.dt)[:, None]
+
+
+@pytest.mark.parametrize("profile", ["rising", "falling", "spike", "waves"])
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+def test_peaked_scores_on_every_kernel(hyb, profile, dt, D, Hq, Hk, rows):
+    c = Case(hyb, [(1600, [3 + (i * 17) % 90 for i in range(rows)])], Hq, Hk, D, dt, seed=3)
+    peaks(c, 1600, profile, rows)
+    c.check(profile)
+
+
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+def test_order_on_every_kernel(hyb, devstatus, dt, D, Hq, Hk, rows):
+    """Calls one behind the other on one workspace, each fed by a kernel just before it; a captured call replayed with other
+    lengths; two streams with workspaces of their own."""
+    in_order(hyb, Case(hyb, [(900, [3 + (i * 7) % 40 for i in range(rows)]), (64, [3, 200])], Hq, Hk, D, dt, seed=10, slack=30))
+    assert devstatus() == (0, 0)
+
+
+def in_order(hyb, c):
+    want, outs = [], []
+    qs = [c.q.clone(), c.q.flip(0), c.q * 0.5, -c.q]
+    for q in qs:
+        c.q.copy_(q)
+        want.append(c.check().clone())
+    torch.cuda.synchronize()
+    for i in range(40):                              # the queries change behind the last call's back, the outputs move away
+        c.q.copy_(qs[i % 4])
+        hyb.check(c.call())
+        outs.append(c.out.clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % 4]) for i, o in enumerate(outs))
+    others = [torch.empty_like(c.out) for _ in range(4)]
+    c.q.copy_(qs[1])
+    for o in others:                                 # nothing between them but the workspace
+        hyb.check(c.call(o))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[1]) for o in others)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hyb.check(c.call())
+        hyb.check(c.call(others[0]))
+    c.dev[0][1] -= 2
+    c.lens[1] -= 2
+    c.out.fill_(7)
+    for _ in range(5):
+        graph.replay()
+    R.check_attention(c.out, c.ref(), c.dt)
+    assert torch.equal(c.out, others[0])
+    two = [torch.empty_like(c.out) for _ in range(2)]
+    spaces = [torch.empty_like(c.ws) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, o, w in zip(streams, two, spaces):
+            hyb.check(c.call(o, w, s))
+    torch.cuda.synchronize()
+    assert torch.equal(two[0], c.out) and torch.equal(two[1], c.out)
+
+
+# ------------------------------------------------ many key tiles in a CTA of the tensor-core kernel
+def tall(hyb, P, Hq, window=0, seed=1):
+    """A group of 70 requests on P tokens, 8 key heads, and 18 small ones: as many (group, key head) units as SMs, so that
+    each has one CTA, which walks all key tiles."""
+    c = Case(hyb, [(P, [1 + (i * 7) % 40 for i in range(70)])] + [(30 + 9 * g, [1 + g % 3] * (1 + g % 2)) for g in range(18)], Hq, 8, 128, seed=seed, window=window)
+    spare_block(c)
+    parts = c.n // (c.B * Hq * (128 * 4 + 8)) - 1    # one of the requests' own tokens
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        assert parts == 1
+    return c
+
+
+TALL = [(600, 8), (1152, 32), (1153, 24), (8190, 8), (8190, 32)]     # 5, 9, 10 and 64 key tiles; 1, 4 and 3 query heads a key head
+
+
+@pytest.mark.parametrize("P,Hq", TALL)
+def test_many_key_tiles(hyb, devstatus, P, Hq):
+    tall(hyb, P, Hq).check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("P,Hq", TALL)
+@pytest.mark.parametrize("share", [0.3, 0.97])
+def test_many_key_tiles_in_a_window(hyb, devstatus, P, Hq, share):
+    c = tall(hyb, P, Hq, window=int(P * share))
+    release(c, 0, "someone else's")
+    c.check()
+    # and some requests that end early: their windows lie before the others'
+    c = tall(hyb, P, Hq, window=int(P * share))
+    for b in range(0, 70, 5):
+        c.lens[b] = P // 3 + b
+    c.dev[0].copy_(torch.tensor(c.lens, dtype=torch.int32))
+    release(c, 0, "someone else's")
+    c.check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("P,Hq", TALL)
+def test_many_key_tiles_with_bad_blocks(hyb, devstatus, P, Hq):
+    c = tall(hyb, P, Hq)
+    clean = c.check().clone()
+    for i in range(3, P // 16, 11):
+        c.bt[0, i] = -1 if i % 2 else c.NB
+    hyb.check(c.call())
+    assert devstatus() == (hyb.HYB_ERR_DEVICE_CHECK, hyb.HYB_DEVERR_BAD_BLOCK)
+    c.bt[c.bt >= c.NB] = -1
+    R.check_attention(c.out, c.ref(), c.dt)
+    assert torch.equal(c.out[70:], clean[70:])
+
+
+@pytest.mark.parametrize("P,Hq", TALL)
+@pytest.mark.parametrize("profile", ["rising", "falling", "spike", "waves"])
+def test_many_key_tiles_of_peaked_scores(hyb, profile, P, Hq):
+    """The maximum moves in every tile, in one, or now and then: the sums are rescaled behind the second tile too."""
+    c = tall(hyb, P, Hq)
+    peaks(c, P, profile, 70)
+    c.check(profile)
+
+
+@pytest.mark.parametrize("P,Hq", TALL[1:4])
+def test_many_key_tiles_in_order(hyb, devstatus, P, Hq):
+    c = tall(hyb, P, Hq)
+    clean = c.check().clone()
+    q = c.q.clone()
+    c.q[1, Hq - 1, 5] = math.nan
+    hyb.check(c.call())
+    assert c.out[1, Hq - 1].isnan().all() and torch.equal(c.out[1, :Hq - 1], clean[1, :Hq - 1]) and torch.equal(c.out[2:], clean[2:])
+    c.q.copy_(q)
+    in_order(hyb, c)
+    assert devstatus() == (0, 0)
