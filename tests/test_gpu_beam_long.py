@@ -192,3 +192,110 @@ def test_the_largest_vocabulary(hyb, devstatus):
     for g, (p, _, y) in zip(got[0][0].tolist(), want):
         assert abs(g - (base[p] + y)) <= 2.0 ** -18 + R.U * abs(base[p] + y)
     assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["none before the end", "few here and there", "masked by the lowest value", "all masked by the lowest value"])
+def test_masks_over_several_batches(hyb, devstatus, kind, dt):
+    """Slices whose first batches hold nothing, or less than is kept."""
+    Rn, W, V = 76, 4, 130001
+    x, s = logits_of("random", Rn, W, V, dt)
+    if kind == "none before the end":
+        x[:, :, :V - 300] = -INF
+        x[3] = -INF
+        x[3, 2, V - 1] = 1.0
+    elif kind == "few here and there":
+        keep = torch.rand(V, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda") < 2e-3
+        x[:, :, ~keep] = -INF
+    else:
+        x[:, :, 100:] = torch.finfo(dt).min
+        if kind == "all masked by the lowest value":
+            x[:] = torch.finfo(dt).min
+    for N in (8, 128):
+        c = Select(hyb, x, s, N)
+        got = c.call()
+        if kind == "none before the end":            # request 3 has one candidate
+            assert got[1][3].tolist() == [2] + [-1] * (N - 1) and got[2][3].tolist() == [V - 1] + [-1] * (N - 1) and (got[0][3, 1:] == -INF).all()
+            got, x2, s2 = tuple(t[4:] for t in got), x[4:], s[4:]
+        else:
+            x2, s2 = x, s
+        check_order(got, ranked(x2, s2, N), N, f"{kind}, {N} kept")
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bad", [math.nan, INF])
+def test_bad_values_in_a_late_batch(hyb, devstatus, bad, dt):
+    Rn, W, V, N = 76, 4, 130001, 8
+    x, s = logits_of("random", Rn, W, V, dt)
+    c = Select(hyb, x, s, N)
+    clean = [t.clone() for t in c.call()]
+    x[5, 2, 60000] = x[70, 0, V - 1] = bad
+    got = c.call()
+    assert devstatus() == (hyb.HYB_ERR_DEVICE_CHECK, hyb.HYB_DEVERR_BAD_VALUE)
+    assert not (got[1][5] == 2).any() and not (got[1][70] == 0).any() and (got[1][[5, 70]] >= 0).all()
+    rest = [r for r in range(Rn) if r not in (5, 70)]
+    assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got, clean))
+    for r, w in ((5, 2), (70, 0)):
+        y = x[r:r + 1, [i for i in range(W) if i != w]]
+        ref = ranked(y, s[r:r + 1, [i for i in range(W) if i != w]], N)
+        ref = [[(t, p + (p >= w), v) for t, p, v in ref[0]]]
+        check_order(tuple(t[r:r + 1] for t in got), ref, N)
+
+
+def test_a_million_rows(hyb, devstatus):
+    Rn, V, N = 1 << 20, 3, 2
+    x, s = rnd(1, Rn, 1, V), -rnd(2, Rn, 1).abs()
+    c = Select(hyb, x, s, N)
+    got = c.call()
+    v, at = torch.sort(torch.log_softmax(x[:, 0].double(), -1), dim=-1, descending=True, stable=True)
+    want = v[:, :N] + s.double()
+    assert (got[1] == 0).all() and torch.equal(got[2].long(), at[:, :N])
+    assert ((got[0].double() - want).abs() <= 2.0 ** -18 + R.U * want.abs()).all()
+    assert devstatus() == (0, 0)
+
+
+# ----------------------------------------------------------------------------- reordering
+def test_reorders_back_to_back(hyb, devstatus):
+    """Each call begins on what the last one left, without the host in between; no prefixes given."""
+    from test_gpu_beam import FULL, LINEAR, SLIDING, Stack, on_gpu, parents_of
+    for types, pre in (([FULL, LINEAR, SLIDING], True), ([LINEAR, FULL], False)):
+        make = lambda: Stack(hyb, types, 5, 6, 37 if pre else 0, 50, seed=8)
+        s, t = make(), make()
+        kw = {} if pre else {"pre": None}
+        par = [parents_of(5, 6, i, ["random", "none", "same"][i % 3]) for i in range(8)]
+        dev = [on_gpu(p) for p in par]
+        for p in dev:
+            hyb.check(s.call(p, **kw))
+        for p in par:                                # one at a time, each checked
+            want = t.expect(p)
+            hyb.check(t.call(on_gpu(p), **kw))
+            t.check(p, want)
+        assert torch.equal(s.bt, t.bt) and torch.equal(s.lens_d, t.lens_d) and torch.equal(s.slots, t.slots)
+        for a, b in zip(s.pools, t.pools):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert devstatus() == (0, 0)
+
+
+def test_reorder_of_65528_beams(hyb, devstatus):
+    from test_gpu_beam import LINEAR, on_gpu, parents_of
+    Rn, W = 8191, 8
+    B = Rn * W
+    p = parents_of(Rn, W, 5, "none")
+    pool = torch.arange(4 * B, device="cuda", dtype=torch.float32).view(B, 4)
+    slots = torch.randperm(B, device="cuda").to(torch.int32)
+    lens = torch.arange(B, device="cuda", dtype=torch.int32)
+    old, want = slots.clone(), pool.clone()
+    rows, src, dst, wl = [], [], [], []
+    for r in range(Rn):
+        seat, copy = R.seats(p[r])
+        for i in range(W):
+            rows.append(r * W + seat[i])
+            wl.append(r * W + (p[r][i] if p[r][i] >= 0 else seat[i]))
+            if copy[i] is not None:
+                src.append(r * W + copy[i])
+                dst.append(r * W + seat[i])
+    want[old[dst].long()] = pool[old[src].long()]
+    hyb.check(hyb.hyb_beam_reorder(on_gpu(p), None, lens, None, slots, [LINEAR], 1, [hyb.layer_io(state_pool=pool, num_state_slots=B)], Rn, W, 0, 4, hyb.dims(1, 16, 1, 1), None, 0))
+    assert torch.equal(slots, old[rows]) and torch.equal(pool, want) and lens.tolist() == wl
+    assert devstatus() == (0, 0)

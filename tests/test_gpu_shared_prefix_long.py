@@ -270,3 +270,95 @@ def test_many_key_tiles_in_order(hyb, devstatus, P, Hq):
     c.q.copy_(q)
     in_order(hyb, c)
     assert devstatus() == (0, 0)
+
+
+# ------------------------------------------------ limits
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+def test_bounds_far_above_the_lengths(hyb, devstatus, dt, D, Hq, Hk, rows):
+    """Bounds as a captured step holds them: the whole batch in a group, prefixes and answers as long as the table."""
+    c = Case(hyb, [(300, [1 + i % 30 for i in range(rows)]), (5, [60]), (0, [0])], Hq, Hk, D, dt, seed=2, extra_rows=3)
+    wide = torch.full((c.B, 2048), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.bt.shape[1]] = c.bt
+    c.bt, c.d.max_blocks_per_seq = wide, 2048
+    c.p = hyb.prefix_dims(Hq, c.G, c.B, 2048 * 16, 2048 * 16)
+    c.n = hyb.hyb_paged_attn_decode_shared_prefix_workspace_size(c.B, c.p, c.d)
+    c.ws = torch.full((c.n // 4 + 4,), math.nan, device="cuda")
+    c.check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("Hq", [64, 65, 100, 127, 128, 129])
+def test_query_heads_about_a_row_tile(hyb, devstatus, Hq):
+    Case(hyb, [(400, [1, 40, 3]), (513, [9] * 2), (20, [-4])], Hq, 1, 128, seed=Hq).check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("D", [16, 64])
+def test_the_most_heads(hyb, devstatus, D):
+    H = 65535
+    Case(hyb, [(20, [1, 3])], H, H, D, seed=1).check()
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt,D", [(B16, 64), (F32, 64), (B16, 16)])
+def test_the_largest_batch(hyb, devstatus, dt, D):
+    """65535 requests: groups of none, one and many."""
+    c = Case(hyb, [(30, [1 + i % 20 for i in range(300)])], 1, 1, D, dt, seed=3)
+    B, n0 = 65535, 300
+    pick = torch.arange(B, device="cuda") % n0               # each request many times, in groups of its own
+    q, bt = torch.randn(B, 1, D, device="cuda").to(dt), c.bt[pick].contiguous()
+    bt[:, 0] = c.bt[0, 0]
+    lens = c.dev[0][pick].contiguous()
+    cu, at = [0], 0
+    while at < B:
+        at = min(B, at + [0, 1, 7, 60][len(cu) % 4])
+        cu.append(at)
+    G = len(cu) - 1
+    # the block in which the prefix ends is each request's own: it holds the same tokens there
+    out = torch.full((B, 1, D), 7.0, device="cuda", dtype=dt)
+    cu_d, pre = torch.tensor(cu, dtype=torch.int32, device="cuda"), torch.full((G,), 30, dtype=torch.int32, device="cuda")
+    p = hyb.prefix_dims(1, G, 60, 30, 20)
+    n = hyb.hyb_paged_attn_decode_shared_prefix_workspace_size(B, p, c.d)
+    ws = torch.empty(n // 4 + 4, device="cuda")
+    hyb.check(hyb.hyb_paged_attn_decode_shared_prefix(out, q, c.kc, c.vc, bt, lens, cu_d, pre, B, p, c.d, ws, n))
+    rows = sorted({0, 1, 2, 59, 60, 31999, 32768, B - 2, B - 1, *range(5, B, 331)})
+    # the plain form, each row a group of its own
+    ref = R.attention(q[rows], c.kc, c.vc, bt[rows], lens[rows].tolist(), list(range(len(rows) + 1)), [30] * len(rows), c.d.scale)
+    R.check_attention(out[rows], ref, dt)
+    assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt,D,rows", [(B16, 64, 2), (B16, 128, 66), (F32, 16, 2), (F32, 16, 9)])
+def test_the_longest_prefix(hyb, devstatus, dt, D, rows):
+    """2^24 tokens, one key head."""
+    P, bs = 1 << 24, 256
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    kc, vc = (torch.randn(P // bs + 1, 1, bs, D, generator=gen, device="cuda").to(dt) for _ in range(2))
+    q = torch.randn(rows, 1, D, generator=gen, device="cuda").to(dt)
+    NB = P // bs + 1
+    d = hyb.dims(1, D, NB, NB, dt, block_size=bs)
+    bt = torch.arange(NB - 1, -1, -1, dtype=torch.int32, device="cuda").expand(rows, NB).contiguous()
+    lens = [P + 1, P - 12345] + [P + 1 + i % 200 for i in range(rows - 2)]
+    dev = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lens, [0, rows], [P])]
+    p = hyb.prefix_dims(1, 1, rows, P, 256)
+    n = hyb.hyb_paged_attn_decode_shared_prefix_workspace_size(rows, p, d)
+    ws, out = torch.full((n // 4 + 4,), math.nan, device="cuda"), torch.empty_like(q)
+    hyb.check(hyb.hyb_paged_attn_decode_shared_prefix(out, q, kc, vc, bt, *dev, rows, p, d, ws, n))
+    # all rows share one table: softmax sums over chunks of the sequence, scores are small enough for no maximum
+    x, L = q[:, 0].double() * d.scale, torch.tensor(lens, device="cuda")
+    num, mag = (torch.zeros(rows, D, dtype=torch.float64, device="cuda") for _ in range(2))
+    den, amax = (torch.zeros(rows, 1, dtype=torch.float64, device="cuda") for _ in range(2))
+    step = 4096
+    for b0 in range(0, NB, step):
+        ids = bt[0, b0:b0 + step].long()
+        k, v = (c[ids, 0].double().flatten(0, 1) for c in (kc, vc))
+        at = b0 * bs + torch.arange(len(k), device="cuda")
+        w = torch.exp(x @ k.T) * (at < L[:, None])
+        num += w @ v
+        mag += w @ v.abs()
+        den += w.sum(-1, keepdim=True)
+        amax = torch.maximum(amax, (x.abs() @ k.abs().T).amax(-1, keepdim=True))
+    ref = (num / den)[:, None], (mag / den)[:, None], amax[:, None], L.double()[:, None, None]
+    lim = R.HALF[dt] * ref[0].abs() + ref[1] * (2 * D * R.U * ref[2] + 2.0 ** -22 + 4 * R.U * ref[3].sqrt() + (2.0 ** -8 + ref[3] / 16 * 2.0 ** -23 if dt == B16 else 0))
+    assert ((out.double() - ref[0]).abs() <= lim * (1 + 2.0 ** -6) + 1e-30).all()
+    assert devstatus() == (0, 0)
