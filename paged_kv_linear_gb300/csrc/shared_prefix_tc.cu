@@ -125,6 +125,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   __shared__ struct {
     const int32_t* btrow;
     int b0, row0, cnt, part, head0, two;             // head0: the first query head of hk
+    int vend;                                        // behind the last key that a row sees
   } info;
   if (tid == 0) {
     info.btrow = btrow;
@@ -143,6 +144,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
   if (warp == kWarpTmaK || warp == kWarpTmaV) {
     for (int b = q0 + lane; b < q1; b += 32) seen.add(a, a.lens[b], P);
     seen.join();
+    if (lane == 0) info.vend = min(k1, seen.hi);
   }
 
   if (warp == kWarpMma) {
@@ -225,7 +227,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
           if (!ok) break;
         }
         // V rows that hold no key of the part must be finite (P is 0 there, but 0 x NaN is NaN): pieces that
-        // are not loaded are zeroed here, rows before k0 and past k1 inside the first and last one by the landing warp
+        // are not loaded are zeroed here, rows before the first and past the last key inside their pieces by the landing warp
         if (!isk && nbox < 16) {
 #pragma unroll
           for (int bi = 0; bi < 8; ++bi)
@@ -255,6 +257,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
       // ------------------------------------------------------------ landing warp
       // Per key tile j: (1) the step before it is done -> stepf; (2) once V_j and K_{j+1} have
       // landed, one arrival on pfull[t] per row tile. Every phase of each barrier is observed in order.
+      const int vend = info.vend;
       bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->kfull[0], 0));
       for (int jj = 0; jj < nloc && ok; ++jj) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[two ? 1 : 0], jj & 1));
@@ -262,13 +265,13 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__
         if (lane == 0) mbar_arrive(&bars->stepf[jj % kNSF]);
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->vfull[jj % kNV], (jj / kNV) & 1));
         if (!ok) break;
-        const int vtail = k1 - (kb + jj * kBN);
-        if (vtail < kBN && (vtail & 15) != 0) {          // rows past k1 in the last piece
+        const int vtail = vend - (kb + jj * kBN);
+        if ((vtail & 15) != 0 && vtail < kBN && vtail > 0) {   // rows past the last key in its piece
           zero_v_rows(sm + kOffV + (jj % kNV) * kTile, vtail, (vtail + 15) & ~15, lane);
           fence_async_smem();
           __syncwarp();
         }
-        if (kWindow && jj == 0 && kb < k0) {             // and before k0 in the first
+        if (kWindow && jj == 0 && kb < k0) {             // and before the first key in its piece
           zero_v_rows(sm + kOffV, 0, k0 - kb, lane);
           fence_async_smem();
           __syncwarp();

@@ -362,3 +362,15 @@ def test_the_longest_prefix(hyb, devstatus, dt, D, rows):
     lim = R.HALF[dt] * ref[0].abs() + ref[1] * (2 * D * R.U * ref[2] + 2.0 ** -22 + 4 * R.U * ref[3].sqrt() + (2.0 ** -8 + ref[3] / 16 * 2.0 ** -23 if dt == B16 else 0))
     assert ((out.double() - ref[0]).abs() <= lim * (1 + 2.0 ** -6) + 1e-30).all()
     assert devstatus() == (0, 0)
+
+
+@pytest.mark.parametrize("dt,D,Hq,Hk,rows", KERNELS)
+def test_tokens_behind_all_requests(hyb, devstatus, dt, D, Hq, Hk, rows):
+    """Where every request is shorter than its prefix, what stands behind the longest in its last block reaches none."""
+    c = Case(hyb, [(1000, [-1000 + 37 + (i * 131) % 700 for i in range(rows)]), (60, [3])], Hq, Hk, D, dt, bs=32, seed=rows)
+    n = max(c.lens[:rows])
+    assert n % 16 and n < 1000
+    for x in (c.kc, c.vc):
+        x[c.bt[0, n // 32].long(), :, n % 32:] = math.nan
+    c.check()
+    assert devstatus() == (0, 0)
