@@ -20,8 +20,10 @@
 // candidates. Four CTAs an SM with the next batch's loads in flight, and a slice of 8 batches where there are rows enough
 // (while the whole took 48 us: five CTAs without loads ahead 54; slices of 4 batches 50, 2 61, 1 75, since each starts
 // its bound anew). Warps that put down their own best without a barrier a batch: 47 us, and rising rows 0.8 ms or more.
-// The same shape with 8 choices and every row constant takes 57 us, falling 44, rising, where each batch raises the
-// bound, 168. One request of 4 beams over 32768 tokens, fp32: 9.6 us, two kernels of some 4 us.
+// The same shape with 8 choices and every row constant takes 56 us, falling 43, rising, where each batch raises the
+// bound, 170. More choices collect more: 16 / 24 / 32 / 64 / 128 take 52 / 58 / 60 / 84 / 123 us (random), 66 / 70 / 64 / 78
+// / 84 (constant), 52 / 57 / 53 / 68 / 93 (falling), 180 / 187 / 206 / 241 / 277 (rising). One request of 4 beams over
+// 32768 tokens, fp32: 10 us, two kernels of some 4 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -121,8 +123,9 @@ __device__ __forceinline__ uint32_t read_low(const uint32_t* low, int N) {
 
 // Whole CTA: thins list[0, count) to at most kThreads entries that hold its N <= 128 best; returns how many.
 // A round finds a bound among the threads' own largest and drops what does not reach it. First the quick
-// bound (see the top), which mostly suffices; then the N-th largest of the 256, which N ceil(count / 256) <
-// count / 2 + 128 entries reach at most: from 4608 entries 2304, 1152, 640, 384, 256.
+// bound (see the top), which mostly suffices; then the N-th largest of the 256, which N ceil(count / 256) <=
+// 128 ceil(count / 256) entries reach at most: from 4608 entries (fp32) 2304, 1152, 640, 384, 256, from 8704 (bf16) 4352,
+// 2176, 1152 and so on.
 template <typename K>
 __device__ __forceinline__ int thin_out(K* list, int count, int N, K* scratch, uint32_t* low, int* left) {
   const int tid = threadIdx.x;

@@ -7,11 +7,11 @@
 //   bf16, D = 128, more than 64 rows of a key head: shared_prefix_tc.cu (96 rows on 8192 tokens, 4 groups of 8 key
 //   heads: 45 us against 73 on warp matrix instructions; at 64 rows both take 46)
 //   the others: prefix_tile_kernel and prefix_part_kernel below, in fp32
-// Then prefix_join_kernel adds the parts' states up. GPU time a call, in a stream of calls (graph replays, inputs
-// larger than L2): 4 beams on 4096 tokens, 32 heads 17.9 us (10.0 at the copy rate); 64 requests behind 2048 tokens,
-// 80 % short and 20 % long answers up to 2048 88 us (68); 16 prompts of up to 8192 tokens, 8 beams, 32 query and 8 key
-// heads 63 us (48); 256 requests on 32768 tokens, 32 and 8 heads 115 us (72 at the tensor rate); the same of
-// hyb_paged_attn_decode, which reads the prefix for each request (32 key heads): 4 beams on 4096 tokens 38 us.
+// Then prefix_join_kernel adds the parts' states up. Time of a call in a stream of calls (inputs larger than L2): 4 beams
+// on 4096 tokens, 32 heads 17.8 us (10.0 at the copy rate); 64 requests behind 2048 tokens, 80 % short and 20 % long
+// answers up to 2048 85 us (68); 16 prompts of up to 8192 tokens, 8 beams, 32 query and 8 key heads 61 us (48); 256
+// requests on 32768 tokens, 32 and 8 heads 122 us (72 at the tensor rate); the same of hyb_paged_attn_decode, which reads
+// the prefix for each request (32 key heads): 4 beams on 4096 tokens 38 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -430,8 +430,9 @@ PrefixPlan plan_prefix(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t*
   const bool mma = prefix_mma_supported(d->dtype, D);
   r.tc = mma && D == 128 && rep <= 128 && d->scale > 0.f && rows > 64;
   if (r.tc) {
-    // one CTA an SM; a key tile of 128 takes it some 1.6 us, setup and drain 8 us; a part's state
-    // is written and read once, at some 6 TB/s
+    // one CTA an SM; a key tile of 128 counts as 1.6 us, setup and drain as 8 us, a part's state, written and read once,
+    // at 6 TB/s. (The kernel now takes 1.43 and 7 us. With these, 2 % of 20000 random shapes would be cut otherwise, for
+    // a gain of 2.6 % at most by this very sum.)
     const int64_t tr = 2 * prefix_tc_tile_rows(rep), units = std::max<int64_t>(1, heads * ((rows + tr - 1) / tr));
     const int tiles = std::max(1, (P + 127) / 128);
     const double state_us = (double)B * p->num_q_heads * (D * 4 + 8) * 2 / 6e6;
@@ -447,7 +448,7 @@ PrefixPlan plan_prefix(int B, const hyb_prefix_dims_t* p, const hyb_attn_dims_t*
     }
   } else if (mma) {
     const int64_t nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, units = std::max<int64_t>(1, heads * ((rows + 16 * nt - 1) / (16 * nt)));
-    const int64_t slots = (int64_t)sms * (D == 256 ? 1 : 3);
+    const int64_t slots = (int64_t)sms * (D == 256 ? 1 : 3);   // (D = 256: rings of 128 KiB but for four row tiles)
     r.Lp = round16(std::min<int64_t>(kMmaMaxPart, std::max<int64_t>(nt == 1 ? 512 : 256, P * units / slots)));
   } else if (use_tiles(rows)) {
     // one wave of the CTAs that shared memory holds, if that leaves parts of 128 to 512 keys

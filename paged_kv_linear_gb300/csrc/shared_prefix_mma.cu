@@ -16,8 +16,8 @@
 // -> 63.9 us), of 16 for one, which waits for memory in any case.
 //
 // 16 prompts of 8, 32 query and 8 key heads, up to 8192 tokens: 60 us, 5.5 TB/s, 0.81 of the copy rate (issue slots
-// 20 % busy, tensor pipe 22 %): it waits for memory, and for the start of its CTAs (group, then lengths, queries and
-// block ids, then keys: three round trips, 4 us). 32 groups of 4 rows, 8 key heads
+// 20 % busy, tensor pipe 22 %): it waits for memory, and for the start of its CTAs (group, then lengths and the part's
+// block ids, then queries and keys: three round trips, 4 us). 32 groups of 4 rows, 8 key heads
 // of 8192 tokens (1.08 GB) run at 0.96.
 #include <cuda_bf16.h>
 
@@ -565,7 +565,7 @@ prefix_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   // early: launched behind the tensor-core kernel of the same call, which began when everything before it had
   // ended and writes nothing that this one reads or writes. So this one runs beside it, on the SMs that it leaves, and
   // its last CTA alone waits for it: the joining kernel waits for this one, which then ends after both. (With every
-  // CTA waiting, the first ones kept the others off those SMs: 256 requests on 32768 tokens 133 us against 115.)
+  // CTA waiting, the first ones kept the others off those SMs: 256 requests on 32768 tokens 135 us against 122.)
   if (!early) pdl_wait();
   pdl_trigger();
   const int rep = a.Hq / a.Hk;
